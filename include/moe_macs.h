@@ -21,6 +21,13 @@
  * moe_routing_fused launch, and moe_expert_ffn_combine makes the last two
  * one call.
  *
+ * Beside the path: moe_linear, the dense product with a fused epilogue (a
+ * shared expert, whose output the routed output joins as the residual), and
+ * what tuning the router and the dense parts takes, on one stream:
+ *   moe_combine_dropout -> (loss) -> moe_combine_backward
+ *   moe_balance_loss -> moe_router_backward (with the gates' gradient)
+ *   -> moe_linear_backward (the router's product, the shared expert)
+ *
  * Conventions shared by every entry point
  *   - Every array argument is a DEVICE pointer owned by the caller; the
  *     library never allocates, frees or keeps pointers after returning.
@@ -39,7 +46,8 @@
  *        MOE_EHIP    the HIP runtime reported a launch error,
  *        MOE_ESCRATCH  the no-allocation variant's fixed buffer is too
  *                    small for the call.
- *   - T == 0 is valid and enqueues nothing.
+ *   - T == 0 is valid and enqueues nothing (moe_linear_backward and
+ *     moe_balance_loss write zeros to the sums over tokens).
  *   - Limits: 1 <= N <= 1024 experts, 1 <= k <= N, 0 <= R <= N - k,
  *     T <= 2^20 tokens.
  *   - Device data are not validated: router logits must be finite, expert
@@ -50,7 +58,8 @@
  * Workspaces
  *   moe_router_topk, moe_capacity_assign, moe_dispatch, moe_routing_fused,
  *   moe_expert_ffn and moe_expert_ffn_combine take a workspace of at least
- *   the size their *_workspace_size() query returns.  The router, capacity,
+ *   the size their *_workspace_size() query returns, and so do moe_linear,
+ *   moe_linear_backward and moe_balance_loss (scratch only).  The router, capacity,
  *   dispatch, fused-routing and FFN-combine workspaces hold a few control
  *   words: they must be filled with zero bytes once, before their first use
  *   (e.g. allocated zeroed); every call leaves those words zero again.  A workspace must not be
@@ -73,6 +82,10 @@ enum { MOE_OK = 0, MOE_EINVAL = -1, MOE_EUNSUP = -2, MOE_EHIP = -3,
  * MOE_BF16_PANELS (expert FFN calls only) is bf16 with the expert weights in
  * the panel layout written by moe_pack_weights */
 enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_BF16_PANELS = 2 };
+
+/* activations of moe_linear */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3,
+       MOE_ACT_SWIGLU = 4 };
 
 /* flags[t,s] bits written by moe_sere_reroute / moe_capacity_assign */
 enum { MOE_FLAG_SERE = 1, MOE_FLAG_MACS = 2, MOE_FLAG_DROP = 4 };
@@ -477,6 +490,162 @@ int moe_expert_ffn_noalloc(const void* x, const int32_t* row_token,
 int moe_combine(const void* out_rows, const int32_t* slot_row,
                 const float* topk_gates, int T, int k, int H, int dtype,
                 void* y, void* stream);
+
+/*
+ * moe_linear -- a dense layer's matrix product with bias, activation and
+ * residual in its epilogue:
+ *   z = x w^T + bias;   y = act(z) + residual
+ * e.g. a shared expert beside the routed ones (MACS §3.3 names the shared
+ * group): its gate-up half is MOE_ACT_SWIGLU on weights in w13's layout, its
+ * down half a plain product with the routed output as the residual.
+ *
+ * x         [T,K]  activations (dtype).
+ * w         [O,K]  one row of K per output column; MOE_ACT_SWIGLU: [2O,K],
+ *                  gate rows 0..O-1 then up rows O..2O-1, and
+ *                  y = silu(z[:, :O]) * z[:, O:] + residual.
+ * bias      [O] ([2O]) (dtype); may be NULL.
+ * residual  [T,O]  (dtype); may be NULL; may equal y (in place).
+ * act       MOE_ACT_NONE; _RELU; _SILU a/(1+e^-a); _GELU a Phi(a) with the
+ *           normal distribution function Phi (the erf form); _SWIGLU.
+ * dtype     MOE_BF16 (bf16 products, fp32 accumulation and epilogue, y and z
+ *           rounded once) or MOE_F32.
+ * z         [T,O] ([T,2O]) out: the product before the activation, for
+ *           moe_linear_backward; may be NULL.
+ * y         [T,O]  out.
+ * Workspace of moe_linear_workspace_size() bytes (scratch only; no
+ * initialisation).  Limits: 1 <= K, O <= MOE_LINEAR_MAX_DIM, multiples of 8
+ * (MOE_BF16) or 4 (MOE_F32), else MOE_EUNSUP; every array and the workspace
+ * start at a multiple of 16 bytes, else MOE_EINVAL.  y and z must not overlap
+ * the inputs (residual apart).  The order of summation depends on the shape,
+ * the dtype and the device's compute-unit count only.
+ */
+#define MOE_LINEAR_MAX_DIM 65536
+size_t moe_linear_workspace_size(int T, int K, int O, int act, int dtype);
+int moe_linear(const void* x, const void* w, const void* bias,
+               const void* residual, int T, int K, int O, int act, int dtype,
+               void* z, void* y, void* workspace, size_t workspace_bytes,
+               void* stream);
+
+/*
+ * moe_linear_backward -- the gradients of moe_linear:
+ *   dz = dy * act'(z);   dx = dz w;   dw = dz^T x;   dbias = sum_t dz
+ * (the residual's gradient is dy).  relu'(0) = 0.
+ *
+ * dy        [T,O] (dtype); x, w as moe_linear (x may be NULL without dw, w
+ *           without dx).
+ * z         moe_linear's z; unused and may be NULL for MOE_ACT_NONE.
+ * dx        [T,K], dw as w, dbias [O] ([2O]): out (dtype), overwritten; each
+ *           may be NULL to skip it, not all three.
+ * dz is rounded to dtype for the two products (bf16 operands, fp32 sums);
+ * dbias sums the unrounded values in fp32.  T == 0 writes zeros to dw and
+ * dbias.  Workspace of moe_linear_backward_workspace_size() bytes (scratch
+ * only), limits and errors as moe_linear.
+ */
+size_t moe_linear_backward_workspace_size(int T, int K, int O, int act,
+                                          int dtype);
+int moe_linear_backward(const void* dy, const void* x, const void* w,
+                        const void* z, int T, int K, int O, int act, int dtype,
+                        void* dx, void* dw, void* dbias, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * moe_balance_loss -- the router's training losses and per-expert counts.
+ * With p_t = softmax(logits[t]), n the tokens that the mask keeps, c_j the
+ * slots of those tokens that name expert j and P_j = (1/n) sum_t p_tj:
+ *   losses[0] = N / (k n) * sum_j c_j P_j      (balance; 1 when uniform)
+ *   losses[1] = (1/n) sum_t logsumexp(logits[t])^2      (z loss)
+ *
+ * logits      f32[T,N]  router scores.  -inf rules an expert out for that
+ *                       token (probability 0); a token whose scores are all
+ *                       -inf has no probabilities: it and its slots count,
+ *                       it adds to no sum and gets no gradient.
+ * slot_ids    i32[T,k]  topk_ids, or the experts after re-routing; ids
+ *                       outside [0,N) (-1 = dropped) are not counted.
+ * token_mask  u8[T]     0 = padding, whose logits and ids are not used; NULL
+ *                       keeps every token.
+ * losses      f32[2]    out.
+ * counts      i32[N+1]  out: c_j, then n.
+ * mean_prob   f32[N]    out: P_j.
+ * lse         f32[T]    out: logsumexp (0 for padding), for
+ *                       moe_router_backward.
+ * n == 0 (T == 0 too) gives zeros.  Sums over tokens are taken in fp64 in a
+ * fixed order.  Workspace of moe_balance_workspace_size(T, N) bytes, at a
+ * multiple of 8 bytes (scratch only; no initialisation).
+ */
+size_t moe_balance_workspace_size(int T, int N);
+int moe_balance_loss(const float* logits, const int32_t* slot_ids,
+                     const uint8_t* token_mask, int T, int N, int k,
+                     float* losses, int32_t* counts, float* mean_prob,
+                     float* lse, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * moe_router_backward -- the gradient of the router's logits, through the
+ * losses of moe_balance_loss and through the gates of moe_route:
+ *   dlogits_tj = p_tj (u_tj - sum_i p_ti u_ti) + d_losses[1] 2 lse_t p_tj / n
+ *   u_tj       = d_losses[0] N c_j / (k n^2) + sum_{s: topk_ids[t,s] = j} d_gates[t,s]
+ * (the counts carry no gradient).
+ *
+ * logits, token_mask, k: as given to moe_balance_loss; lse and counts: its
+ *                       outputs.
+ * topk_ids    i32[T,k]  moe_route's output (the ranked experts whose softmax
+ *                       the gates are); an id may repeat, ids outside [0,N)
+ *                       take no gradient.  May be NULL without d_gates.
+ * d_losses    f32[2]    loss gradients, read on the device; NULL = 0.
+ * d_gates     f32[T,k]  gradient of topk_gates; NULL = 0.
+ * dlogits     [T,N]     out, element type dtype (MOE_F32 or MOE_BF16); rows
+ *                       of padding are zeros, and their d_gates are not used.
+ * T == 0 enqueues nothing.  One launch.
+ */
+int moe_router_backward(const float* logits, const int32_t* topk_ids,
+                        const uint8_t* token_mask, const float* lse,
+                        const int32_t* counts, const float* d_losses,
+                        const float* d_gates, int T, int N, int k, int dtype,
+                        void* dlogits, void* stream);
+
+/*
+ * moe_combine_dropout -- moe_combine with dropout and a residual:
+ *   y[t,c] = residual[t,c] + m[t,c] * sum over s with slot_row[t,s] >= 0 of
+ *            topk_gates[t,s] * out_rows[slot_row[t,s], c]
+ * accumulated in fp32 in slot order and rounded once.  m is 0 with
+ * probability p, else 1/(1-p), and is never stored: element e = t H + c is
+ * kept iff word e % 4 of Philox4x32-10 (Salmon et al. 2011) with key
+ * {seed low, seed high} and counter {low, high of e/4, low, high of offset}
+ * is at least floor(p 2^32).
+ *
+ * residual  [T,H] (dtype); may be NULL; may equal y (in place).
+ * p         0 <= p < 1.
+ * rng       u64[2] {seed, offset}, read on the device, so that a captured
+ *           graph draws a new mask on each replay when the caller advances
+ *           the offset between replays; may be NULL when p == 0.
+ * out_rows, slot_row, topk_gates, T, k, H, dtype, y: as moe_combine.
+ * H % 8 == 0, else MOE_EUNSUP; out_rows, residual and y start at a multiple
+ * of 16 bytes, rng of 8, else MOE_EINVAL.  One launch.
+ */
+int moe_combine_dropout(const void* out_rows, const int32_t* slot_row,
+                        const float* topk_gates, const void* residual, double p,
+                        const uint64_t* rng, int T, int k, int H, int dtype,
+                        void* y, void* stream);
+
+/*
+ * moe_combine_backward -- the gradients of moe_combine_dropout (and, with
+ * p == 0, of moe_combine), with the same p and rng:
+ *   d_out_rows[r,c] = topk_gates[t,s] * (m[t,c] dy[t,c]),   r = slot_row[t,s]
+ *   d_gates[t,s]    = sum_c out_rows[r,c] * (m[t,c] dy[t,c])
+ * (the residual's gradient is dy).  The m dy of a row stays in fp32.
+ *
+ * dy          [T,H] (dtype).
+ * d_out_rows  [T*k,H] out (dtype): the rows that a slot names; the others
+ *             are left as they were.  May be NULL.
+ * d_gates     f32[T,k] out: 0 for dropped slots.  May be NULL, not both.
+ * out_rows may be NULL without d_gates.  Errors and alignment as
+ * moe_combine_dropout.  One launch; T == 0 enqueues nothing.
+ */
+int moe_combine_backward(const void* dy, const void* out_rows,
+                         const int32_t* slot_row, const float* topk_gates,
+                         double p, const uint64_t* rng, int T, int k, int H,
+                         int dtype, void* d_out_rows, float* d_gates,
+                         void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,7 @@ FFN_NOALLOC_MAX_BYTES = 32 << 20
 MOE_F32, MOE_BF16, MOE_BF16_PANELS = 0, 1, 2
 FLAG_SERE, FLAG_MACS, FLAG_DROP = 1, 2, 4
 WEIGHT_ONE = 65536
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 
 _ERR = {MOE_EINVAL: "MOE_EINVAL (bad argument)",
         MOE_EUNSUP: "MOE_EUNSUP (unsupported type or shape)",
@@ -71,6 +72,16 @@ _SIGS = {
     "moe_ffn_down": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     "moe_combine": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_pack_weights": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_linear_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_linear": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_linear_backward_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_linear_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P,
+                                 _P, _SZ, _P]),
+    "moe_balance_workspace_size": (_SZ, [_I, _I]),
+    "moe_balance_loss": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_router_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_combine_dropout": (_I, [_P, _P, _P, _P, _D, _P, _I, _I, _I, _I, _P, _P]),
+    "moe_combine_backward": (_I, [_P, _P, _P, _P, _D, _P, _I, _I, _I, _I, _P, _P, _P]),
 }
 
 
@@ -143,6 +154,20 @@ def _ffn_format(dtype: torch.dtype, panels: bool) -> int:
 
 def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r}, expected one of {sorted(ACTS)}")
+    return ACTS[act]
+
+
+def _one_device(ref, *tensors):
+    """The launches go to the current device: every tensor must live there."""
+    here = torch.cuda.current_device()
+    for t in (ref,) + tensors:
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{here}")
 
 
 # ---------------------------------------------------------------- the ABI
@@ -511,6 +536,154 @@ def moe_combine(out_rows, slot_row, topk_gates, y=None):
         _dev(y, out_rows.dtype, "y", (T, H)), _stream())
     _check(rc, "moe_combine")
     return y
+
+
+# ------------------------------------------- dense layer and training calls
+def moe_linear_workspace_size(T, K, O, act, dtype) -> int:
+    return int(_lib.moe_linear_workspace_size(T, K, O, _act(act), _elem(dtype)))
+
+
+def moe_linear_backward_workspace_size(T, K, O, act, dtype) -> int:
+    return int(_lib.moe_linear_backward_workspace_size(T, K, O, _act(act), _elem(dtype)))
+
+
+def _linear_shapes(x, w, act):
+    T, K = x.shape
+    rows = w.shape[0]
+    if act == "swiglu" and rows % 2:
+        raise ValueError("swiglu weights need an even number of rows (gate, then up)")
+    return T, K, rows // 2 if act == "swiglu" else rows, rows
+
+
+def moe_linear(x, w, workspace, bias=None, residual=None, act="none", z=None, y=None):
+    """act(x w^T + bias) + residual; z, if given, receives the product before
+    the activation for moe_linear_backward.  w is [O,K], or [2O,K] (gate rows,
+    then up rows) for act "swiglu"."""
+    code, dt = _act(act), _elem(x.dtype)
+    T, K, O, W = _linear_shapes(x, w, act)
+    if y is None:
+        y = _empty((T, O), x.dtype, x)
+    args = (_dev(x, x.dtype, "x"), _dev(w, x.dtype, "w", (W, K)),
+            _opt(bias, x.dtype, "bias", (W,)), _opt(residual, x.dtype, "residual", (T, O)),
+            T, K, O, code, dt, _opt(z, x.dtype, "z", (T, W)), _dev(y, x.dtype, "y", (T, O)),
+            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    _one_device(x, w, bias, residual, z, y, workspace)
+    _check(_lib.moe_linear(*args, _stream()), "moe_linear")
+    return y
+
+
+def moe_linear_backward(dy, x, w, workspace, z=None, act="none", dx=None, dw=None,
+                        dbias=None):
+    """Fills those of dx [T,K], dw (as w) and dbias [rows of w] that are given
+    with the gradients of moe_linear; z is moe_linear's (not needed for act
+    "none")."""
+    code, dt = _act(act), _elem(x.dtype)
+    T, K, O, W = _linear_shapes(x, w, act)
+    if z is None and code != 0 and T > 0:
+        raise ValueError(f"act {act!r} needs moe_linear's z")
+    if dx is None and dw is None and dbias is None:
+        raise ValueError("no gradient asked for")
+    args = (_dev(dy, x.dtype, "dy", (T, O)), _dev(x, x.dtype, "x"),
+            _dev(w, x.dtype, "w", (W, K)), _opt(z, x.dtype, "z", (T, W)),
+            T, K, O, code, dt, _opt(dx, x.dtype, "dx", (T, K)),
+            _opt(dw, x.dtype, "dw", (W, K)), _opt(dbias, x.dtype, "dbias", (W,)),
+            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    _one_device(x, dy, w, z, dx, dw, dbias, workspace)
+    _check(_lib.moe_linear_backward(*args, _stream()), "moe_linear_backward")
+    return dx, dw, dbias
+
+
+def moe_balance_workspace_size(T, N) -> int:
+    return int(_lib.moe_balance_workspace_size(T, N))
+
+
+def moe_balance_loss(logits, slot_ids, workspace, token_mask=None, out=None):
+    """Balance and z loss, counts, mean probabilities and logsumexps of the
+    router's scores: a dict of losses [2], counts [N+1] (the last one the
+    tokens counted), mean_prob [N] and lse [T]."""
+    T, N = logits.shape
+    k = slot_ids.shape[1]
+    if out is None:
+        out = dict(losses=_empty((2,), torch.float32, logits),
+                   counts=_empty((N + 1,), torch.int32, logits),
+                   mean_prob=_empty((N,), torch.float32, logits),
+                   lse=_empty((T,), torch.float32, logits))
+    args = (_dev(logits, torch.float32, "logits"),
+            _dev(slot_ids, torch.int32, "slot_ids", (T, k)),
+            _opt(token_mask, torch.uint8, "token_mask", (T,)), T, N, k,
+            _dev(out["losses"], torch.float32, "losses", (2,)),
+            _dev(out["counts"], torch.int32, "counts", (N + 1,)),
+            _dev(out["mean_prob"], torch.float32, "mean_prob", (N,)),
+            _dev(out["lse"], torch.float32, "lse", (T,)),
+            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    _one_device(logits, slot_ids, token_mask, workspace, *out.values())
+    _check(_lib.moe_balance_loss(*args, _stream()), "moe_balance_loss")
+    return out
+
+
+def moe_router_backward(logits, topk_ids, lse, counts, d_losses=None, token_mask=None,
+                        d_gates=None, dlogits=None, dtype=torch.float32):
+    """Gradient of the router's logits through moe_balance_loss (d_losses [2])
+    and through the gates (d_gates [T,k]); dtype is that of a new dlogits."""
+    T, N = logits.shape
+    k = topk_ids.shape[1]
+    if dlogits is None:
+        dlogits = _empty((T, N), dtype, logits)
+    args = (_dev(logits, torch.float32, "logits"),
+            _dev(topk_ids, torch.int32, "topk_ids", (T, k)),
+            _opt(token_mask, torch.uint8, "token_mask", (T,)),
+            _dev(lse, torch.float32, "lse", (T,)),
+            _dev(counts, torch.int32, "counts", (N + 1,)),
+            _opt(d_losses, torch.float32, "d_losses", (2,)),
+            _opt(d_gates, torch.float32, "d_gates", (T, k)), T, N, k,
+            _elem(dlogits.dtype), _dev(dlogits, dlogits.dtype, "dlogits", (T, N)))
+    _one_device(logits, topk_ids, token_mask, lse, counts, d_losses, d_gates, dlogits)
+    _check(_lib.moe_router_backward(*args, _stream()), "moe_router_backward")
+    return dlogits
+
+
+def _rng(rng, p):
+    """Address of the {seed, offset} pair, an int64 tensor on the GPU."""
+    if rng is None and p > 0:
+        raise ValueError("dropout needs rng, an int64 tensor {seed, offset}")
+    return _opt(rng, torch.int64, "rng", (2,))
+
+
+def moe_combine_dropout(out_rows, slot_row, topk_gates, p=0.0, rng=None, residual=None,
+                        y=None):
+    """moe_combine with dropout (probability p, mask from rng = int64 [2]
+    {seed, offset}) and a residual."""
+    T, k = slot_row.shape
+    H = out_rows.shape[1]
+    if y is None:
+        y = _empty((T, H), out_rows.dtype, out_rows)
+    args = (_dev(out_rows, out_rows.dtype, "out_rows", (T * k, H)),
+            _dev(slot_row, torch.int32, "slot_row"),
+            _dev(topk_gates, torch.float32, "topk_gates", (T, k)),
+            _opt(residual, out_rows.dtype, "residual", (T, H)), float(p), _rng(rng, p),
+            T, k, H, _elem(out_rows.dtype), _dev(y, out_rows.dtype, "y", (T, H)))
+    _one_device(out_rows, slot_row, topk_gates, residual, rng, y)
+    _check(_lib.moe_combine_dropout(*args, _stream()), "moe_combine_dropout")
+    return y
+
+
+def moe_combine_backward(dy, out_rows, slot_row, topk_gates, p=0.0, rng=None,
+                         d_out_rows=None, d_gates=None):
+    """Fills those of d_out_rows [T*k,H] (rows that a slot names) and d_gates
+    [T,k] that are given with the gradients of moe_combine_dropout."""
+    T, k = slot_row.shape
+    H = out_rows.shape[1]
+    if d_out_rows is None and d_gates is None:
+        raise ValueError("no gradient asked for")
+    dt = out_rows.dtype
+    args = (_dev(dy, dt, "dy", (T, H)), _dev(out_rows, dt, "out_rows", (T * k, H)),
+            _dev(slot_row, torch.int32, "slot_row"),
+            _dev(topk_gates, torch.float32, "topk_gates", (T, k)), float(p), _rng(rng, p),
+            T, k, H, _elem(dt), _opt(d_out_rows, dt, "d_out_rows", (T * k, H)),
+            _opt(d_gates, torch.float32, "d_gates", (T, k)))
+    _one_device(out_rows, dy, slot_row, topk_gates, rng, d_out_rows, d_gates)
+    _check(_lib.moe_combine_backward(*args, _stream()), "moe_combine_backward")
+    return d_out_rows, d_gates
 
 
 # ------------------------------------------------------------- one layer

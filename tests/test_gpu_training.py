@@ -1,0 +1,587 @@
+"""The dense layer, the router's losses and the training combine on the GPU,
+through the binding, against the 64-bit definitions of training_ref."""
+import numpy as np
+import pytest
+import torch
+
+import training_ref as R
+from gpu_util import load_binding, needs_gpu
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def B():
+    return load_binding()
+
+
+def _rand(g, shape, scale=1.0, dtype=F32):
+    return (torch.from_numpy(g.normal(size=shape)) * scale).to(dtype).cuda()
+
+
+def _near(got, want, bound, what):
+    got = R.f64(got)
+    assert got.shape == want.shape
+    bad = ~(np.abs(got - want) <= bound + 1e-30)
+    if bad.any():
+        i = np.unravel_index(np.argmax(np.where(bad, np.abs(got - want) / (bound + 1e-30), 0)), got.shape)
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} over the bound, e.g. at {i}: "
+                             f"{got[i]} for {want[i]}, bound {bound[i]:.3e}")
+
+
+def _guard(shape, dtype, pad=64):
+    """A contiguous tensor inside a buffer whose other elements stay as they were."""
+    n = int(np.prod(shape))
+    buf = torch.full((n + 2 * pad,), 7.0, dtype=dtype, device="cuda")
+    return buf, buf[pad:pad + n].view(shape), pad
+
+
+def _untouched(buf, pad):
+    return bool((buf[:pad] == 7).all() and (buf[-pad:] == 7).all())
+
+
+# --------------------------------------------------------------------- linear
+# T, K, O: single tokens, a few rows, sizes around every tile edge, reduction
+# lengths that end inside a slice, more columns than a tile
+LINEAR = [
+    (1, 8, 8), (1, 2048, 1536), (1, 2056, 24), (2, 136, 264), (3, 64, 8), (5, 1032, 72),
+    (15, 520, 40), (16, 256, 128), (17, 264, 136), (31, 72, 1000), (33, 2048, 16), (64, 776, 200),
+    (65, 4104, 48), (100, 768, 2048), (127, 200, 136), (128, 64, 256), (129, 328, 264),
+    (200, 1032, 520), (255, 128, 128), (257, 264, 248), (300, 520, 776), (512, 4096, 64),
+    (700, 72, 1544), (1030, 264, 1544), (2100, 136, 264),
+]
+ACTS = ["none", "relu", "silu", "gelu", "swiglu"]
+
+
+def _linear_inputs(T, K, O, act, dtype, seed, bias, residual):
+    g = np.random.default_rng(seed)
+    W = 2 * O if act == "swiglu" else O
+    x = _rand(g, (T, K), 1.0, dtype)
+    w = _rand(g, (W, K), K ** -0.5, dtype)
+    b = _rand(g, (W,), 0.5, dtype) if bias else None
+    r = _rand(g, (T, O), 1.0, dtype) if residual else None
+    return g, x, w, b, r
+
+
+@pytest.mark.parametrize("i", range(len(LINEAR)))
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_linear(B, i, dtype):
+    T, K, O = LINEAR[i]
+    for j in range(2):  # two of the activations with each size, all of them over the sizes
+        act = ACTS[(i + 3 * j) % 5]
+        bias, residual, keep = (i + j) % 2 == 0, (i + j) % 3 != 0, (i + j) % 4 < 2
+        print(f"[gpu-test] linear {T} {K} {O} {act} {dtype}", flush=True)
+        g, x, w, b, r = _linear_inputs(T, K, O, act, dtype, 10 * i + j, bias, residual)
+        ws = B.new_workspace(B.moe_linear_workspace_size(T, K, O, act, dtype), "cuda")
+        ybuf, y, pad = _guard((T, O), dtype)
+        zbuf, z, _ = _guard((T, w.shape[0]), dtype)
+        B.moe_linear(x, w, ws, bias=b, residual=r, act=act, z=z if keep else None, y=y)
+        yr, zr, ey, ez = R.linear(R.f64(x), R.f64(w), R.f64(b), R.f64(r), act, dtype)
+        _near(y, yr, ey, "y")
+        if keep:
+            _near(z, zr, ez, "z")
+        assert _untouched(ybuf, pad) and _untouched(zbuf, pad)
+        first = y.clone()
+        ws.fill_(0xFF)  # the workspace needs no initialisation
+        B.moe_linear(x, w, ws, bias=b, residual=r, act=act, z=z if keep else None, y=y)
+        assert torch.equal(first, y)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_linear_residual_in_place_and_no_tokens(B, dtype, T):
+    g, x, w, b, r = _linear_inputs(T, 136, 264, "gelu", dtype, 5, True, True)
+    ws = B.new_workspace(B.moe_linear_workspace_size(T, 136, 264, "gelu", dtype), "cuda")
+    want = B.moe_linear(x, w, ws, bias=b, residual=r, act="gelu")
+    B.moe_linear(x, w, ws, bias=b, residual=r, act="gelu", y=r)
+    assert torch.equal(want, r)
+    assert B.moe_linear(x[:0], w, ws, bias=b, act="gelu").shape == (0, 264)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,K,O", [(40, 72, 136), (300, 200, 264), (7, 2056, 40)])
+def test_linear_keeps_rows_and_columns_apart(B, dtype, T, K, O):
+    """A token of NaN and a weight row of infinities reach only their own
+    output row and column; a reduction length inside a slice reads no
+    neighbour (the operands are followed by NaN)."""
+    g, x, w, b, _ = _linear_inputs(T, K, O, "none", dtype, 6, False, False)
+    ws = B.new_workspace(B.moe_linear_workspace_size(T, K, O, "none", dtype), "cuda")
+    clean = B.moe_linear(x, w, ws)
+    hold = torch.full((2 * (T + O) * K + 512,), float("nan"), dtype=dtype, device="cuda")
+    xs, wsx = hold[:T * K].view(T, K), hold[T * K + 256:T * K + 256 + O * K].view(O, K)
+    xs.copy_(x)
+    wsx.copy_(w)
+    assert torch.equal(B.moe_linear(xs, wsx, ws), clean)
+    xs[T // 2] = float("nan")
+    wsx[O // 3] = float("inf")
+    y = B.moe_linear(xs, wsx, ws)
+    rows = torch.arange(T, device="cuda") != T // 2
+    cols = torch.arange(O, device="cuda") != O // 3
+    assert torch.equal(y[rows][:, cols], clean[rows][:, cols])
+    assert y[T // 2].isnan().all() and not y[rows][:, O // 3].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_activations_at_extreme_values(B, dtype):
+    """Large and infinite arguments: the activations' limits, no NaN."""
+    v = [0.0, -0.0, 1e-30, -1e-30, 20.0, -20.0, 100.0, -100.0, 1e4, -1e4, 1e30, -1e30,
+         float("inf"), -float("inf")]
+    x = torch.zeros(len(v), 8, dtype=dtype, device="cuda")
+    x[:, 0] = torch.tensor(v, dtype=dtype)
+    w = torch.zeros(16, 8, dtype=dtype, device="cuda")
+    w[:, 0] = 1
+    ws = B.new_workspace(1 << 16, "cuda")
+    z = R.f64(x[:, 0])
+    for act, low in (("relu", 0.0), ("silu", None), ("gelu", None)):
+        y = R.f64(B.moe_linear(x, w, ws, act=act))
+        fin = np.isfinite(z)
+        want = R.act_value(z, act)
+        assert np.all(np.abs(y[fin] - want[fin][:, None]) <=
+                      (2 * R.half(dtype) * np.abs(want) + R.ACT * R.U * (np.abs(z) + 1))[fin][:, None] + 1e-30)
+        assert np.all(y[12] == np.inf)
+
+
+BACK = [(1, 64, 72), (2, 2056, 24), (7, 136, 264), (33, 200, 128), (64, 64, 64), (130, 264, 520),
+        (251, 136, 264), (256, 512, 256), (300, 1032, 72), (777, 328, 264), (1030, 136, 776),
+        (2100, 264, 136), (4100, 64, 40)]
+
+
+@pytest.mark.parametrize("i", range(len(BACK)))
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_linear_backward(B, i, dtype):
+    T, K, O = BACK[i]
+    for j in range(2):
+        act = ACTS[(i + 2 * j) % 5]
+        print(f"[gpu-test] linear backward {T} {K} {O} {act} {dtype}", flush=True)
+        g, x, w, b, _ = _linear_inputs(T, K, O, act, dtype, 100 + 10 * i + j, True, False)
+        W = w.shape[0]
+        dy, z = _rand(g, (T, O), 0.5, dtype), _rand(g, (T, W), 1.0, dtype)
+        ws = B.new_workspace(B.moe_linear_backward_workspace_size(T, K, O, act, dtype), "cuda")
+        bufs = {"dx": _guard((T, K), dtype), "dw": _guard((W, K), dtype), "db": _guard((W,), dtype)}
+        outs = {n: v[1] for n, v in bufs.items()}
+        B.moe_linear_backward(dy, x, w, ws, z=z, act=act, dx=outs["dx"], dw=outs["dw"], dbias=outs["db"])
+        want = R.linear_backward(R.f64(dy), R.f64(x), R.f64(w), R.f64(z), act, dtype)
+        for n, (v, e) in want.items():
+            _near(outs[n], v, e, n)
+            assert _untouched(bufs[n][0], bufs[n][2]), n
+        ws.fill_(0xFF)
+        for n in outs:  # each alone gives the same bits
+            alone = {m: torch.empty_like(outs[m]) if m == n else None for m in outs}
+            B.moe_linear_backward(dy, x, w, ws, z=z, act=act, dx=alone["dx"], dw=alone["dw"],
+                                  dbias=alone["db"])
+            assert torch.equal(alone[n], outs[n]), n
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_linear_backward_without_tokens_writes_zeros(B, dtype):
+    x, w = torch.empty(0, 64, dtype=dtype, device="cuda"), torch.ones(48, 64, dtype=dtype, device="cuda")
+    dw, db = torch.ones_like(w), torch.ones(48, dtype=dtype, device="cuda")
+    ws = B.new_workspace(0, "cuda")
+    B.moe_linear_backward(x.new_empty(0, 48), x, w, ws, act="none", dw=dw, dbias=db)
+    assert (dw == 0).all() and (db == 0).all()
+
+
+def test_linear_gradient_against_the_kernels_own_differences(B):
+    """The fp32 forward kernel's difference quotient along a direction equals
+    the 64-bit one up to the forward's rounding over 2h."""
+    T, K, O, h = 9, 64, 32, 2.0 ** -6
+    for act in ACTS:
+        g, x, w, b, _ = _linear_inputs(T, K, O, act, F32, 8, True, False)
+        ws = B.new_workspace(1 << 20, "cuda")
+        z = torch.empty(T, w.shape[0], device="cuda")
+        B.moe_linear(x, w, ws, bias=b, act=act, z=z)
+        c = _rand(g, (T, O))
+        dx = torch.empty_like(x)
+        wsb = B.new_workspace(B.moe_linear_backward_workspace_size(T, K, O, act, F32), "cuda")
+        B.moe_linear_backward(c, x, w, wsb, z=z, act=act, dx=dx)
+        v = _rand(g, (T, K), 0.1)
+        kern, ref, slack = 0.0, 0.0, 0.0
+        for sign in (1, -1):
+            xs = (x.double() + sign * h * v.double()).float()
+            y = B.moe_linear(xs, w, ws, bias=b, act=act)
+            yr, _, ey, _ = R.linear(R.f64(xs), R.f64(w), R.f64(b), None, act, F32)
+            kern += sign * (R.f64(c) * R.f64(y)).sum() / (2 * h)
+            ref += sign * (R.f64(c) * yr).sum() / (2 * h)
+            slack += (np.abs(R.f64(c)) * ey).sum() / (2 * h)
+        assert abs(kern - ref) <= slack
+        # the quotient against the gradient: smooth activations to second order
+        # (h |v| ~ 2e-3 relative to unit-scale arguments), relu where no argument changes sign
+        if act != "relu":
+            dot = (R.f64(dx) * R.f64(v)).sum()
+            assert abs(ref - dot) <= 1e-3 * (np.abs(R.f64(dx) * R.f64(v)).sum()) + slack
+
+
+# -------------------------------------------------------------------- balance
+def _balance_inputs(T, N, k, seed, drop=True):
+    g = np.random.default_rng(seed)
+    logits = (g.normal(size=(T, N)) * 2).astype(np.float32)
+    ids = np.stack([g.permutation(N)[:k] for _ in range(T)]).astype(np.int32) if T else np.zeros((0, k), np.int32)
+    if drop and T:
+        ids[g.random((T, k)) < 0.1] = -1
+    return g, logits, ids
+
+
+def _check_balance(B, logits, ids, mask, dl, dg, dtype=F32):
+    T, N = logits.shape
+    k = ids.shape[1]
+    dev = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    L, S, M, DL, DG = dev(logits), dev(ids), dev(mask), dev(dl), dev(dg)
+    ws = torch.full((max(1, B.moe_balance_workspace_size(T, N)),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = B.moe_balance_loss(L, S, ws, token_mask=M)
+    buf, dz, pad = _guard((T, N), dtype)
+    B.moe_router_backward(L, S, out["lse"], out["counts"], d_losses=DL, token_mask=M, d_gates=DG,
+                          dlogits=dz)
+    r = R.balance(logits.astype(np.float64), ids, mask, None if dl is None else dl.astype(np.float64),
+                  None if dg is None else dg.astype(np.float64))
+    assert np.array_equal(out["counts"].cpu().numpy(), r["counts"])
+    # fp32 logits up to |z|: exp and log in fp32 (a few units, and |z| 2^-24 from the argument), N-term sums
+    zmax = np.abs(logits[np.isfinite(logits)]).max() if np.isfinite(logits).any() else 0.0
+    e = (R.ACT + N / 16 + 2 * zmax) * R.U
+    fin = np.isfinite(r["lse"])
+    got = R.f64(out["lse"])
+    assert np.array_equal(got[~fin], r["lse"][~fin])
+    _near(torch.from_numpy(got[fin]), r["lse"][fin], e + R.U * np.abs(r["lse"][fin]), "lse")
+    _near(out["mean_prob"], r["mean_prob"], 2 * e * r["mean_prob"], "mean_prob")
+    zl = np.sqrt(r["losses"][1])
+    _near(out["losses"], r["losses"], np.array([2 * e * r["losses"][0], 4 * (e + R.U * zmax) * (zl + 1) * (zl + 1)]),
+          "losses")
+    # p is off by a relative 2 e (through lse, with |lse| 2^-24 from its own rounding); then N-term sums
+    h = R.half(dtype)
+    _near(dz, r["dlogits"], 6 * (e + R.U * zmax) * r["scale"] + h * np.abs(r["dlogits"]) * 1.01, "dlogits")
+    assert _untouched(buf, pad)
+    out2 = B.moe_balance_loss(L, S, ws, token_mask=M)
+    for n in out:
+        assert torch.equal(out[n], out2[n]), n
+    return out, dz
+
+
+@pytest.mark.parametrize("T,N,k", [(1, 1, 1), (1, 8, 2), (2, 5, 5), (3, 64, 8), (7, 65, 3), (16, 128, 8),
+                                   (33, 130, 8), (63, 256, 8), (129, 257, 4), (300, 1000, 8), (40, 1024, 70),
+                                   (1500, 31, 2), (5000, 16, 4), (9001, 128, 8)])
+def test_balance(B, T, N, k):
+    g, logits, ids = _balance_inputs(T, N, k, T + N)
+    mask = (g.random(T) > 0.2).astype(np.uint8)
+    dl, dg = np.array([0.5, 0.25], np.float32), g.normal(size=(T, k)).astype(np.float32)
+    _check_balance(B, logits, ids, mask, dl, dg)
+    _check_balance(B, logits, ids, None, dl, None)
+    _check_balance(B, logits, ids, None, None, dg, BF16)
+
+
+def test_balance_masked_places(B):
+    """Padding full of NaN and infinities, experts ruled out by -inf, a token
+    with nothing left, and a batch of padding alone."""
+    g, logits, ids = _balance_inputs(50, 40, 4, 9)
+    mask = np.ones(50, np.uint8)
+    mask[[0, 7, 49]] = 0
+    logits[0] = np.nan
+    logits[7] = np.inf
+    logits[49, ::2] = -np.inf
+    logits[3, 5:] = -np.inf
+    logits[4] = -np.inf
+    logits[5, :] = -np.inf
+    logits[5, 39] = np.finfo(np.float32).min
+    logits[6] = np.finfo(np.float32).min
+    ids[0] = 1 << 30
+    dl, dg = np.array([0.5, 0.25], np.float32), g.normal(size=(50, 4)).astype(np.float32)
+    dg[0] = np.nan
+    finite = logits.copy()
+    # a logsumexp of 3.4e38 squares past fp32: the z loss is left out of this check
+    dl[1] = 0
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    L, S, M, DL, DG = (dev(a) for a in (logits, ids, mask, dl, dg))
+    ws = B.new_workspace(B.moe_balance_workspace_size(50, 40), "cuda")
+    out = B.moe_balance_loss(L, S, ws, token_mask=M)
+    dz = R.f64(B.moe_router_backward(L, S, out["lse"], out["counts"], DL, M, DG))
+    finite[[0, 7, 49]] = 0
+    r = R.balance(finite.astype(np.float64), ids, mask, dl.astype(np.float64),
+                  np.nan_to_num(dg.astype(np.float64)))
+    assert np.array_equal(out["counts"].cpu().numpy(), r["counts"])
+    assert np.allclose(R.f64(out["mean_prob"]), r["mean_prob"], rtol=100 * R.U, atol=0)
+    assert abs(float(out["losses"][0]) - r["losses"][0]) <= 100 * R.U * r["losses"][0]
+    assert (dz[[0, 4, 7, 49]] == 0).all() and np.isfinite(dz).all()
+    assert (dz[3, 5:] == 0).all()
+    rows = [t for t in range(50) if t not in (5, 6)]
+    assert np.all(np.abs(dz - r["dlogits"])[rows] <= 100 * R.U * r["scale"][rows] + 1e-30)
+    M.zero_()
+    out = B.moe_balance_loss(L, S, ws, token_mask=M)
+    assert all((out[n] == 0).all() for n in out)
+    assert (B.moe_router_backward(L, S, out["lse"], out["counts"], DL, M, DG) == 0).all()
+
+
+def test_balance_without_tokens(B):
+    ws = torch.full((B.moe_balance_workspace_size(0, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = B.moe_balance_loss(torch.empty(0, 16, device="cuda"),
+                             torch.empty(0, 2, dtype=torch.int32, device="cuda"), ws)
+    assert all((out[n] == 0).all() for n in out)
+    assert out["counts"].shape == (17,)
+
+
+def test_router_backward_same_expert_twice(B):
+    """Gate gradients of one expert named by several slots add up."""
+    logits = np.random.default_rng(1).normal(size=(6, 70)).astype(np.float32)
+    ids = np.full((6, 3), 66, np.int32)
+    ids[:, 2] = 1
+    dg = np.arange(18, dtype=np.float32).reshape(6, 3) / 8
+    _check_balance(B, logits, ids, None, np.zeros(2, np.float32), dg)
+
+
+# -------------------------------------------------------------------- combine
+def _combine_inputs(T, H, k, dtype, seed):
+    g = np.random.default_rng(seed)
+    kept = g.random((T, k)) > 0.15
+    if T > 2:
+        kept[T // 2] = False
+    slot_row = np.full((T, k), -1, np.int32)
+    slot_row[kept] = g.permutation(int(kept.sum()))
+    rows = _rand(g, (T * k, H), 1.0, dtype)
+    gates = g.random((T, k)).astype(np.float32)
+    return g, rows, slot_row, gates
+
+
+@pytest.mark.parametrize("T,H,k,p,res", [
+    (1, 8, 1, 0.0, False), (1, 2048, 8, 0.1, True), (2, 16, 3, 0.5, True), (3, 264, 8, 0.25, False),
+    (5, 1032, 2, 0.1, True), (9, 520, 9, 0.9, True), (17, 64, 20, 0.0, True), (33, 128, 2, 0.1, False),
+    (4, 4104, 4, 0.3, True), (70, 40, 5, 0.999999, True)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_combine(B, T, H, k, p, res, dtype):
+    g, rows, slot_row, gates = _combine_inputs(T, H, k, dtype, T + H)
+    seed, offset = 0x1234_5678_9ABC_DEF0 + T, (1 << 40) + 3
+    rng = torch.tensor([seed, offset], dtype=torch.int64, device="cuda") if p else None
+    r = _rand(g, (T, H), 1.0, dtype) if res else None
+    S, G = torch.from_numpy(slot_row).cuda(), torch.from_numpy(gates).cuda()
+    buf, y, pad = _guard((T, H), dtype)
+    B.moe_combine_dropout(rows, S, G, p=p, rng=rng, residual=r, y=y)
+    m = R.keep(seed, offset, T, H, p) / (1 - p) if p else np.ones((T, H))
+    gd = gates.astype(np.float64)
+    want, bound = R.combine(R.f64(rows), slot_row, gd, R.f64(r), m, dtype)
+    _near(y, want, bound, "y")
+    assert _untouched(buf, pad)
+    if r is not None:  # in place
+        B.moe_combine_dropout(rows, S, G, p=p, rng=rng, residual=r, y=r)
+        assert torch.equal(r, y)
+    dy = _rand(g, (T, H), 1.0, dtype)
+    d_rows = torch.full((T * k, H), 7.0, dtype=dtype, device="cuda")
+    dg = torch.empty(T, k, device="cuda")
+    B.moe_combine_backward(dy, rows, S, G, p=p, rng=rng, d_out_rows=d_rows, d_gates=dg)
+    wr, er, wg, eg = R.combine_backward(R.f64(dy), R.f64(rows), slot_row, gd, m, dtype)
+    named = ~np.isnan(wr[:, 0])
+    _near(d_rows[torch.from_numpy(named).cuda()], wr[named], er[named], "d_rows")
+    assert (d_rows[torch.from_numpy(~named).cuda()] == 7).all()
+    _near(dg, wg, eg, "d_gates")
+    dg2, dr2 = torch.empty_like(dg), torch.full_like(d_rows, 7.0)
+    B.moe_combine_backward(dy, rows, S, G, p=p, rng=rng, d_gates=dg2)
+    B.moe_combine_backward(dy, rows, S, G, p=p, rng=rng, d_out_rows=dr2)
+    assert torch.equal(dg, dg2) and torch.equal(d_rows, dr2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_combine_dropped_places_hide_nan(B, dtype):
+    """A dropped element is 0 (plus the residual) whatever the rows or dy hold."""
+    T, H, k, p = 12, 64, 2, 0.5
+    g, rows, slot_row, gates = _combine_inputs(T, H, k, dtype, 2)
+    rng = torch.tensor([5, 6], dtype=torch.int64, device="cuda")
+    S, G = torch.from_numpy(slot_row).cuda(), torch.from_numpy(gates).cuda()
+    rows.fill_(float("nan"))
+    y = B.moe_combine_dropout(rows, S, G, p=p, rng=rng)
+    m = torch.from_numpy(R.keep(5, 6, T, H, p)).cuda()
+    live = torch.from_numpy((slot_row >= 0).any(1)).cuda()
+    assert (y[~m] == 0).all() and y[m & live[:, None]].isnan().all()
+    dy = torch.where(m, 1.0, float("nan")).to(dtype)
+    dr = torch.zeros(T * k, H, dtype=dtype, device="cuda")
+    B.moe_combine_backward(dy, torch.ones_like(rows), S, G, p=p, rng=rng, d_out_rows=dr,
+                           d_gates=(dg := torch.empty(T, k, device="cuda")))
+    assert not dr.isnan().any() and not dg.isnan().any()
+
+
+def test_combine_without_dropout_is_moe_combine(B):
+    for dtype in (BF16, F32):
+        g, rows, slot_row, gates = _combine_inputs(50, 256, 8, dtype, 3)
+        S, G = torch.from_numpy(slot_row).cuda(), torch.from_numpy(gates).cuda()
+        assert torch.equal(B.moe_combine_dropout(rows, S, G), B.moe_combine(rows, S, G))
+
+
+# ------------------------------------------------- together, streams, graphs
+class _Step:
+    """One tuning step of a router and a shared expert beside frozen routed
+    experts, as a user's program runs it: forward, losses, and the gradients of
+    the router's and the shared expert's weights."""
+
+    def __init__(self, B, T=96, H=256, N=16, k=4, I=128, dtype=BF16, seed=0):
+        self.B, self.k, self.N, self.T = B, k, N, T
+        g = np.random.default_rng(seed)
+        c = lambda *s: _rand(g, s, s[-1] ** -0.5, dtype)  # noqa: E731
+        self.x, self.target = _rand(g, (T, H), 1.0, dtype), _rand(g, (T, H), 1.0, dtype)
+        self.wg, self.w13, self.w2 = c(N, H), c(N, 2 * I, H), c(N, H, I)
+        self.s13, self.s2, self.b2 = c(2 * I, H), c(H, I), _rand(g, (H,), 0.1, dtype)
+        self.mask = torch.ones(T, dtype=torch.uint8, device="cuda")
+        self.mask[-5:] = 0
+        self.rng = torch.tensor([11, 0], dtype=torch.int64, device="cuda")
+        self.d_losses = torch.tensor([0.02, 0.001], device="cuda")
+        self.p = 0.1
+        e = lambda *s: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+        n = lambda size: B.new_workspace(size, "cuda")  # noqa: E731
+        lay = B.Layer(T, H, N, k, I, 0, dtype)
+        self.lay = lay
+        self.ws_router = n(B.moe_router_workspace_size(T, N, H, dtype))
+        self.ws = n(max(B.moe_linear_workspace_size(T, H, I, "swiglu", dtype),
+                        B.moe_linear_workspace_size(T, I, H, "none", dtype),
+                        B.moe_linear_backward_workspace_size(T, H, I, "swiglu", dtype),
+                        B.moe_linear_backward_workspace_size(T, I, H, "none", dtype),
+                        B.moe_linear_backward_workspace_size(T, H, N, "none", dtype),
+                        B.moe_balance_workspace_size(T, N), B.moe_ffn_workspace_size(T, N, k, H, I, dtype)))
+        self.z, self.h, self.shared, self.y = e(T, 2 * I), e(T, I), e(T, H), e(T, H)
+        self.logits = torch.empty(T, N, device="cuda")
+        self.loss = dict(losses=torch.empty(2, device="cuda"),
+                         counts=torch.empty(N + 1, dtype=torch.int32, device="cuda"),
+                         mean_prob=torch.empty(N, device="cuda"), lse=torch.empty(T, device="cuda"))
+        self.dy, self.dg, self.dl = e(T, H), torch.empty(T, k, device="cuda"), e(T, N)
+        self.dh = e(T, I)
+        self.grads = dict(wg=e(N, H), s13=e(2 * I, H), s2=e(H, I), b2=e(H), xr=e(T, H), xs=e(T, H))
+
+    def run(self):
+        B, lay, k = self.B, self.lay, self.k
+        B.moe_router_topk(self.x, self.wg, k, 0, self.ws_router, self.logits, lay.topk_ids,
+                          lay.topk_gates, lay.fallback_ids)
+        B.moe_dispatch(lay.topk_ids, self.N, lay.ws_disp, lay.disp)
+        B.moe_expert_ffn(self.x, lay.disp["row_token"], lay.disp["expert_offsets"], self.w13, self.w2,
+                         k, self.ws, lay.out_rows)
+        B.moe_linear(self.x, self.s13, self.ws, act="swiglu", z=self.z, y=self.h)
+        B.moe_linear(self.h, self.s2, self.ws, bias=self.b2, residual=self.x, y=self.shared)
+        B.moe_combine_dropout(lay.out_rows, lay.disp["slot_row"], lay.topk_gates, self.p, self.rng,
+                              self.shared, self.y)
+        B.moe_balance_loss(self.logits, lay.topk_ids, self.ws, self.mask, self.loss)
+        torch.sub(self.y, self.target, out=self.dy)
+        self.dy.mul_(self.mask[:, None])
+        B.moe_combine_backward(self.dy, lay.out_rows, lay.disp["slot_row"], lay.topk_gates, self.p,
+                               self.rng, d_gates=self.dg)
+        B.moe_router_backward(self.logits, lay.topk_ids, self.loss["lse"], self.loss["counts"],
+                              self.d_losses, self.mask, self.dg, self.dl)
+        G = self.grads
+        B.moe_linear_backward(self.dl, self.x, self.wg, self.ws, dx=G["xr"], dw=G["wg"])
+        B.moe_linear_backward(self.dy, self.h, self.s2, self.ws, dx=self.dh, dw=G["s2"], dbias=G["b2"])
+        B.moe_linear_backward(self.dh, self.x, self.s13, self.ws, z=self.z, act="swiglu", dx=G["xs"],
+                              dw=G["s13"])
+
+    def outputs(self):
+        return {"y": self.y, "losses": self.loss["losses"], "counts": self.loss["counts"], **self.grads}
+
+
+def test_tuning_step_against_autograd(B):
+    """The step's gradients against a 64-bit autograd of the same step (same
+    routing, mask and expert rows).  Every intermediate that the kernels hand on
+    in bf16 (h, z, the shared output, y, dy, dlogits, dh) is off by half a step,
+    2^-8; a dozen such roundings along a chain keep the relative error of a whole
+    gradient tensor (2-norm) under 12 2^-8."""
+    st = _Step(B)
+    st.run()
+    T, k = st.T, st.k
+    lay = st.lay
+    D = lambda t: t.detach().double().cpu()  # noqa: E731
+    x0, wg, s13, s2, b2 = (D(t).requires_grad_() for t in (st.x, st.wg, st.s13, st.s2, st.b2))
+    xr = D(st.x).requires_grad_()
+    ids, slot_row = lay.topk_ids.cpu().long(), lay.disp["slot_row"].cpu().long()
+    logits = xr @ wg.t()
+    prob = torch.softmax(logits, 1)
+    gates = prob.gather(1, ids)
+    rows = D(lay.out_rows)[slot_row]
+    z = x0 @ s13.t()
+    I = z.shape[1] // 2
+    hh = torch.nn.functional.silu(z[:, :I]) * z[:, I:]
+    shared = hh @ s2.t() + b2 + D(st.x)
+    m = torch.from_numpy(R.keep(11, 0, T, x0.shape[1], st.p) / (1 - st.p))
+    y = shared + m * (gates[:, :, None] * rows).sum(1)
+    on = st.mask.cpu().double()
+    n = on.sum()
+    counts = torch.zeros(st.N, dtype=torch.float64)
+    for t in range(T):
+        if on[t]:
+            counts[ids[t]] += 1
+    bal = st.N / (k * n) * (counts * (prob * on[:, None]).sum(0) / n).sum()
+    zl = ((torch.logsumexp(logits, 1) ** 2) * on).sum() / n
+    total = 0.5 * (((y - D(st.target)) ** 2) * on[:, None]).sum() + 0.02 * bal + 0.001 * zl
+    total.backward()
+    assert np.array_equal(st.loss["counts"].cpu().numpy()[:-1], counts.numpy().astype(np.int64))
+    want = dict(wg=wg.grad, s13=s13.grad, s2=s2.grad, b2=b2.grad, xr=xr.grad, xs=x0.grad, y=y.detach())
+    for name, v in want.items():
+        got = D(st.outputs()[name])
+        rel = float((got - v).norm() / v.norm())
+        print(f"[gpu-test] step {name}: {rel:.2e}", flush=True)
+        assert rel <= 12 * 2.0 ** -8, (name, rel)
+
+
+def test_tuning_step_on_a_side_stream(B):
+    st = _Step(B, seed=1)
+    st.run()
+    torch.cuda.synchronize()
+    want = {n: t.clone() for n, t in st.outputs().items()}
+    for t in st.outputs().values():
+        t.zero_()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        st.run()
+    side.synchronize()
+    for n, t in st.outputs().items():
+        assert torch.equal(t, want[n]), n
+
+
+def test_tuning_steps_captured_with_one_workspace(B):
+    """Two captured steps that share a workspace, replayed in turn with eager
+    work between; the dropout offset and the inputs change between replays, and
+    every replay equals the eager step."""
+    a, b = _Step(B, seed=2), _Step(B, T=80, seed=3)
+    if b.ws.numel() > a.ws.numel():
+        a.ws = b.ws
+    b.ws = a.ws
+    graphs = []
+    for st in (a, b):
+        st.run()
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            st.run()
+        graphs.append(gr)
+    seen = []
+    for rep in range(4):
+        for st, gr in zip((a, b), graphs):
+            st.rng[1] = 100 + rep
+            st.x.mul_(-1 if rep % 2 else 1.0)
+            st.run()
+            torch.cuda.synchronize()
+            want = {n: t.clone() for n, t in st.outputs().items()}
+            for t in st.outputs().values():
+                t.zero_()
+            gr.replay()
+            torch.cuda.synchronize()
+            for n, t in st.outputs().items():
+                assert torch.equal(t, want[n]), (rep, n)
+            if st is a:
+                seen.append(want["y"])
+    assert not torch.equal(seen[0], seen[2])  # another offset, another mask
+
+
+def test_binding_refusals_on_the_gpu(B):
+    x, w = torch.zeros(4, 64, device="cuda"), torch.zeros(32, 64, device="cuda")
+    ws = B.new_workspace(1 << 16, "cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        B.moe_linear(x.t().contiguous().t(), w, ws)
+    with pytest.raises(ValueError, match="shape"):
+        B.moe_linear(x, w, ws, bias=torch.zeros(31, device="cuda"))
+    with pytest.raises(ValueError, match="dtype"):
+        B.moe_linear(x, w.bfloat16(), ws)
+    with pytest.raises(RuntimeError, match="EUNSUP"):
+        B.moe_linear(torch.zeros(4, 62, device="cuda"), torch.zeros(32, 62, device="cuda"), ws)
+    flat = torch.zeros(4 * 64 + 1, device="cuda")
+    with pytest.raises(RuntimeError, match="EINVAL"):
+        B.moe_linear(flat[1:].view(4, 64), w, ws)
+    with pytest.raises(RuntimeError, match="EINVAL"):
+        B.moe_linear_backward(torch.zeros(4, 32, device="cuda"), x, w, ws[:16], dw=w.clone(),
+                              dbias=torch.zeros(32, device="cuda"))
+    rows, S, G = torch.zeros(8, 64, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda"), \
+        torch.zeros(4, 2, device="cuda")
+    with pytest.raises(RuntimeError, match="EINVAL"):
+        B.moe_combine_dropout(rows, S, G, p=1.0, rng=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="dropout needs rng"):
+        B.moe_combine_dropout(rows, S, G, p=0.5)

@@ -7,66 +7,29 @@
 //
 // act "swiglu" takes W [2O,K], gate rows first: y = silu(z[:, :O]) z[:, O:].
 #include <algorithm>
-#include <type_traits>
+#include <atomic>
 
 #include "common.h"
+#include "linear_common.h"
+#include "linear_mma.h"
 
 namespace moe {
 namespace lin {
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ float load_elem(const float* p) { return *p; }
-__device__ __forceinline__ float load_elem(const __bf16* p) { return static_cast<float>(*p); }
-__device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_elem(__bf16* p, float v) { *p = static_cast<__bf16>(v); }
-
-// ------------------------------------------------------------- activations
-__device__ __forceinline__ float sigmoid(float a) { return 1.f / (1.f + expf(-a)); }
-__device__ __forceinline__ float gauss_cdf(float a) {
-  return 0.5f * erfcf(a * -0.70710678118654752f);
-}
-
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? z : 0.f;
-    case MOE_ACT_SILU: return z * sigmoid(z);
-    case MOE_ACT_GELU: return z * gauss_cdf(z);
-    default: return z;
-  }
-}
-
-__device__ __forceinline__ float act_slope(int act, float z) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case MOE_ACT_SILU: {
-      const float s = sigmoid(z);
-      return s * (1.f + z * (1.f - s));
-    }
-    case MOE_ACT_GELU: return gauss_cdf(z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-    default: return 1.f;
-  }
-}
-
-// ------------------------------------------------------------ tile product
+// ------------------------------------------------------------ fp32 product
 // C[m][n] = sum_k A(m, k) B(n, k), A(m, k) = a[m * am + k * ak] and so on.
 struct Prod {
-  const void *a, *b;
+  const float *a, *b;
   long am, ak, bm, bk;
   int M, N, K;
-  // epilogue
-  int act;
-  const void *bias, *residual;
-  void *z, *c;
+  Epilogue e;
 };
 
 constexpr int TILE = 64, BK = 16, NTHR = 256;
 
-template <typename E, bool GLU>
-__global__ __launch_bounds__(NTHR) void product_kernel(Prod p) {
+template <bool GLU>
+__global__ __launch_bounds__(NTHR) void product_f32_kernel(Prod p) {
   __shared__ float sa[BK][TILE + 1], sb[GLU ? 2 : 1][BK][TILE + 1];
-  const E* a = static_cast<const E*>(p.a);
-  const E* b = static_cast<const E*>(p.b);
   const int m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   float acc[GLU ? 2 : 1][4][4] = {};
@@ -76,12 +39,11 @@ __global__ __launch_bounds__(NTHR) void product_kernel(Prod p) {
       // consecutive threads along the operand's contiguous axis
       const int am = p.ak == 1 ? i / BK : i % TILE, ak = p.ak == 1 ? i % BK : i / TILE;
       const int bm = p.bk == 1 ? i / BK : i % TILE, bk = p.bk == 1 ? i % BK : i / TILE;
-      sa[ak][am] = m0 + am < p.M && k0 + ak < p.K ? load_elem(a + (m0 + am) * p.am + (k0 + ak) * p.ak)
-                                                  : 0.f;
+      sa[ak][am] = m0 + am < p.M && k0 + ak < p.K ? p.a[(m0 + am) * p.am + (k0 + ak) * p.ak] : 0.f;
 #pragma unroll
       for (int h = 0; h < (GLU ? 2 : 1); ++h)
         sb[h][bk][bm] = n0 + bm < p.N && k0 + bk < p.K
-                            ? load_elem(b + (h * static_cast<long>(p.N) + n0 + bm) * p.bm + (k0 + bk) * p.bk)
+                            ? p.b[(h * static_cast<long>(p.N) + n0 + bm) * p.bm + (k0 + bk) * p.bk]
                             : 0.f;
     }
     __syncthreads();
@@ -95,93 +57,193 @@ __global__ __launch_bounds__(NTHR) void product_kernel(Prod p) {
           for (int h = 0; h < (GLU ? 2 : 1); ++h)
             acc[h][i][j] += sa[kk][ty * 4 + i] * sb[h][kk][tx * 4 + j];
   }
-  const E* bias = static_cast<const E*>(p.bias);
-  const E* residual = static_cast<const E*>(p.residual);
-  E* z = static_cast<E*>(p.z);
-  E* c = static_cast<E*>(p.c);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= p.M || n >= p.N) continue;
-      const size_t at = static_cast<size_t>(m) * p.N + n;
-      float v;
-      if constexpr (GLU) {
-        const float g = acc[0][i][j] + (bias ? load_elem(bias + n) : 0.f);
-        const float u = acc[1][i][j] + (bias ? load_elem(bias + p.N + n) : 0.f);
-        if (z) {
-          const size_t zr = static_cast<size_t>(m) * 2 * p.N;
-          store_elem(z + zr + n, g);
-          store_elem(z + zr + p.N + n, u);
-        }
-        v = g * sigmoid(g) * u;
-      } else {
-        const float s = acc[0][i][j] + (bias ? load_elem(bias + n) : 0.f);
-        if (z) store_elem(z + at, s);
-        v = act_value(p.act, s);
-      }
-      if (residual) v += load_elem(residual + at);
-      store_elem(c + at, v);
-    }
+  const int n = n0 + tx * 4;
+  if (n >= p.N) return;
+  for (int i = 0; i < 4; ++i) {
+    const int m = m0 + ty * 4 + i;
+    if (m < p.M) finish4<float, GLU>(p.e, m, n, p.N, acc[0][i], acc[GLU ? 1 : 0][i]);
+  }
 }
 
-template <typename E>
-void launch_product(const Prod& p, bool glu, hipStream_t s) {
+inline int product(const Prod& p, bool glu, hipStream_t s) {
   const dim3 grid((p.N + TILE - 1) / TILE, (p.M + TILE - 1) / TILE);
-  if (glu) hipLaunchKernelGGL((product_kernel<E, true>), grid, dim3(NTHR), 0, s, p);
-  else hipLaunchKernelGGL((product_kernel<E, false>), grid, dim3(NTHR), 0, s, p);
+  if (glu) hipLaunchKernelGGL(product_f32_kernel<true>, grid, dim3(NTHR), 0, s, p);
+  else hipLaunchKernelGGL(product_f32_kernel<false>, grid, dim3(NTHR), 0, s, p);
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------ bf16 product
+template <bool RS, bool CS, int BM, int BN, int WM, int WN, bool GLU, bool PART, int WGS>
+int launch_mma(const Mma& a, hipStream_t s) {
+  constexpr int lds = (2 * BM + 3 * BN) * SLICE * 2;
+  const void* fn = reinterpret_cast<const void*>(mma_kernel<RS, CS, BM, BN, WM, WN, GLU, PART, WGS>);
+  // the LDS limit is a per-device function attribute: set once per device
+  static std::atomic<bool> attr_set[64];
+  const int dev = current_device();
+  if (dev < 0 || !attr_set[dev].load(std::memory_order_acquire)) {
+    if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
+      return MOE_EHIP;
+    if (dev >= 0) attr_set[dev].store(true, std::memory_order_release);
+  }
+  const int total = a.tm * a.tn * a.splits;
+  hipLaunchKernelGGL((mma_kernel<RS, CS, BM, BN, WM, WN, GLU, PART, WGS>), dim3((total + 7) / 8 * 8),
+                     dim3(WM * WN * MOE_WAVE), lds, s, a);
+  return MOE_OK;
+}
+
+// Sums the splits' partial products in their order and finishes the output.
+// GLU: the parts hold gate and up columns, 2 N of them.
+template <typename E, bool GLU>
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int splits,
+                                                   int M, int N, Epilogue e) {
+  const size_t i = (blockIdx.x * static_cast<size_t>(256) + threadIdx.x) * 4;
+  if (i >= static_cast<size_t>(M) * N) return;
+  const int m = static_cast<int>(i / N), n = static_cast<int>(i % N);
+  const size_t W = GLU ? 2 * static_cast<size_t>(N) : N;
+  float g[4] = {}, u[4] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float* p = part + (static_cast<size_t>(s) * M + m) * W + n;
+    float f[4];
+    load4(p, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g[j] += f[j];
+    if constexpr (GLU) {
+      load4(p + N, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] += f[j];
+    }
+  }
+  finish4<E, GLU>(e, m, n, N, g, u);
+}
+
+struct Plan {
+  int tile;    // edge of the square tile: 256 or 128
+  int splits;  // of the reduction
+};
+
+template <bool RS, bool CS, bool GLU, bool PART>
+int launch_tile(Mma& a, int tile, hipStream_t s) {
+  a.tm = (a.M + tile - 1) / tile;
+  const int nc = GLU ? tile / 2 : tile;
+  a.tn = (a.N + nc - 1) / nc;
+  if (tile == 256) return launch_mma<RS, CS, 256, 256, 2, 4, GLU, PART, 1>(a, s);
+  return launch_mma<RS, CS, 128, 128, 2, 2, GLU, PART, 2>(a, s);
+}
+
+// Product with the plan's tile and splits; part: room for the partial sums.
+template <bool RS, bool CS, bool GLU>
+int product(Mma a, Plan p, float* part, hipStream_t s) {
+  const int slices = (a.K + SLICE - 1) / SLICE;
+  a.per_split = (slices + p.splits - 1) / p.splits;
+  a.splits = (slices + a.per_split - 1) / a.per_split;
+  a.part = part;
+  if (a.splits == 1) return launch_tile<RS, CS, GLU, false>(a, p.tile, s);
+  const int N = a.N;
+  if (GLU) a.N *= 2;
+  const int rc = launch_tile<RS, CS, false, true>(a, p.tile, s);
+  if (rc != MOE_OK) return rc;
+  const size_t quads = static_cast<size_t>(a.M) * N / 4;
+  hipLaunchKernelGGL((join_kernel<uint16_t, GLU>), dim3((quads + 255) / 256), dim3(256), 0, s, part,
+                     a.splits, a.M, N, a.e);
+  return MOE_OK;
+}
+
+inline Plan plan(int M, int W, int K) {
+  Plan p;
+  const long big = static_cast<long>((M + 255) / 256) * ((W + 255) / 256);
+  p.tile = big >= cu_count() / 2 ? 256 : 128;
+  const long tiles = p.tile == 256 ? big : static_cast<long>((M + 127) / 128) * ((W + 127) / 128);
+  const int slices = (K + SLICE - 1) / SLICE;
+  p.splits = static_cast<int>(std::max(1L, std::min<long>(std::min(16, slices / 4), cu_count() / std::max(1L, tiles))));
+  return p;
+}
+inline size_t part_bytes(int M, int W, int K) {
+  const Plan p = plan(M, W, K);
+  return p.splits > 1 ? static_cast<size_t>(p.splits) * M * W * 4 : 0;
 }
 
 // ------------------------------------------------ activation gradient, bias
 // dz (rounded to the element type, the operand of both products) and, per
-// block of token rows, the fp32 column sums of the unrounded dz.
-constexpr int ROWS = 64;
+// block of token rows, the fp32 column sums of the unrounded dz.  A thread
+// owns 16 bytes of dy's columns in every eighth row of the block; bound by
+// HBM: dy and z read, dz written once.
+constexpr int COLT = 32, ROWT = 8;  // threads along the columns and the rows
 
-template <typename E>
-__global__ __launch_bounds__(64) void act_grad_kernel(const E* __restrict__ dy,
-                                                      const E* __restrict__ z, int T, int O,
-                                                      int act, E* __restrict__ dz,
-                                                      float* __restrict__ part) {
-  const int o = blockIdx.x * 64 + threadIdx.x;
-  if (o >= O) return;
-  const int W = act == MOE_ACT_SWIGLU ? 2 * O : O;
-  float s0 = 0.f, s1 = 0.f;
-  const int t1 = min(T, static_cast<int>(blockIdx.y + 1) * ROWS);
-  for (int t = blockIdx.y * ROWS; t < t1; ++t) {
-    const float g = load_elem(dy + static_cast<size_t>(t) * O + o);
+template <typename D>
+__global__ __launch_bounds__(COLT * ROWT) void act_grad_kernel(
+    const typename D::elem* __restrict__ dy, const typename D::elem* __restrict__ z, int T, int O,
+    int act, int rows, typename D::elem* __restrict__ dz, float* __restrict__ part) {
+  constexpr int V = D::V;
+  __shared__ float red[ROWT][COLT * V];
+  const int cx = threadIdx.x % COLT, ry = threadIdx.x / COLT;
+  const int o = (blockIdx.x * COLT + cx) * V;
+  const bool live = o < O, glu = act == MOE_ACT_SWIGLU;
+  const int W = glu ? 2 * O : O;
+  float s0[V] = {}, s1[V] = {};
+  const int t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
+  for (int t = live ? t0 + ry : t1; t < t1; t += ROWT) {
     const size_t zr = static_cast<size_t>(t) * W + o;
-    if (act == MOE_ACT_SWIGLU) {
-      const float a = load_elem(z + zr), b = load_elem(z + zr + O);
-      const float da = g * b * act_slope(MOE_ACT_SILU, a), db = g * a * sigmoid(a);
-      store_elem(dz + zr, da);
-      store_elem(dz + zr + O, db);
-      s0 += da;
-      s1 += db;
-    } else {
-      const float d = act == MOE_ACT_NONE ? g : g * act_slope(act, load_elem(z + zr));
-      if (act != MOE_ACT_NONE) store_elem(dz + zr, d);
-      s0 += d;
+#pragma unroll
+    for (int h = 0; h < V; h += 4) {
+      float g[4], a[4], b[4];
+      load4(dy + static_cast<size_t>(t) * O + o + h, g);
+      if (act != MOE_ACT_NONE) load4(z + zr + h, a);
+      if (glu) {
+        load4(z + zr + O + h, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float sg = sigmoid(a[i]);
+          const float up = g[i] * a[i] * sg;
+          g[i] = g[i] * b[i] * (sg * (1.f + a[i] * (1.f - sg)));
+          b[i] = up;
+        }
+        store4(dz + zr + O + h, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s1[h + i] += b[i];
+      } else if (act != MOE_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) g[i] *= act_slope(act, a[i]);
+      }
+      if (act != MOE_ACT_NONE) store4(dz + zr + h, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s0[h + i] += g[i];
     }
   }
-  if (part) {
-    part[static_cast<size_t>(blockIdx.y) * W + o] = s0;
-    if (act == MOE_ACT_SWIGLU) part[static_cast<size_t>(blockIdx.y) * W + O + o] = s1;
+  if (!part) return;
+  for (int half = 0; half < (glu ? 2 : 1); ++half) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) red[ry][cx * V + i] = half ? s1[i] : s0[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < COLT * V; c += COLT * ROWT) {
+      const int col = blockIdx.x * COLT * V + c;
+      if (col >= O) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int r = 0; r < ROWT; ++r) v += red[r][c];
+      part[static_cast<size_t>(blockIdx.y) * W + half * O + col] = v;
+    }
   }
 }
 
 template <typename E>
-__global__ __launch_bounds__(64) void bias_sum_kernel(const float* __restrict__ part, int blocks,
-                                                      int W, E* __restrict__ dbias) {
-  const int o = blockIdx.x * 64 + threadIdx.x;
-  if (o >= W) return;
-  float s = 0.f;
-  for (int b = 0; b < blocks; ++b) s += part[static_cast<size_t>(b) * W + o];
-  store_elem(dbias + o, s);
+__global__ __launch_bounds__(256) void bias_sum_kernel(const float* __restrict__ part, int blocks,
+                                                       int W, E* __restrict__ dbias) {
+  __shared__ float red[4][64];
+  const int c = threadIdx.x % 64, r = threadIdx.x / 64, o = blockIdx.x * 64 + c;
+  float v = 0.f;
+  if (o < W)
+#pragma unroll 8
+    for (int b = r; b < blocks; b += 4) v += part[static_cast<size_t>(b) * W + o];
+  red[r][c] = v;
+  __syncthreads();
+  if (r == 0 && o < W) store1(dbias + o, red[0][c] + red[1][c] + red[2][c] + red[3][c]);
 }
 
 template <typename E>
 __global__ void zero_kernel(E* p, size_t n) {
   const size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x;
-  if (i < n) store_elem(p + i, 0.f);
+  if (i < n) store1(p + i, 0.f);
 }
 
 // --------------------------------------------------------------------- host
@@ -201,24 +263,42 @@ inline int check(int T, int K, int O, int act, int dtype) {
 }
 
 struct BackPlan {
-  size_t dz, part, bytes;  // offsets, size
-  int blocks;
+  int rows, blocks;                // token rows of an act_grad block, their number
+  size_t dz, sums, parts, bytes;  // offsets, size
 };
 
-inline BackPlan back_plan(int T, int O, int act, int dtype) {
+inline BackPlan back_plan(int T, int K, int O, int act, int dtype) {
   BackPlan p;
-  const size_t W = width(O, act);
-  p.blocks = (T + ROWS - 1) / ROWS;
+  const int W = width(O, act);
+  p.rows = std::max(ROWT, (T + 255) / 256);
+  p.blocks = (T + p.rows - 1) / p.rows;
   p.dz = 0;
-  p.part = act == MOE_ACT_NONE ? 0 : up256(static_cast<size_t>(T) * W * elem_size(dtype));
-  p.bytes = p.part + up256(static_cast<size_t>(p.blocks) * W * 4) + 256;
+  p.sums = act == MOE_ACT_NONE ? 0 : up256(static_cast<size_t>(T) * W * elem_size(dtype));
+  p.parts = p.sums + up256(static_cast<size_t>(p.blocks) * W * 4);
+  p.bytes = p.parts + 256;
+  if (dtype == MOE_BF16 && T > 0)
+    p.bytes += std::max(part_bytes(T, K, W), part_bytes(W, K, T));
   return p;
 }
 
-template <typename E>
+template <typename D>
+int act_grad(const void* dy, const void* z, int T, int O, int act, const BackPlan& p, void* dz,
+             float* sums, void* dbias, hipStream_t s) {
+  typedef typename D::elem E;
+  const int W = width(O, act);
+  hipLaunchKernelGGL(act_grad_kernel<D>, dim3((O + COLT * D::V - 1) / (COLT * D::V), p.blocks),
+                     dim3(COLT * ROWT), 0, s, static_cast<const E*>(dy), static_cast<const E*>(z),
+                     T, O, act, p.rows, static_cast<E*>(dz), sums);
+  if (dbias)
+    hipLaunchKernelGGL(bias_sum_kernel<E>, dim3((W + 63) / 64), dim3(256), 0, s, sums, p.blocks, W,
+                       static_cast<E*>(dbias));
+  return MOE_OK;
+}
+
+template <typename D>
 int backward(const void* dy, const void* x, const void* w, const void* z, int T, int K, int O,
              int act, int dtype, void* dx, void* dw, void* dbias, char* ws, hipStream_t s) {
-  const BackPlan p = back_plan(T, O, act, dtype);
+  typedef typename D::elem E;
   const int W = width(O, act);
   if (T == 0) {  // sums over no tokens
     if (!dw && !dbias) return MOE_OK;
@@ -231,34 +311,57 @@ int backward(const void* dy, const void* x, const void* w, const void* z, int T,
                          static_cast<E*>(dbias), static_cast<size_t>(W));
     return launch_status();
   }
+  const BackPlan p = back_plan(T, K, O, act, dtype);
   const void* dz = dy;
-  float* part = dbias ? reinterpret_cast<float*>(ws + p.part) : nullptr;
-  if (act != MOE_ACT_NONE || dbias) {
-    hipLaunchKernelGGL(act_grad_kernel<E>, dim3((O + 63) / 64, p.blocks), dim3(64), 0, s,
-                       static_cast<const E*>(dy), static_cast<const E*>(z), T, O, act,
-                       reinterpret_cast<E*>(ws + p.dz), part);
+  if ((act != MOE_ACT_NONE && (dx || dw)) || dbias) {
+    float* sums = dbias ? reinterpret_cast<float*>(ws + p.sums) : nullptr;
+    act_grad<D>(dy, z, T, O, act, p, ws + p.dz, sums, dbias, s);
     if (act != MOE_ACT_NONE) dz = ws + p.dz;
   }
-  if (dbias)
-    hipLaunchKernelGGL(bias_sum_kernel<E>, dim3((W + 63) / 64), dim3(64), 0, s, part, p.blocks, W,
-                       static_cast<E*>(dbias));
-  if (dx) {
+  int rc = MOE_OK;
+  if (dtype == MOE_BF16) {
+    float* part = reinterpret_cast<float*>(ws + p.parts);
+    Mma q{};
+    q.N = K;
+    q.ldr = W;
+    q.ldc = K;
+    q.r = static_cast<const uint16_t*>(dz);
+    if (dx) {
+      q.c = static_cast<const uint16_t*>(w);
+      q.M = T;
+      q.K = W;
+      q.e.y = dx;
+      rc = product<false, true, false>(q, plan(T, K, W), part, s);
+    }
+    if (dw && rc == MOE_OK) {
+      q.c = static_cast<const uint16_t*>(x);
+      q.M = W;
+      q.K = T;
+      q.e.y = dw;
+      rc = product<true, true, false>(q, plan(W, K, T), part, s);
+    }
+  } else {
     Prod q{};
-    q.a = dz; q.am = W; q.ak = 1;
-    q.b = w; q.bm = 1; q.bk = K;
-    q.M = T; q.N = K; q.K = W;
-    q.c = dx;
-    launch_product<E>(q, false, s);
+    q.a = static_cast<const float*>(dz);
+    q.bm = 1;
+    q.bk = K;
+    q.N = K;
+    if (dx) {
+      q.am = W; q.ak = 1;
+      q.b = static_cast<const float*>(w);
+      q.M = T; q.K = W;
+      q.e.y = dx;
+      rc = product(q, false, s);
+    }
+    if (dw && rc == MOE_OK) {
+      q.am = 1; q.ak = W;
+      q.b = static_cast<const float*>(x);
+      q.M = W; q.K = T;
+      q.e.y = dw;
+      rc = product(q, false, s);
+    }
   }
-  if (dw) {
-    Prod q{};
-    q.a = dz; q.am = 1; q.ak = W;
-    q.b = x; q.bm = 1; q.bk = K;
-    q.M = W; q.N = K; q.K = T;
-    q.c = dw;
-    launch_product<E>(q, false, s);
-  }
-  return launch_status();
+  return rc == MOE_OK ? launch_status() : rc;
 }
 
 }  // namespace lin
@@ -269,7 +372,7 @@ using namespace moe::lin;
 
 extern "C" size_t moe_linear_workspace_size(int T, int K, int O, int act, int dtype) {
   if (check(T, K, O, act, dtype) != MOE_OK) return 0;
-  return 256;
+  return 256 + (dtype == MOE_BF16 && T > 0 ? part_bytes(T, width(O, act), K) : 0);
 }
 
 extern "C" int moe_linear(const void* x, const void* w, const void* bias, const void* residual,
@@ -283,21 +386,39 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
     if (!aligned16(q)) return MOE_EINVAL;
   if (workspace_bytes < moe_linear_workspace_size(T, K, O, act, dtype)) return MOE_EINVAL;
   hipStream_t s = as_stream(stream);
-  Prod p{};
-  p.a = x; p.am = K; p.ak = 1;
-  p.b = w; p.bm = K; p.bk = 1;
-  p.M = T; p.N = O; p.K = K;
-  p.act = act;
-  p.bias = bias; p.residual = residual;
-  p.z = z; p.c = y;
-  if (dtype == MOE_BF16) launch_product<__bf16>(p, act == MOE_ACT_SWIGLU, s);
-  else launch_product<float>(p, act == MOE_ACT_SWIGLU, s);
-  return launch_status();
+  const bool glu = act == MOE_ACT_SWIGLU;
+  const Epilogue e{bias, residual, z, y, act};
+  int r;
+  if (dtype == MOE_BF16) {
+    Mma q{};
+    q.r = static_cast<const uint16_t*>(x);
+    q.c = static_cast<const uint16_t*>(w);
+    q.ldr = q.ldc = K;
+    q.M = T;
+    q.N = O;
+    q.K = K;
+    q.e = e;
+    float* part = static_cast<float*>(workspace);
+    const Plan p = plan(T, width(O, act), K);
+    r = glu ? product<false, false, true>(q, p, part, s) : product<false, false, false>(q, p, part, s);
+  } else {
+    Prod q{};
+    q.a = static_cast<const float*>(x);
+    q.b = static_cast<const float*>(w);
+    q.am = q.bm = K;
+    q.ak = q.bk = 1;
+    q.M = T;
+    q.N = O;
+    q.K = K;
+    q.e = e;
+    r = product(q, glu, s);
+  }
+  return r == MOE_OK ? launch_status() : r;
 }
 
 extern "C" size_t moe_linear_backward_workspace_size(int T, int K, int O, int act, int dtype) {
   if (check(T, K, O, act, dtype) != MOE_OK) return 0;
-  return back_plan(T, O, act, dtype).bytes;
+  return back_plan(T, K, O, act, dtype).bytes;
 }
 
 extern "C" int moe_linear_backward(const void* dy, const void* x, const void* w, const void* z,
@@ -317,6 +438,6 @@ extern "C" int moe_linear_backward(const void* dy, const void* x, const void* w,
   char* ws = static_cast<char*>(workspace);
   hipStream_t s = as_stream(stream);
   if (dtype == MOE_BF16)
-    return backward<__bf16>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
-  return backward<float>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
+    return backward<Bf16>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
+  return backward<F32>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
 }

@@ -1,0 +1,165 @@
+// Activations and the output epilogue of the dense layer.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+namespace lin {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------- element types: vectors
+struct Bf16 {
+  typedef uint16_t elem;
+  static constexpr int V = 8;  // elements in 16 bytes
+};
+struct F32 {
+  typedef float elem;
+  static constexpr int V = 4;
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {  // round to nearest even
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float* f) {
+  const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+  f[0] = __uint_as_float(w.x << 16);
+  f[1] = __uint_as_float(w.x & 0xffff0000u);
+  f[2] = __uint_as_float(w.y << 16);
+  f[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float* f) {
+  const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+  f[0] = v.x;
+  f[1] = v.y;
+  f[2] = v.z;
+  f[3] = v.w;
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float* f) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{pack2(f[0], f[1]), pack2(f[2], f[3])};
+}
+__device__ __forceinline__ void store4(float* p, const float* f) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+}
+__device__ __forceinline__ void store1(uint16_t* p, float v) {
+  *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
+// ------------------------------------------------------------- activations
+// The hardware exponential and reciprocal (about one unit each); the rounded
+// argument of the exponential costs |a| 2^-24 relative.
+__device__ __forceinline__ float sigmoid(float a) {
+  return __builtin_amdgcn_rcpf(1.f + __expf(-a));
+}
+
+// Normal distribution function Phi(a) and, in *density, exp(-a^2/2): the
+// rational form 7.1.26 of Abramowitz and Stegun for erfc, whose polynomial is
+// off by at most 1.5e-7 (erf) and which shares its exponential with the
+// density.  The library's erfc took a quarter of a wide layer's time.
+__device__ __forceinline__ float normal_cdf(float a, float* density) {
+  const float x = fabsf(a) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+  const float e = __expf(-x * x);
+  float p = 1.061405429f;
+  p = p * t - 1.453152027f;
+  p = p * t + 1.421413741f;
+  p = p * t - 0.284496736f;
+  p = p * t + 0.254829592f;
+  const float tail = 0.5f * p * t * e;
+  *density = e;
+  return a >= 0.f ? 1.f - tail : tail;
+}
+
+__device__ __forceinline__ float act_value(int act, float z) {
+  float e;
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? z : 0.f;
+    case MOE_ACT_SILU: return z * sigmoid(z);
+    case MOE_ACT_GELU: return z * normal_cdf(z, &e);
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float act_slope(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case MOE_ACT_SILU: {
+      const float s = sigmoid(z);
+      return s * (1.f + z * (1.f - s));
+    }
+    case MOE_ACT_GELU: {
+      float e;
+      const float c = normal_cdf(z, &e);
+      return c + z * 0.39894228040143268f * e;
+    }
+    default: return 1.f;
+  }
+}
+
+// ------------------------------------------------------------------ output
+// What follows the product: bias, z, activation, residual, y.
+struct Epilogue {
+  const void *bias, *residual;
+  void *z, *y;
+  int act;
+};
+
+// Columns n .. n + 3 of row m; N: columns of y.  GLU: g and u are the gate
+// and up sums of those columns.  residual may be y: each element is read by
+// the lane that writes it, before it does.
+template <typename E, bool GLU>
+__device__ __forceinline__ void finish4(const Epilogue& e, int m, int n, int N, float* g,
+                                        float* u) {
+  const size_t at = static_cast<size_t>(m) * N + n;
+  if (e.bias) {
+    float b[4];
+    load4(static_cast<const E*>(e.bias) + n, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] += b[i];
+    if constexpr (GLU) {
+      load4(static_cast<const E*>(e.bias) + N + n, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] += b[i];
+    }
+  }
+  if (e.z) {
+    E* z = static_cast<E*>(e.z) + (GLU ? at + static_cast<size_t>(m) * N : at);
+    store4(z, g);
+    if constexpr (GLU) store4(z + N, u);
+  }
+  float v[4];
+  if constexpr (GLU) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+  } else {
+    if (e.act == MOE_ACT_GELU) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = act_value(MOE_ACT_GELU, g[i]);
+    } else if (e.act == MOE_ACT_SILU) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = act_value(MOE_ACT_SILU, g[i]);
+    } else if (e.act == MOE_ACT_RELU) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = act_value(MOE_ACT_RELU, g[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = g[i];
+    }
+  }
+  if (e.residual) {
+    float r[4];
+    load4(static_cast<const E*>(e.residual) + at, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += r[i];
+  }
+  store4(static_cast<E*>(e.y) + at, v);
+}
+
+}  // namespace lin
+}  // namespace moe

@@ -162,12 +162,40 @@ def _act(act: str) -> int:
     return ACTS[act]
 
 
-def _one_device(ref, *tensors):
-    """The launches go to the current device: every tensor must live there."""
-    here = torch.cuda.current_device()
-    for t in (ref,) + tensors:
-        if t is not None and t.device.index != here:
-            raise ValueError(f"a tensor on {t.device}, but the current device is cuda:{here}")
+def _here(ref: torch.Tensor, name: str) -> int:
+    """The current device, where the launches go; ref must be on a GPU."""
+    if not isinstance(ref, torch.Tensor) or not ref.is_cuda:
+        _dev(ref, None, name)
+    return torch.cuda.current_device()
+
+
+def _arg(t, dtype, name, shape, here):
+    """Address of a required array: on the current device, of this type and
+    shape, contiguous.  (One test for a good argument; _dev names what is wrong
+    with a bad one.)"""
+    try:
+        if (t.get_device() == here and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name, shape)
+    raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{here}")
+
+
+def _arg_opt(t, dtype, name, shape, here):
+    return None if t is None else _arg(t, dtype, name, shape, here)
+
+
+def _raw_stream(here) -> int:
+    """_stream() of a known device, without building a Stream object (2.8 us,
+    a third of a small call's host time)."""
+    return torch._C._cuda_getCurrentRawStream(here)
+
+
+def _work(t, here):
+    """Address and size of a workspace."""
+    return _arg(t, torch.uint8, "workspace", t.shape, here), t.numel()
 
 
 # ---------------------------------------------------------------- the ABI
@@ -559,16 +587,16 @@ def moe_linear(x, w, workspace, bias=None, residual=None, act="none", z=None, y=
     """act(x w^T + bias) + residual; z, if given, receives the product before
     the activation for moe_linear_backward.  w is [O,K], or [2O,K] (gate rows,
     then up rows) for act "swiglu"."""
-    code, dt = _act(act), _elem(x.dtype)
+    code, dt, d = _act(act), _elem(x.dtype), x.dtype
     T, K, O, W = _linear_shapes(x, w, act)
+    here = _here(x, "x")
     if y is None:
-        y = _empty((T, O), x.dtype, x)
-    args = (_dev(x, x.dtype, "x"), _dev(w, x.dtype, "w", (W, K)),
-            _opt(bias, x.dtype, "bias", (W,)), _opt(residual, x.dtype, "residual", (T, O)),
-            T, K, O, code, dt, _opt(z, x.dtype, "z", (T, W)), _dev(y, x.dtype, "y", (T, O)),
-            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    _one_device(x, w, bias, residual, z, y, workspace)
-    _check(_lib.moe_linear(*args, _stream()), "moe_linear")
+        y = _empty((T, O), d, x)
+    _check(_lib.moe_linear(
+        _arg(x, d, "x", (T, K), here), _arg(w, d, "w", (W, K), here),
+        _arg_opt(bias, d, "bias", (W,), here), _arg_opt(residual, d, "residual", (T, O), here),
+        T, K, O, code, dt, _arg_opt(z, d, "z", (T, W), here), _arg(y, d, "y", (T, O), here),
+        *_work(workspace, here), _raw_stream(here)), "moe_linear")
     return y
 
 
@@ -577,19 +605,19 @@ def moe_linear_backward(dy, x, w, workspace, z=None, act="none", dx=None, dw=Non
     """Fills those of dx [T,K], dw (as w) and dbias [rows of w] that are given
     with the gradients of moe_linear; z is moe_linear's (not needed for act
     "none")."""
-    code, dt = _act(act), _elem(x.dtype)
+    code, dt, d = _act(act), _elem(x.dtype), x.dtype
     T, K, O, W = _linear_shapes(x, w, act)
     if z is None and code != 0 and T > 0:
         raise ValueError(f"act {act!r} needs moe_linear's z")
     if dx is None and dw is None and dbias is None:
         raise ValueError("no gradient asked for")
-    args = (_dev(dy, x.dtype, "dy", (T, O)), _dev(x, x.dtype, "x"),
-            _dev(w, x.dtype, "w", (W, K)), _opt(z, x.dtype, "z", (T, W)),
-            T, K, O, code, dt, _opt(dx, x.dtype, "dx", (T, K)),
-            _opt(dw, x.dtype, "dw", (W, K)), _opt(dbias, x.dtype, "dbias", (W,)),
-            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    _one_device(x, dy, w, z, dx, dw, dbias, workspace)
-    _check(_lib.moe_linear_backward(*args, _stream()), "moe_linear_backward")
+    here = _here(x, "x")
+    _check(_lib.moe_linear_backward(
+        _arg(dy, d, "dy", (T, O), here), _arg(x, d, "x", (T, K), here),
+        _arg(w, d, "w", (W, K), here), _arg_opt(z, d, "z", (T, W), here), T, K, O, code, dt,
+        _arg_opt(dx, d, "dx", (T, K), here), _arg_opt(dw, d, "dw", (W, K), here),
+        _arg_opt(dbias, d, "dbias", (W,), here), *_work(workspace, here), _raw_stream(here)),
+        "moe_linear_backward")
     return dx, dw, dbias
 
 
@@ -603,21 +631,19 @@ def moe_balance_loss(logits, slot_ids, workspace, token_mask=None, out=None):
     tokens counted), mean_prob [N] and lse [T]."""
     T, N = logits.shape
     k = slot_ids.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    here = _here(logits, "logits")
     if out is None:
-        out = dict(losses=_empty((2,), torch.float32, logits),
-                   counts=_empty((N + 1,), torch.int32, logits),
-                   mean_prob=_empty((N,), torch.float32, logits),
-                   lse=_empty((T,), torch.float32, logits))
-    args = (_dev(logits, torch.float32, "logits"),
-            _dev(slot_ids, torch.int32, "slot_ids", (T, k)),
-            _opt(token_mask, torch.uint8, "token_mask", (T,)), T, N, k,
-            _dev(out["losses"], torch.float32, "losses", (2,)),
-            _dev(out["counts"], torch.int32, "counts", (N + 1,)),
-            _dev(out["mean_prob"], torch.float32, "mean_prob", (N,)),
-            _dev(out["lse"], torch.float32, "lse", (T,)),
-            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    _one_device(logits, slot_ids, token_mask, workspace, *out.values())
-    _check(_lib.moe_balance_loss(*args, _stream()), "moe_balance_loss")
+        out = dict(losses=_empty((2,), f32, logits), counts=_empty((N + 1,), i32, logits),
+                   mean_prob=_empty((N,), f32, logits), lse=_empty((T,), f32, logits))
+    _check(_lib.moe_balance_loss(
+        _arg(logits, f32, "logits", (T, N), here), _arg(slot_ids, i32, "slot_ids", (T, k), here),
+        _arg_opt(token_mask, torch.uint8, "token_mask", (T,), here), T, N, k,
+        _arg(out["losses"], f32, "losses", (2,), here),
+        _arg(out["counts"], i32, "counts", (N + 1,), here),
+        _arg(out["mean_prob"], f32, "mean_prob", (N,), here),
+        _arg(out["lse"], f32, "lse", (T,), here), *_work(workspace, here), _raw_stream(here)),
+        "moe_balance_loss")
     return out
 
 
@@ -627,26 +653,25 @@ def moe_router_backward(logits, topk_ids, lse, counts, d_losses=None, token_mask
     and through the gates (d_gates [T,k]); dtype is that of a new dlogits."""
     T, N = logits.shape
     k = topk_ids.shape[1]
+    f32, i32 = torch.float32, torch.int32
+    here = _here(logits, "logits")
     if dlogits is None:
         dlogits = _empty((T, N), dtype, logits)
-    args = (_dev(logits, torch.float32, "logits"),
-            _dev(topk_ids, torch.int32, "topk_ids", (T, k)),
-            _opt(token_mask, torch.uint8, "token_mask", (T,)),
-            _dev(lse, torch.float32, "lse", (T,)),
-            _dev(counts, torch.int32, "counts", (N + 1,)),
-            _opt(d_losses, torch.float32, "d_losses", (2,)),
-            _opt(d_gates, torch.float32, "d_gates", (T, k)), T, N, k,
-            _elem(dlogits.dtype), _dev(dlogits, dlogits.dtype, "dlogits", (T, N)))
-    _one_device(logits, topk_ids, token_mask, lse, counts, d_losses, d_gates, dlogits)
-    _check(_lib.moe_router_backward(*args, _stream()), "moe_router_backward")
+    _check(_lib.moe_router_backward(
+        _arg(logits, f32, "logits", (T, N), here), _arg(topk_ids, i32, "topk_ids", (T, k), here),
+        _arg_opt(token_mask, torch.uint8, "token_mask", (T,), here),
+        _arg(lse, f32, "lse", (T,), here), _arg(counts, i32, "counts", (N + 1,), here),
+        _arg_opt(d_losses, f32, "d_losses", (2,), here),
+        _arg_opt(d_gates, f32, "d_gates", (T, k), here), T, N, k, _elem(dlogits.dtype),
+        _arg(dlogits, dlogits.dtype, "dlogits", (T, N), here), _raw_stream(here)), "moe_router_backward")
     return dlogits
 
 
-def _rng(rng, p):
+def _rng(rng, p, here):
     """Address of the {seed, offset} pair, an int64 tensor on the GPU."""
     if rng is None and p > 0:
         raise ValueError("dropout needs rng, an int64 tensor {seed, offset}")
-    return _opt(rng, torch.int64, "rng", (2,))
+    return _arg_opt(rng, torch.int64, "rng", (2,), here)
 
 
 def moe_combine_dropout(out_rows, slot_row, topk_gates, p=0.0, rng=None, residual=None,
@@ -654,16 +679,16 @@ def moe_combine_dropout(out_rows, slot_row, topk_gates, p=0.0, rng=None, residua
     """moe_combine with dropout (probability p, mask from rng = int64 [2]
     {seed, offset}) and a residual."""
     T, k = slot_row.shape
-    H = out_rows.shape[1]
+    H, d = out_rows.shape[1], out_rows.dtype
+    dt, here = _elem(d), _here(out_rows, "out_rows")
     if y is None:
-        y = _empty((T, H), out_rows.dtype, out_rows)
-    args = (_dev(out_rows, out_rows.dtype, "out_rows", (T * k, H)),
-            _dev(slot_row, torch.int32, "slot_row"),
-            _dev(topk_gates, torch.float32, "topk_gates", (T, k)),
-            _opt(residual, out_rows.dtype, "residual", (T, H)), float(p), _rng(rng, p),
-            T, k, H, _elem(out_rows.dtype), _dev(y, out_rows.dtype, "y", (T, H)))
-    _one_device(out_rows, slot_row, topk_gates, residual, rng, y)
-    _check(_lib.moe_combine_dropout(*args, _stream()), "moe_combine_dropout")
+        y = _empty((T, H), d, out_rows)
+    _check(_lib.moe_combine_dropout(
+        _arg(out_rows, d, "out_rows", (T * k, H), here),
+        _arg(slot_row, torch.int32, "slot_row", (T, k), here),
+        _arg(topk_gates, torch.float32, "topk_gates", (T, k), here),
+        _arg_opt(residual, d, "residual", (T, H), here), p, _rng(rng, p, here), T, k, H, dt,
+        _arg(y, d, "y", (T, H), here), _raw_stream(here)), "moe_combine_dropout")
     return y
 
 
@@ -672,17 +697,17 @@ def moe_combine_backward(dy, out_rows, slot_row, topk_gates, p=0.0, rng=None,
     """Fills those of d_out_rows [T*k,H] (rows that a slot names) and d_gates
     [T,k] that are given with the gradients of moe_combine_dropout."""
     T, k = slot_row.shape
-    H = out_rows.shape[1]
+    H, d = out_rows.shape[1], out_rows.dtype
     if d_out_rows is None and d_gates is None:
         raise ValueError("no gradient asked for")
-    dt = out_rows.dtype
-    args = (_dev(dy, dt, "dy", (T, H)), _dev(out_rows, dt, "out_rows", (T * k, H)),
-            _dev(slot_row, torch.int32, "slot_row"),
-            _dev(topk_gates, torch.float32, "topk_gates", (T, k)), float(p), _rng(rng, p),
-            T, k, H, _elem(dt), _opt(d_out_rows, dt, "d_out_rows", (T * k, H)),
-            _opt(d_gates, torch.float32, "d_gates", (T, k)))
-    _one_device(out_rows, dy, slot_row, topk_gates, rng, d_out_rows, d_gates)
-    _check(_lib.moe_combine_backward(*args, _stream()), "moe_combine_backward")
+    dt, here = _elem(d), _here(out_rows, "out_rows")
+    _check(_lib.moe_combine_backward(
+        _arg(dy, d, "dy", (T, H), here), _arg(out_rows, d, "out_rows", (T * k, H), here),
+        _arg(slot_row, torch.int32, "slot_row", (T, k), here),
+        _arg(topk_gates, torch.float32, "topk_gates", (T, k), here), p, _rng(rng, p, here), T, k,
+        H, dt, _arg_opt(d_out_rows, d, "d_out_rows", (T * k, H), here),
+        _arg_opt(d_gates, torch.float32, "d_gates", (T, k), here), _raw_stream(here)),
+        "moe_combine_backward")
     return d_out_rows, d_gates
 
 

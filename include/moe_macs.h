@@ -570,7 +570,7 @@ int moe_linear_backward(const void* dy, const void* x, const void* w,
  *                       moe_router_backward.
  * n == 0 (T == 0 too) gives zeros.  Sums over tokens are taken in fp64 in a
  * fixed order.  Workspace of moe_balance_workspace_size(T, N) bytes, at a
- * multiple of 8 bytes (scratch only; no initialisation).
+ * multiple of 16 bytes (scratch only; no initialisation).
  */
 size_t moe_balance_workspace_size(int T, int N);
 int moe_balance_loss(const float* logits, const int32_t* slot_ids,

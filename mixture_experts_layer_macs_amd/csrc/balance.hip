@@ -42,24 +42,48 @@ __device__ __forceinline__ float group_max(float v) {
   return group_reduce<float, GL>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// Partial sums of one workgroup, in the workspace.
+// Partial sums of the workgroups, in the workspace, and the outputs.
 struct Part {
   double* zsq;     // [G]
+  float* prob;     // [G][pitch], zeros behind column N
+  int32_t* count;  // [G][pitch]
   int32_t* n;      // [G]
-  float* prob;     // [G][N]
-  int32_t* count;  // [G][N]
   float *losses, *mean_prob;
   int32_t* counts;
-  int G, N, k;
+  int G, N, k, pitch;  // pitch: N rounded up to 4
 };
 
-// The workgroups' sums to the outputs: a thread owns a column in every R-th
-// partial row, 8 rows in flight.
-__device__ __forceinline__ void finish(const Part& p) {
-  __shared__ double s_p[NTHR];
-  __shared__ int s_c[NTHR];
-  __shared__ double s_dot[WAVES], s_z;
+// The losses from sum_j c_j P_j (dot), sum_t lse^2 and n.
+__device__ __forceinline__ void write_losses(const Part& p, double dot, double zsq, int n) {
+  const double inv = n > 0 ? 1.0 / n : 0.0;
+  p.losses[0] = static_cast<float>(dot * inv * p.N / p.k);
+  p.losses[1] = static_cast<float>(zsq * inv);
+  p.counts[p.N] = n;
+}
+
+// Sum of one value per thread of the workgroup, in thread 0.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+  v = wave_sum_f64(v);
+  __syncthreads();
+  if (lane_id() == 0) red[threadIdx.x / MOE_WAVE] = v;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < WAVES; ++w) s += red[w];
+  return s;
+}
+
+// The workgroups' sums to the outputs, one workgroup: a thread owns four
+// columns of every R-th partial row, 8 rows in flight.  What it reads was
+// written on other XCDs, so a dependent round costs a trip to memory (one
+// column per thread and as many rounds took 23 us at G = N = 256).
+__global__ __launch_bounds__(NTHR) void finish_kernel(Part p) {
+  __shared__ double s_p[NTHR][4];
+  __shared__ int s_c[NTHR][4];
+  __shared__ double red[WAVES], s_z;
   __shared__ int s_n;
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
   const int tid = threadIdx.x;
   if (tid < MOE_WAVE) {
     int n = 0;
@@ -75,63 +99,61 @@ __device__ __forceinline__ void finish(const Part& p) {
       s_z = z;
     }
   }
-  int cols = 32;  // threads along the columns: a power of two that covers N
-  while (cols < p.N) cols *= 2;
-  const int R = NTHR / cols, c = tid & (cols - 1), r = tid / cols;
-  double sum = 0.0;
-  int count = 0;
+  int quads = 4;  // threads along the columns: a power of two that covers N / 4
+  while (quads * 4 < p.N) quads *= 2;
+  const int R = NTHR / quads, c = (tid & (quads - 1)) * 4, r = tid / quads;
+  double sum[4] = {};
+  int count[4] = {};
   if (c < p.N) {
     for (int g0 = r; g0 < p.G; g0 += 8 * R) {
-      float f[8];
-      int m[8];
+      f32x4 f[8];
+      i32x4 m[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int g = g0 + u * R;
-        f[u] = g < p.G ? p.prob[static_cast<size_t>(g) * p.N + c] : 0.f;
-        m[u] = g < p.G ? p.count[static_cast<size_t>(g) * p.N + c] : 0;
+        const size_t at = static_cast<size_t>(min(g0 + u * R, p.G - 1)) * p.pitch + c;
+        f[u] = *reinterpret_cast<const f32x4*>(p.prob + at);
+        m[u] = *reinterpret_cast<const i32x4*>(p.count + at);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        sum += f[u];
-        count += m[u];
+        const bool in = g0 + u * R < p.G;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i] += in ? f[u][i] : 0.f;
+          count[i] += in ? m[u][i] : 0;
+        }
       }
     }
   }
-  s_p[tid] = sum;
-  s_c[tid] = count;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s_p[tid][i] = sum[i];
+    s_c[tid][i] = count[i];
+  }
   __syncthreads();
   const int n = s_n;
   const double inv = n > 0 ? 1.0 / n : 0.0;
   double dot = 0.0;
   if (tid < p.N) {
-    sum = 0.0;
-    count = 0;
+    double v = 0.0;
+    int m = 0;
     for (int i = 0; i < R; ++i) {  // the same order every time
-      sum += s_p[i * cols + tid];
-      count += s_c[i * cols + tid];
+      v += s_p[i * quads + tid / 4][tid % 4];
+      m += s_c[i * quads + tid / 4][tid % 4];
     }
-    sum *= inv;
-    p.counts[tid] = count;
-    p.mean_prob[tid] = static_cast<float>(sum);
-    dot = sum * count;
+    v *= inv;
+    p.counts[tid] = m;
+    p.mean_prob[tid] = static_cast<float>(v);
+    dot = v * m;
   }
-  dot = wave_sum_f64(dot);
-  if (lane_id() == 0) s_dot[tid / MOE_WAVE] = dot;
-  __syncthreads();
-  if (tid == 0) {
-    double d = 0.0;
-    for (int w = 0; w < WAVES; ++w) d += s_dot[w];
-    p.losses[0] = static_cast<float>(d * inv * p.N / p.k);
-    p.losses[1] = static_cast<float>(s_z * inv);
-    p.counts[p.N] = n;
-  }
+  dot = block_sum(dot, red);
+  if (tid == 0) write_losses(p, dot, s_z, n);
 }
 
-__global__ __launch_bounds__(NTHR) void finish_kernel(Part p) { finish(p); }
-
 // A row whose logits are all -inf has no probabilities: it counts as a token
-// and adds nothing else.  The next token's logits are requested before the
-// current one is worked on.
+// and adds nothing else.  The logits of the next D tokens are in flight while
+// one is worked on: a short batch is a chain of memory latencies otherwise
+// (one token ahead took 10.8 us for 128 tokens, 128 experts).
 template <int GL, int KPL>
 __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ logits,
                                                     const int32_t* __restrict__ ids,
@@ -146,7 +168,8 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
   const int lane = lane_id(), wave = threadIdx.x / MOE_WAVE, gl = lane & (GL - 1);
   for (int j = threadIdx.x; j < N; j += NTHR) s_count[j] = 0;
   __syncthreads();
-  float pf[KPL], znext[KPL];
+  constexpr int D = KPL <= 4 ? 4 : KPL <= 8 ? 2 : 1;
+  float pf[KPL], znext[D][KPL];
   double pd[KPL];
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
@@ -154,29 +177,26 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
     pd[i] = 0.0;
   }
   double zsq = 0.0;
-  int n = 0, since = 0, idnext = -1;
-  bool onnext = false;
+  int n = 0, since = 0, idnext[D];
+  uint8_t onnext[D];
   const int step = gridDim.x * WAVES * TPW;
-  auto request = [&](int t) {
-    const bool in = t < T;
-    onnext = in && (mask == nullptr || mask[t] != 0);
+  auto request = [&](int t, int d) {
+    const int u = min(t, T - 1);  // past the end: a token that is not used
+    onnext[d] = mask ? mask[u] : 1;
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
       const int j = gl + GL * i;
-      znext[i] = in && j < N ? logits[static_cast<size_t>(t) * N + j] : -INFINITY;
+      znext[d][i] = logits[static_cast<size_t>(u) * N + min(j, N - 1)];
     }
-    idnext = in && gl < k ? ids[static_cast<size_t>(t) * k + gl] : -1;
+    idnext[d] = gl < k ? ids[static_cast<size_t>(u) * k + gl] : -1;
   };
-  const int t0 = (blockIdx.x * WAVES + wave) * TPW;
-  request(t0 + lane / GL);
-  for (int tb = t0; tb < T; tb += step) {
-    const int t = tb + lane / GL;
+  auto work = [&](int t, int d) {
     float z[KPL], top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) z[i] = znext[i];
-    int id = idnext;
-    const bool on = onnext;
-    request(t + step);
+    for (int i = 0; i < KPL; ++i) z[i] = gl + GL * i < N ? znext[d][i] : -INFINITY;
+    int id = idnext[d];
+    const bool on = t < T && onnext[d] != 0;
+    request(t + D * step, d);
 #pragma unroll
     for (int i = 0; i < KPL; ++i) top = fmaxf(top, z[i]);
     if (on) {
@@ -210,6 +230,14 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
         pf[i] = 0.f;
       }
     }
+  };
+  const int t0 = (blockIdx.x * WAVES + wave) * TPW + lane / GL;
+  if (T > 0) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) request(t0 + d * step, d);
+    for (int tb = t0 - lane / GL; tb < T; tb += D * step)
+#pragma unroll
+      for (int d = 0; d < D; ++d) work(tb + lane / GL + d * step, d);
   }
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
@@ -222,8 +250,19 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
     s_z[wave] = zsq;
     s_n[wave] = n;
   }
+  __syncthreads();
+  double zall = 0.0;
+  int nall = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    zall += s_z[w];
+    nall += s_n[w];
+  }
+  const bool alone = gridDim.x == 1;  // a short batch: one workgroup, one launch
+  const double invn = nall > 0 ? 1.0 / nall : 0.0;
   const size_t g = blockIdx.x;
   constexpr int PER = COLS / GL;  // registers of a wave per round
+  double dot = 0.0;
 #pragma unroll
   for (int i0 = 0; i0 < KPL; i0 += PER) {
     __syncthreads();
@@ -232,27 +271,26 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
       if (lane < GL) s_prob[wave][(i - i0) * GL + gl] = pd[i];
     __syncthreads();
     const int j = i0 * GL + threadIdx.x;
-    if (threadIdx.x < COLS && j < N && threadIdx.x < (KPL - i0) * GL) {
-      double v = 0.0;
+    if (threadIdx.x >= COLS || threadIdx.x >= (KPL - i0) * GL || j >= part.pitch) continue;
+    double v = 0.0;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) v += s_prob[w][threadIdx.x];
-      part.prob[g * N + j] = static_cast<float>(v);
-      part.count[g * N + j] = s_count[j];
+    for (int w = 0; w < WAVES; ++w) v += s_prob[w][threadIdx.x];
+    const int c = j < N ? s_count[j] : 0;
+    if (alone && j < N) {
+      part.mean_prob[j] = static_cast<float>(v * invn);
+      part.counts[j] = c;
+      dot += v * invn * c;
+    } else if (!alone) {
+      part.prob[g * part.pitch + j] = j < N ? static_cast<float>(v) : 0.f;
+      part.count[g * part.pitch + j] = c;
     }
   }
-  if (threadIdx.x == 0) {
-    double z = 0.0;
-    int m = 0;
-    for (int w = 0; w < WAVES; ++w) {
-      z += s_z[w];
-      m += s_n[w];
-    }
-    part.zsq[g] = z;
-    part.n[g] = m;
-  }
-  if (gridDim.x == 1) {  // a short batch: one workgroup, one launch
-    __syncthreads();
-    finish(part);
+  if (alone) {
+    dot = block_sum(dot, s_z);
+    if (threadIdx.x == 0) write_losses(part, dot, zall, nall);
+  } else if (threadIdx.x == 0) {
+    part.zsq[g] = zall;
+    part.n[g] = nall;
   }
 }
 
@@ -261,10 +299,8 @@ __device__ __forceinline__ void store_elem(__bf16* p, float v) { *p = static_cas
 
 constexpr int GNTHR = 256, GWAVES = GNTHR / MOE_WAVE;
 
-// With GL == 64 the token's slots are the same for the whole wave: ids and
-// gate gradients come through scalar registers, and a slot touches the one
-// register that holds its expert.  (Comparing every slot with every register
-// made this kernel VALU bound: 38 us at 65521 x 256 against 28 us of traffic.)
+// Slot q of a token sits in lane q of its group.  With GL == 64 a slot is read
+// into scalar registers and touches only the register that holds its expert.
 template <int GL, int KPL, typename E>
 __global__ __launch_bounds__(GNTHR) void grad_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids,
@@ -285,23 +321,28 @@ __global__ __launch_bounds__(GNTHR) void grad_kernel(
   }
   const float zc = static_cast<float>(2.0 * dzl * inv);
   const int step = gridDim.x * GWAVES * TPW, t0 = (blockIdx.x * GWAVES + wave) * TPW;
-  float znext[KPL], lnext = 0.f;
-  bool onnext = false;
+  float znext[KPL], lnext, dgnext = 0.f;
+  int idnext = -1;
+  uint8_t onnext;
   auto request = [&](int t) {
-    const bool in = t < T;
-    onnext = in && (mask == nullptr || mask[t] != 0);
-    lnext = in ? lse[t] : 0.f;
+    const int u = min(t, T - 1);  // past the end: a token that is not used
+    onnext = mask ? mask[u] : 1;
+    lnext = lse[u];
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      const int j = gl + GL * i;
-      znext[i] = in && j < N ? logits[static_cast<size_t>(t) * N + j] : 0.f;
+    for (int i = 0; i < KPL; ++i)
+      znext[i] = logits[static_cast<size_t>(u) * N + min(gl + GL * i, N - 1)];
+    if (d_gates && gl < k) {
+      idnext = ids[static_cast<size_t>(u) * k + gl];
+      dgnext = d_gates[static_cast<size_t>(u) * k + gl];
     }
   };
   request(t0 + lane / GL);
   for (int tb = t0; tb < T; tb += step) {
     const int t = tb + lane / GL;
     const float l = lnext;
-    const bool on = onnext && l != -INFINITY;
+    const bool on = onnext != 0 && l != -INFINITY;
+    int id = idnext;
+    float dg = dgnext;
     float p[KPL], u[KPL];
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
@@ -311,24 +352,29 @@ __global__ __launch_bounds__(GNTHR) void grad_kernel(
     request(t + step);
     if (d_gates) {
       if constexpr (GL == MOE_WAVE) {
-        const int32_t* idp = ids + static_cast<size_t>(tb) * k;
-        const float* dgp = d_gates + static_cast<size_t>(tb) * k;
-        for (int q = 0; q < k; ++q) {
-          const int e = idp[q], r = e >> 6;
-          if (static_cast<unsigned>(e) >= static_cast<unsigned>(N)) continue;
-          const float d = lane == (e & 63) ? dgp[q] : 0.f;
-          if constexpr (KPL == 1) {
-            u[0] += r == 0 ? d : 0.f;
-          } else {
+        for (int s0 = 0; s0 < k; s0 += MOE_WAVE) {
+          if (s0 > 0) {  // more than 64 slots
+            const bool in = s0 + lane < k;
+            id = in ? ids[static_cast<size_t>(tb) * k + s0 + lane] : -1;
+            dg = in ? d_gates[static_cast<size_t>(tb) * k + s0 + lane] : 0.f;
+          }
+          const int m = min(MOE_WAVE, k - s0);
+          for (int q = 0; q < m; ++q) {
+            const int e = read_lane(id, q);
+            if (static_cast<unsigned>(e) >= static_cast<unsigned>(N)) continue;
+            const float d = __uint_as_float(read_lane(__float_as_uint(dg), q));
+            const float mine = lane == (e & 63) ? d : 0.f;
 #pragma unroll
             for (int i = 0; i < KPL; ++i)
-              if (r == i) u[i] += d;
+              if (KPL == 1 || (e >> 6) == i) u[i] += mine;
           }
         }
-      } else if (t < T) {
+      } else {  // k <= N <= GL
         for (int q = 0; q < k; ++q) {
-          const int e = ids[static_cast<size_t>(t) * k + q];
-          u[0] += e == gl && e < N ? d_gates[static_cast<size_t>(t) * k + q] : 0.f;
+          const int from = (lane & ~(GL - 1)) + q;
+          const int e = __shfl(id, from, MOE_WAVE);
+          const float d = __shfl(dg, from, MOE_WAVE);
+          u[0] += e == gl && e < N ? d : 0.f;
         }
       }
     }
@@ -370,7 +416,9 @@ inline int blocks(int T, int N) {
   return std::min(256, (T + 4 * tpb - 1) / (4 * tpb));
 }
 
-inline size_t part_bytes(int G, int N) { return static_cast<size_t>(G) * (N * 8 + 12) + 64; }
+inline size_t up4(int n) { return (static_cast<size_t>(n) + 3) & ~size_t(3); }
+
+inline size_t part_bytes(int G, int N) { return static_cast<size_t>(G) * (up4(N) * 8 + 12) + 64; }
 
 }  // namespace bal
 }  // namespace moe
@@ -391,13 +439,14 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* slot_ids,
   if (!losses || !counts || !mean_prob || !workspace) return MOE_EINVAL;
   if (T > 0 && (!logits || !slot_ids || !lse)) return MOE_EINVAL;
   const int G = blocks(T, N);
-  if (workspace_bytes < part_bytes(G, N) || reinterpret_cast<uintptr_t>(workspace) % 8 != 0)
+  if (workspace_bytes < part_bytes(G, N) || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
     return MOE_EINVAL;
   Part p;
-  p.zsq = static_cast<double*>(workspace);
+  p.pitch = static_cast<int>(up4(N));
+  p.prob = static_cast<float*>(workspace);
+  p.count = reinterpret_cast<int32_t*>(p.prob + static_cast<size_t>(G) * p.pitch);
+  p.zsq = reinterpret_cast<double*>(p.count + static_cast<size_t>(G) * p.pitch);
   p.n = reinterpret_cast<int32_t*>(p.zsq + G);
-  p.count = p.n + G;
-  p.prob = reinterpret_cast<float*>(p.count + static_cast<size_t>(G) * N);
   p.losses = losses;
   p.counts = counts;
   p.mean_prob = mean_prob;

@@ -67,11 +67,11 @@ struct Drop {
   float scale;
 };
 
-// f[i] *= m of element e + i, for V elements from e (a multiple of 4).  A
-// dropped element becomes 0 whatever it held.
+// Bit i: element e + i is kept, for V elements from e (a multiple of 4).
 template <int V>
-__device__ __forceinline__ void apply_mask(float* f, uint64_t e, uint64_t seed, uint64_t offset,
-                                           uint32_t threshold, float scale) {
+__device__ __forceinline__ uint32_t keep_bits(uint64_t e, uint64_t seed, uint64_t offset,
+                                              uint32_t threshold) {
+  uint32_t bits = 0;
 #pragma unroll
   for (int b = 0; b < V / 4; ++b) {
     const uint64_t ctr = e / 4 + b;
@@ -80,19 +80,28 @@ __device__ __forceinline__ void apply_mask(float* f, uint64_t e, uint64_t seed, 
     uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
-      const uint32_t h0 = __umulhi(0xD2511F53u, c0), l0 = 0xD2511F53u * c0;
-      const uint32_t h1 = __umulhi(0xCD9E8D57u, c2), l1 = 0xCD9E8D57u * c2;
-      c0 = h1 ^ c1 ^ k0;
-      c1 = l1;
-      c2 = h0 ^ c3 ^ k1;
-      c3 = l0;
+      // one 64-bit multiply-add gives both halves of a product
+      const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c0;
+      const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c2;
+      c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ k0;
+      c1 = static_cast<uint32_t>(p1);
+      c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ k1;
+      c3 = static_cast<uint32_t>(p0);
       k0 += 0x9E3779B9u;
       k1 += 0xBB67AE85u;
     }
     const uint32_t w[4] = {c0, c1, c2, c3};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[4 * b + i] = w[i] >= threshold ? f[4 * b + i] * scale : 0.f;
+    for (int i = 0; i < 4; ++i) bits |= w[i] >= threshold ? 1u << (4 * b + i) : 0u;
   }
+  return bits;
+}
+
+// f *= m; a dropped element becomes 0 whatever it held.
+template <int V>
+__device__ __forceinline__ void apply_mask(float* f, uint32_t bits, float scale) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = bits >> i & 1 ? f[i] * scale : 0.f;
 }
 
 template <typename D>
@@ -113,6 +122,9 @@ __global__ __launch_bounds__(NTHR) void forward_kernel(
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    const size_t e = static_cast<size_t>(t) * H + v * V;
+    uint4 rq = make_uint4(0, 0, 0, 0);
+    uint32_t keep = 0;
     for (int s0 = 0; s0 < k; s0 += SB) {
       int r[SB];
       float g[SB];
@@ -128,6 +140,10 @@ __global__ __launch_bounds__(NTHR) void forward_kernel(
       for (int u = 0; u < SB; ++u)
         if (r[u] >= 0)
           q[u] = *reinterpret_cast<const uint4*>(rows + static_cast<size_t>(r[u]) * H + v * V);
+      if (s0 == 0) {  // the mask is computed while the first rows are in flight
+        if (residual) rq = *reinterpret_cast<const uint4*>(residual + e);
+        if (drop.rng) keep = keep_bits<V>(e, seed, offset, drop.threshold);
+      }
 #pragma unroll
       for (int u = 0; u < SB; ++u) {
         if (r[u] < 0) continue;
@@ -137,11 +153,10 @@ __global__ __launch_bounds__(NTHR) void forward_kernel(
         for (int i = 0; i < V; ++i) acc[i] += g[u] * f[i];
       }
     }
-    const size_t e = static_cast<size_t>(t) * H + v * V;
-    if (drop.rng) apply_mask<V>(acc, e, seed, offset, drop.threshold, drop.scale);
+    if (drop.rng) apply_mask<V>(acc, keep, drop.scale);
     if (residual) {
       float f[V];
-      D::unpack(*reinterpret_cast<const uint4*>(residual + e), f);
+      D::unpack(rq, f);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] += f[i];
     }
@@ -193,7 +208,8 @@ __global__ __launch_bounds__(NTHR) void backward_kernel(
       const size_t e = static_cast<size_t>(t) * H + v * V;
       float d[V];
       D::unpack(*reinterpret_cast<const uint4*>(dy + e), d);
-      if (drop.rng) apply_mask<V>(d, e, seed, offset, drop.threshold, drop.scale);
+      if (drop.rng)
+        apply_mask<V>(d, keep_bits<V>(e, seed, offset, drop.threshold), drop.scale);
 #pragma unroll
       for (int u = 0; u < SB; ++u) {
         if (r[u] < 0) continue;

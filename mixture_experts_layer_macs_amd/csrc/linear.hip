@@ -11,66 +11,12 @@
 
 #include "common.h"
 #include "linear_common.h"
+#include "linear_f32.h"
 #include "linear_mma.h"
+#include "linear_skinny.h"
 
 namespace moe {
 namespace lin {
-
-// ------------------------------------------------------------ fp32 product
-// C[m][n] = sum_k A(m, k) B(n, k), A(m, k) = a[m * am + k * ak] and so on.
-struct Prod {
-  const float *a, *b;
-  long am, ak, bm, bk;
-  int M, N, K;
-  Epilogue e;
-};
-
-constexpr int TILE = 64, BK = 16, NTHR = 256;
-
-template <bool GLU>
-__global__ __launch_bounds__(NTHR) void product_f32_kernel(Prod p) {
-  __shared__ float sa[BK][TILE + 1], sb[GLU ? 2 : 1][BK][TILE + 1];
-  const int m0 = blockIdx.y * TILE, n0 = blockIdx.x * TILE;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[GLU ? 2 : 1][4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += BK) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < TILE * BK; i += NTHR) {
-      // consecutive threads along the operand's contiguous axis
-      const int am = p.ak == 1 ? i / BK : i % TILE, ak = p.ak == 1 ? i % BK : i / TILE;
-      const int bm = p.bk == 1 ? i / BK : i % TILE, bk = p.bk == 1 ? i % BK : i / TILE;
-      sa[ak][am] = m0 + am < p.M && k0 + ak < p.K ? p.a[(m0 + am) * p.am + (k0 + ak) * p.ak] : 0.f;
-#pragma unroll
-      for (int h = 0; h < (GLU ? 2 : 1); ++h)
-        sb[h][bk][bm] = n0 + bm < p.N && k0 + bk < p.K
-                            ? p.b[(h * static_cast<long>(p.N) + n0 + bm) * p.bm + (k0 + bk) * p.bk]
-                            : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < BK; ++kk)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int h = 0; h < (GLU ? 2 : 1); ++h)
-            acc[h][i][j] += sa[kk][ty * 4 + i] * sb[h][kk][tx * 4 + j];
-  }
-  const int n = n0 + tx * 4;
-  if (n >= p.N) return;
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + ty * 4 + i;
-    if (m < p.M) finish4<float, GLU>(p.e, m, n, p.N, acc[0][i], acc[GLU ? 1 : 0][i]);
-  }
-}
-
-inline int product(const Prod& p, bool glu, hipStream_t s) {
-  const dim3 grid((p.N + TILE - 1) / TILE, (p.M + TILE - 1) / TILE);
-  if (glu) hipLaunchKernelGGL(product_f32_kernel<true>, grid, dim3(NTHR), 0, s, p);
-  else hipLaunchKernelGGL(product_f32_kernel<false>, grid, dim3(NTHR), 0, s, p);
-  return MOE_OK;
-}
 
 // ------------------------------------------------------------ bf16 product
 template <bool RS, bool CS, int BM, int BN, int WM, int WN, bool GLU, bool PART, int WGS>
@@ -148,6 +94,44 @@ int product(Mma a, Plan p, float* part, hipStream_t s) {
   return MOE_OK;
 }
 
+// ------------------------------------------------------------ fp32 product
+inline Plan plan_f32(int M, int W, int K) {
+  Plan p;
+  const long large = static_cast<long>((M + 127) / 128) * ((W + 127) / 128);
+  p.tile = large * 4 >= cu_count() ? 128 : 32;
+  p.splits = 1;
+  if (p.tile == 128)
+    p.splits = static_cast<int>(std::max(1L, std::min<long>(K / 128, cu_count() / large)));
+  return p;
+}
+
+template <bool RS, bool CS, bool GLU>
+int product_f32(F32Prod a, float* part, hipStream_t s) {
+  const Plan p = plan_f32(a.M, GLU ? 2 * a.N : a.N, a.K);
+  if (p.tile == 32) {
+    hipLaunchKernelGGL((f32_small_kernel<RS, CS, GLU>), dim3((a.N + 31) / 32, (a.M + 31) / 32),
+                       dim3(256), 0, s, a);
+    return MOE_OK;
+  }
+  a.per_split = (a.K + p.splits - 1) / p.splits;
+  a.per_split = (a.per_split + 15) / 16 * 16;
+  const int splits = (a.K + a.per_split - 1) / a.per_split;
+  a.part = part;
+  const int nc = GLU && splits == 1 ? 64 : 128, N = a.N;
+  if (GLU && splits > 1) a.N *= 2;
+  const dim3 grid((a.N + nc - 1) / nc, (a.M + 127) / 128, splits);
+  if (splits == 1) {
+    hipLaunchKernelGGL((f32_large_kernel<RS, CS, GLU, false>), grid, dim3(256), 0, s, a);
+    return MOE_OK;
+  }
+  hipLaunchKernelGGL((f32_large_kernel<RS, CS, false, true>), grid, dim3(256), 0, s, a);
+  const size_t quads = static_cast<size_t>(a.M) * N / 4;
+  hipLaunchKernelGGL((join_kernel<float, GLU>), dim3((quads + 255) / 256), dim3(256), 0, s, part,
+                     splits, a.M, N, a.e);
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------- the choices
 inline Plan plan(int M, int W, int K) {
   Plan p;
   const long big = static_cast<long>((M + 255) / 256) * ((W + 255) / 256);
@@ -157,9 +141,22 @@ inline Plan plan(int M, int W, int K) {
   p.splits = static_cast<int>(std::max(1L, std::min<long>(std::min(16, slices / 4), cu_count() / std::max(1L, tiles))));
   return p;
 }
-inline size_t part_bytes(int M, int W, int K) {
-  const Plan p = plan(M, W, K);
+inline size_t part_bytes(int M, int W, int K, int dtype) {
+  const Plan p = dtype == MOE_BF16 ? plan(M, W, K) : plan_f32(M, W, K);
   return p.splits > 1 ? static_cast<size_t>(p.splits) * M * W * 4 : 0;
+}
+
+// A few tokens: weights straight to registers, no tile of 128 rows.
+inline bool is_skinny(int T, int dtype) { return dtype == MOE_BF16 && T <= 128; }
+
+template <bool GLU>
+int launch_skinny(const Skinny& p, hipStream_t s) {
+  const dim3 grid(GLU ? (p.O + 7) / 8 : (p.O + 15) / 16), block(SK_WAVES * MOE_WAVE);
+  if (p.T <= 16) hipLaunchKernelGGL((skinny_kernel<1, GLU>), grid, block, 0, s, p);
+  else if (p.T <= 32) hipLaunchKernelGGL((skinny_kernel<2, GLU>), grid, block, 0, s, p);
+  else if (p.T <= 64) hipLaunchKernelGGL((skinny_kernel<4, GLU>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((skinny_kernel<8, GLU>), grid, block, 0, s, p);
+  return MOE_OK;
 }
 
 // ------------------------------------------------ activation gradient, bias
@@ -276,8 +273,7 @@ inline BackPlan back_plan(int T, int K, int O, int act, int dtype) {
   p.sums = act == MOE_ACT_NONE ? 0 : up256(static_cast<size_t>(T) * W * elem_size(dtype));
   p.parts = p.sums + up256(static_cast<size_t>(p.blocks) * W * 4);
   p.bytes = p.parts + 256;
-  if (dtype == MOE_BF16 && T > 0)
-    p.bytes += std::max(part_bytes(T, K, W), part_bytes(W, K, T));
+  if (T > 0) p.bytes += std::max(part_bytes(T, K, W, dtype), part_bytes(W, K, T, dtype));
   return p;
 }
 
@@ -319,8 +315,8 @@ int backward(const void* dy, const void* x, const void* w, const void* z, int T,
     if (act != MOE_ACT_NONE) dz = ws + p.dz;
   }
   int rc = MOE_OK;
+  float* part = reinterpret_cast<float*>(ws + p.parts);
   if (dtype == MOE_BF16) {
-    float* part = reinterpret_cast<float*>(ws + p.parts);
     Mma q{};
     q.N = K;
     q.ldr = W;
@@ -341,24 +337,24 @@ int backward(const void* dy, const void* x, const void* w, const void* z, int T,
       rc = product<true, true, false>(q, plan(W, K, T), part, s);
     }
   } else {
-    Prod q{};
-    q.a = static_cast<const float*>(dz);
-    q.bm = 1;
-    q.bk = K;
+    F32Prod q{};
     q.N = K;
+    q.ldr = W;
+    q.ldc = K;
+    q.r = static_cast<const float*>(dz);
     if (dx) {
-      q.am = W; q.ak = 1;
-      q.b = static_cast<const float*>(w);
-      q.M = T; q.K = W;
+      q.c = static_cast<const float*>(w);
+      q.M = T;
+      q.K = W;
       q.e.y = dx;
-      rc = product(q, false, s);
+      rc = product_f32<false, true, false>(q, part, s);
     }
     if (dw && rc == MOE_OK) {
-      q.am = 1; q.ak = W;
-      q.b = static_cast<const float*>(x);
-      q.M = W; q.K = T;
+      q.c = static_cast<const float*>(x);
+      q.M = W;
+      q.K = T;
       q.e.y = dw;
-      rc = product(q, false, s);
+      rc = product_f32<true, true, false>(q, part, s);
     }
   }
   return rc == MOE_OK ? launch_status() : rc;
@@ -372,7 +368,8 @@ using namespace moe::lin;
 
 extern "C" size_t moe_linear_workspace_size(int T, int K, int O, int act, int dtype) {
   if (check(T, K, O, act, dtype) != MOE_OK) return 0;
-  return 256 + (dtype == MOE_BF16 && T > 0 ? part_bytes(T, width(O, act), K) : 0);
+  if (T == 0 || is_skinny(T, dtype)) return 256;
+  return 256 + part_bytes(T, width(O, act), K, dtype);
 }
 
 extern "C" int moe_linear(const void* x, const void* w, const void* bias, const void* residual,
@@ -388,8 +385,12 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
   hipStream_t s = as_stream(stream);
   const bool glu = act == MOE_ACT_SWIGLU;
   const Epilogue e{bias, residual, z, y, act};
+  float* part = static_cast<float*>(workspace);
   int r;
-  if (dtype == MOE_BF16) {
+  if (is_skinny(T, dtype)) {
+    const Skinny q{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), T, K, O, e};
+    r = glu ? launch_skinny<true>(q, s) : launch_skinny<false>(q, s);
+  } else if (dtype == MOE_BF16) {
     Mma q{};
     q.r = static_cast<const uint16_t*>(x);
     q.c = static_cast<const uint16_t*>(w);
@@ -398,20 +399,18 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
     q.N = O;
     q.K = K;
     q.e = e;
-    float* part = static_cast<float*>(workspace);
     const Plan p = plan(T, width(O, act), K);
     r = glu ? product<false, false, true>(q, p, part, s) : product<false, false, false>(q, p, part, s);
   } else {
-    Prod q{};
-    q.a = static_cast<const float*>(x);
-    q.b = static_cast<const float*>(w);
-    q.am = q.bm = K;
-    q.ak = q.bk = 1;
+    F32Prod q{};
+    q.r = static_cast<const float*>(x);
+    q.c = static_cast<const float*>(w);
+    q.ldr = q.ldc = K;
     q.M = T;
     q.N = O;
     q.K = K;
     q.e = e;
-    r = product(q, glu, s);
+    r = glu ? product_f32<false, false, true>(q, part, s) : product_f32<false, false, false>(q, part, s);
   }
   return r == MOE_OK ? launch_status() : r;
 }

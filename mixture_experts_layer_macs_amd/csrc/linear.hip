@@ -19,10 +19,10 @@ namespace moe {
 namespace lin {
 
 // ------------------------------------------------------------ bf16 product
-template <bool RS, bool CS, int BM, int BN, int WM, int WN, bool GLU, bool PART, int WGS>
+template <bool RS, bool CS, int BM, int BN, int WGS, bool GLU, bool PART>
 int launch_mma(const Mma& a, hipStream_t s) {
-  constexpr int lds = (2 * BM + 3 * BN) * SLICE * 2;
-  const void* fn = reinterpret_cast<const void*>(mma_kernel<RS, CS, BM, BN, WM, WN, GLU, PART, WGS>);
+  constexpr int lds = (SA * BM + SB * BN) * SLICE * 2;
+  const void* fn = reinterpret_cast<const void*>(mma_kernel<RS, CS, BM, BN, WGS, GLU, PART>);
   // the LDS limit is a per-device function attribute: set once per device
   static std::atomic<bool> attr_set[64];
   const int dev = current_device();
@@ -32,8 +32,8 @@ int launch_mma(const Mma& a, hipStream_t s) {
     if (dev >= 0) attr_set[dev].store(true, std::memory_order_release);
   }
   const int total = a.tm * a.tn * a.splits;
-  hipLaunchKernelGGL((mma_kernel<RS, CS, BM, BN, WM, WN, GLU, PART, WGS>), dim3((total + 7) / 8 * 8),
-                     dim3(WM * WN * MOE_WAVE), lds, s, a);
+  hipLaunchKernelGGL((mma_kernel<RS, CS, BM, BN, WGS, GLU, PART>), dim3((total + 7) / 8 * 8),
+                     dim3(W * MOE_WAVE), lds, s, a);
   return MOE_OK;
 }
 
@@ -47,6 +47,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   const int m = static_cast<int>(i / N), n = static_cast<int>(i % N);
   const size_t W = GLU ? 2 * static_cast<size_t>(N) : N;
   float g[4] = {}, u[4] = {};
+#pragma unroll 4
   for (int s = 0; s < splits; ++s) {
     const float* p = part + (static_cast<size_t>(s) * M + m) * W + n;
     float f[4];
@@ -59,29 +60,38 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
       for (int j = 0; j < 4; ++j) u[j] += f[j];
     }
   }
-  finish4<E, GLU>(e, m, n, N, g, u);
+  finish<E, GLU, 4>(e, m, n, N, g, u);
 }
 
 struct Plan {
-  int tile;    // edge of the square tile: 256 or 128
+  int tile;    // index into TILES (bf16), edge of the tile (fp32)
   int splits;  // of the reduction
 };
 
+struct Tile {
+  int m, n;
+};
+constexpr Tile TILES[] = {{256, 256}, {256, 192}, {192, 256}, {128, 128}};
+
 template <bool RS, bool CS, bool GLU, bool PART>
 int launch_tile(Mma& a, int tile, hipStream_t s) {
-  a.tm = (a.M + tile - 1) / tile;
-  const int nc = GLU ? tile / 2 : tile;
+  const Tile t = TILES[tile];
+  a.tm = (a.M + t.m - 1) / t.m;
+  const int nc = GLU ? t.n / 2 : t.n;
   a.tn = (a.N + nc - 1) / nc;
-  if (tile == 256) return launch_mma<RS, CS, 256, 256, 2, 4, GLU, PART, 1>(a, s);
-  return launch_mma<RS, CS, 128, 128, 2, 2, GLU, PART, 2>(a, s);
+  switch (tile) {
+    case 0: return launch_mma<RS, CS, 256, 256, 1, GLU, PART>(a, s);
+    case 1: return launch_mma<RS, CS, 256, 192, 1, GLU, PART>(a, s);
+    case 2: return launch_mma<RS, CS, 192, 256, 1, GLU, PART>(a, s);
+    default: return launch_mma<RS, CS, 128, 128, 2, GLU, PART>(a, s);
+  }
 }
 
 // Product with the plan's tile and splits; part: room for the partial sums.
 template <bool RS, bool CS, bool GLU>
 int product(Mma a, Plan p, float* part, hipStream_t s) {
-  const int slices = (a.K + SLICE - 1) / SLICE;
-  a.per_split = (slices + p.splits - 1) / p.splits;
-  a.splits = (slices + a.per_split - 1) / a.per_split;
+  a.per_split = ((a.K + p.splits - 1) / p.splits + 63) / 64 * 64;
+  a.splits = (a.K + a.per_split - 1) / a.per_split;
   a.part = part;
   if (a.splits == 1) return launch_tile<RS, CS, GLU, false>(a, p.tile, s);
   const int N = a.N;
@@ -132,14 +142,37 @@ int product_f32(F32Prod a, float* part, hipStream_t s) {
 }
 
 // ------------------------------------------------------------- the choices
+// Tile and splits of a bf16 product of M x W outputs: the least time by a
+// model fitted to 4 tiles and up to 16 splits of 50 shapes of all four operand
+// layouts (136 .. 8192 rows, 64 .. 14336 columns, reductions of 64 .. 8192; 9 %
+// rms off, its choice 2 % above the best of each shape in the mean).  Times in
+// us.  Large tiles take a CU each, in rounds: 1.32 per slice of a 256 x 256
+// tile and 8.6 for its output, in proportion to the area, and 3.5 to start;
+// 128 x 128 tiles, up to two on a CU at once, 0.45 per slice and 2.2 for the
+// output each.  Partial sums cost a launch and their traffic.
 inline Plan plan(int M, int W, int K) {
-  Plan p;
-  const long big = static_cast<long>((M + 255) / 256) * ((W + 255) / 256);
-  p.tile = big >= cu_count() / 2 ? 256 : 128;
-  const long tiles = p.tile == 256 ? big : static_cast<long>((M + 127) / 128) * ((W + 127) / 128);
-  const int slices = (K + SLICE - 1) / SLICE;
-  p.splits = static_cast<int>(std::max(1L, std::min<long>(std::min(16, slices / 4), cu_count() / std::max(1L, tiles))));
-  return p;
+  Plan best{3, 1};
+  double least = 1e30;
+  const long cus = cu_count();
+  for (int t = 0; t < 4; ++t) {
+    const long tiles = static_cast<long>((M + TILES[t].m - 1) / TILES[t].m) *
+                       ((W + TILES[t].n - 1) / TILES[t].n);
+    const double area = TILES[t].m * TILES[t].n / 65536.0;
+    for (int want = 1; want <= 8; ++want) {
+      const int per = ((K + want - 1) / want + 63) / 64, splits = (K + per * 64 - 1) / (per * 64);
+      if (splits != want) continue;
+      const double rounds = static_cast<double>((tiles * splits + cus - 1) / cus);
+      const double out = splits > 1 ? 0.63 : 1.0;  // partial sums are stored as they are
+      double us = t < 3 ? rounds * (per * 1.32 * area + 8.6 * area * out + 3.5)
+                        : rounds * (per * 0.45 + 2.2 * out) + 2.3;
+      if (splits > 1) us += 3.6 + static_cast<double>(splits) * M * W * (4 / 4.0e6);
+      if (us < least) {
+        least = us;
+        best = Plan{t, splits};
+      }
+    }
+  }
+  return best;
 }
 inline size_t part_bytes(int M, int W, int K, int dtype) {
   const Plan p = dtype == MOE_BF16 ? plan(M, W, K) : plan_f32(M, W, K);

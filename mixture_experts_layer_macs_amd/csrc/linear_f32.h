@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void f32_small_kernel(F32Prod p) {
     for (int i = 0; i < 4; ++i)
       v[h][i] = (red[h][0][row][col + i] + red[h][1][row][col + i]) +
                 (red[h][2][row][col + i] + red[h][3][row][col + i]);
-  finish4<float, GLU>(p.e, m0 + row, n0 + col, p.N, v[0], v[1]);
+  finish<float, GLU, 4>(p.e, m0 + row, n0 + col, p.N, v[0], v[1]);
 }
 
 // Large outputs: 128 x 128 tiles, 4 waves of 64 x 64, slices of 16 k through
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
         if constexpr (PART)
           store4(p.part + (static_cast<size_t>(blockIdx.z) * p.M + m) * p.N + n, g);
         else
-          finish4<float, GLU>(p.e, m, n, p.N, g, u);
+          finish<float, GLU, 4>(p.e, m, n, p.N, g, u);
       }
   }
 }

@@ -102,7 +102,7 @@ __global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
         if constexpr (GLU) u[j] += red[v][t][8 + c + j];
       }
     }
-    finish4<uint16_t, GLU>(p.e, t, n0 + c, p.O, g, u);
+    finish<uint16_t, GLU, 4>(p.e, t, n0 + c, p.O, g, u);
   }
 }
 

@@ -30,15 +30,16 @@ __device__ __forceinline__ T group_reduce(T v, Op op) {
   v = op(v, dpp_t<T, DPP_ROW_HALF_MIRROR>(v, v));
   if constexpr (GL > 8) v = op(v, dpp_t<T, 0x140>(v, v));  // lane 15-i of each row
   if constexpr (GL > 16) v = op(v, __shfl_xor(v, 16, MOE_WAVE));
-  if constexpr (GL > 32) v = op(v, __shfl_xor(v, 32, MOE_WAVE));
   return v;
 }
 template <int GL>
 __device__ __forceinline__ float group_sum(float v) {
+  if constexpr (GL == MOE_WAVE) return wave_sum(v);
   return group_reduce<float, GL>(v, [](float a, float b) { return a + b; });
 }
 template <int GL>
 __device__ __forceinline__ float group_max(float v) {
+  if constexpr (GL == MOE_WAVE) return wave_max(v);
   return group_reduce<float, GL>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
       sum += z[i];
     }
     sum = group_sum<GL>(sum);
-    const float inv = 1.f / sum, l = top + __logf(sum);
+    const float inv = __builtin_amdgcn_rcpf(sum), l = top + logf(sum);
 #pragma unroll
     for (int i = 0; i < KPL; ++i) pf[i] += some ? z[i] * inv : 0.f;  // padding may hold NaN
     if (gl == 0 && t < T) {
@@ -359,6 +360,7 @@ __global__ __launch_bounds__(GNTHR) void grad_kernel(
             dg = in ? d_gates[static_cast<size_t>(tb) * k + s0 + lane] : 0.f;
           }
           const int m = min(MOE_WAVE, k - s0);
+#pragma unroll 4
           for (int q = 0; q < m; ++q) {
             const int e = read_lane(id, q);
             if (static_cast<unsigned>(e) >= static_cast<unsigned>(N)) continue;

@@ -66,6 +66,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 struct Plan {
   int tile;    // index into TILES (bf16), edge of the tile (fp32)
   int splits;  // of the reduction
+  double us;   // estimate
 };
 
 struct Tile {
@@ -106,7 +107,7 @@ int product(Mma a, Plan p, float* part, hipStream_t s) {
 
 // ------------------------------------------------------------ fp32 product
 inline Plan plan_f32(int M, int W, int K) {
-  Plan p;
+  Plan p{};
   const long large = static_cast<long>((M + 127) / 128) * ((W + 127) / 128);
   p.tile = large * 4 >= cu_count() ? 128 : 32;
   p.splits = 1;
@@ -149,10 +150,10 @@ int product_f32(F32Prod a, float* part, hipStream_t s) {
 // us.  Large tiles take a CU each, in rounds: 1.32 per slice of a 256 x 256
 // tile and 8.6 for its output, in proportion to the area, and 3.5 to start;
 // 128 x 128 tiles, up to two on a CU at once, 0.45 per slice and 2.2 for the
-// output each.  Partial sums cost a launch and their traffic.
+// output each.  Partial sums cost a launch and their traffic; the column
+// operand streams at 4.5 TB/s at best.
 inline Plan plan(int M, int W, int K) {
-  Plan best{3, 1};
-  double least = 1e30;
+  Plan best{3, 1, 1e30};
   const long cus = cu_count();
   for (int t = 0; t < 4; ++t) {
     const long tiles = static_cast<long>((M + TILES[t].m - 1) / TILES[t].m) *
@@ -165,11 +166,9 @@ inline Plan plan(int M, int W, int K) {
       const double out = splits > 1 ? 0.63 : 1.0;  // partial sums are stored as they are
       double us = t < 3 ? rounds * (per * 1.32 * area + 8.6 * area * out + 3.5)
                         : rounds * (per * 0.45 + 2.2 * out) + 2.3;
+      us = std::max(us, static_cast<double>(W) * K * (2 / 4.5e6));
       if (splits > 1) us += 3.6 + static_cast<double>(splits) * M * W * (4 / 4.0e6);
-      if (us < least) {
-        least = us;
-        best = Plan{t, splits};
-      }
+      if (us < best.us) best = Plan{t, splits, us};
     }
   }
   return best;
@@ -179,28 +178,96 @@ inline size_t part_bytes(int M, int W, int K, int dtype) {
   return p.splits > 1 ? static_cast<size_t>(p.splits) * M * W * 4 : 0;
 }
 
-// A few tokens: weights straight to registers, no tile of 128 rows.
-inline bool is_skinny(int T, int dtype) { return dtype == MOE_BF16 && T <= 128; }
+// Few tokens: the skinny product or the tiles, whichever is estimated faster.
+// The skinny one is bound by its loads' addresses: a block of 64 k costs a
+// workgroup 0.25 us for the weights and 0.4 us for each 16 tokens (less for
+// rows that repeat), on top of 3 us, and the weights stream at 5.5 TB/s at
+// best (sweep of 7 weights of 256 x 4096 .. 14336 x 4096, 1 .. 512 tokens).
+// 768 x 2048: 3.9 us for 1 token, 6.1 for 128 (tiles: 9.6); 4096 x 14336: 24
+// for 1 token, but 145 for 128, where two splits of 128 x 128 tiles take 36.
+// Returns the fragments of 16 tokens per workgroup; 0: tiles.
+inline int skinny_plan(int T, int K, int W) {
+  int best = 0;
+  if (T > 128) return best;
+  double least = plan(T, W, K).us;
+  for (int rf = 1; rf <= 8; rf *= 2) {
+    if (rf > 1 && T <= rf * 8) break;  // half the fragments would be empty
+    const double wgs = static_cast<double>((W + 15) / 16) * ((T + rf * 16 - 1) / (rf * 16));
+    const double turns = std::max(1.0, wgs / cu_count()) * K / 512.0;
+    const double full = 0.25 + 0.75 * std::min(1.0, T / (16.0 * rf));
+    const double us = 3.0 + std::max(turns * 0.25, static_cast<double>(W) * K * (2 / 5.5e6)) +
+                      turns * 0.4 * rf * full;
+    if (us < least) {
+      least = us;
+      best = rf;
+    }
+  }
+  return best;
+}
 
 template <bool GLU>
-int launch_skinny(const Skinny& p, hipStream_t s) {
-  const dim3 grid(GLU ? (p.O + 7) / 8 : (p.O + 15) / 16), block(SK_WAVES * MOE_WAVE);
-  if (p.T <= 16) hipLaunchKernelGGL((skinny_kernel<1, GLU>), grid, block, 0, s, p);
-  else if (p.T <= 32) hipLaunchKernelGGL((skinny_kernel<2, GLU>), grid, block, 0, s, p);
-  else if (p.T <= 64) hipLaunchKernelGGL((skinny_kernel<4, GLU>), grid, block, 0, s, p);
+int launch_skinny(Skinny p, int rf, hipStream_t s) {
+  p.panels = GLU ? (p.O + 7) / 8 : (p.O + 15) / 16;
+  p.parts = (p.T + rf * 16 - 1) / (rf * 16);
+  const dim3 grid((p.panels * p.parts + 7) / 8 * 8), block(SK_WAVES * MOE_WAVE);
+  if (rf == 1) hipLaunchKernelGGL((skinny_kernel<1, GLU>), grid, block, 0, s, p);
+  else if (rf == 2) hipLaunchKernelGGL((skinny_kernel<2, GLU>), grid, block, 0, s, p);
+  else if (rf == 4) hipLaunchKernelGGL((skinny_kernel<4, GLU>), grid, block, 0, s, p);
   else hipLaunchKernelGGL((skinny_kernel<8, GLU>), grid, block, 0, s, p);
   return MOE_OK;
 }
 
 // ------------------------------------------------ activation gradient, bias
-// dz (rounded to the element type, the operand of both products) and, per
-// block of token rows, the fp32 column sums of the unrounded dz.  A thread
-// owns 16 bytes of dy's columns in every eighth row of the block; bound by
-// HBM: dy and z read, dz written once.
+// dz of V consecutive columns from dy and z, in fp32.  GLU: g ends as the gate
+// half and up as the up half.
+template <typename E, int V>
+__device__ __forceinline__ void act_grad(const E* dy, const E* z, int O, int act, float* g,
+                                         float* up) {
+  load_v<V>(dy, g);
+  if (act == MOE_ACT_NONE) return;
+  float a[V];
+  load_v<V>(z, a);
+  if (act == MOE_ACT_SWIGLU) {
+    load_v<V>(z + O, up);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float sg = sigmoid(a[i]), d = g[i] * a[i] * sg;
+      g[i] = g[i] * up[i] * (sg * (1.f + a[i] * (1.f - sg)));
+      up[i] = d;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] *= act_slope(act, a[i]);
+  }
+}
+
+// dz rounded to the element type, the operand of both products: 16 bytes of
+// dy's columns per thread.  Bound by HBM: dy and z read, dz written once.
+template <typename D>
+__global__ __launch_bounds__(256) void act_grad_kernel(const typename D::elem* __restrict__ dy,
+                                                       const typename D::elem* __restrict__ z,
+                                                       int T, int O, int act,
+                                                       typename D::elem* __restrict__ dz) {
+  constexpr int V = D::V;
+  const unsigned cols = O / V;
+  const size_t n = static_cast<size_t>(T) * cols, step = gridDim.x * static_cast<size_t>(256);
+  const bool glu = act == MOE_ACT_SWIGLU;
+  for (size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; i < n; i += step) {
+    const unsigned t = i / cols, o = (i - static_cast<size_t>(t) * cols) * V;
+    const size_t zr = static_cast<size_t>(t) * (glu ? 2 * O : O) + o;
+    float g[V], up[V];
+    act_grad<typename D::elem, V>(dy + i * V, z + zr, O, act, g, up);
+    store_v<V>(dz + zr, g);
+    if (glu) store_v<V>(dz + zr + O, up);
+  }
+}
+
+// The same with, per block of token rows, the fp32 column sums of the unrounded
+// dz: a thread owns 16 bytes of dy's columns in every eighth row of the block.
 constexpr int COLT = 32, ROWT = 8;  // threads along the columns and the rows
 
 template <typename D>
-__global__ __launch_bounds__(COLT * ROWT) void act_grad_kernel(
+__global__ __launch_bounds__(COLT * ROWT) void act_grad_sum_kernel(
     const typename D::elem* __restrict__ dy, const typename D::elem* __restrict__ z, int T, int O,
     int act, int rows, typename D::elem* __restrict__ dz, float* __restrict__ part) {
   constexpr int V = D::V;
@@ -213,33 +280,16 @@ __global__ __launch_bounds__(COLT * ROWT) void act_grad_kernel(
   const int t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
   for (int t = live ? t0 + ry : t1; t < t1; t += ROWT) {
     const size_t zr = static_cast<size_t>(t) * W + o;
+    float g[V], up[V];
+    act_grad<typename D::elem, V>(dy + static_cast<size_t>(t) * O + o, z + zr, O, act, g, up);
+    if (act != MOE_ACT_NONE) store_v<V>(dz + zr, g);
+    if (glu) store_v<V>(dz + zr + O, up);
 #pragma unroll
-    for (int h = 0; h < V; h += 4) {
-      float g[4], a[4], b[4];
-      load4(dy + static_cast<size_t>(t) * O + o + h, g);
-      if (act != MOE_ACT_NONE) load4(z + zr + h, a);
-      if (glu) {
-        load4(z + zr + O + h, b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float sg = sigmoid(a[i]);
-          const float up = g[i] * a[i] * sg;
-          g[i] = g[i] * b[i] * (sg * (1.f + a[i] * (1.f - sg)));
-          b[i] = up;
-        }
-        store4(dz + zr + O + h, b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s1[h + i] += b[i];
-      } else if (act != MOE_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) g[i] *= act_slope(act, a[i]);
-      }
-      if (act != MOE_ACT_NONE) store4(dz + zr + h, g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s0[h + i] += g[i];
+    for (int i = 0; i < V; ++i) {
+      s0[i] += g[i];
+      if (glu) s1[i] += up[i];
     }
   }
-  if (!part) return;
   for (int half = 0; half < (glu ? 2 : 1); ++half) {
     __syncthreads();
 #pragma unroll
@@ -272,13 +322,19 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float* __restrict__
 
 template <typename E>
 __global__ void zero_kernel(E* p, size_t n) {
-  const size_t i = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x;
-  if (i < n) store1(p + i, 0.f);
+  const size_t step = gridDim.x * static_cast<size_t>(256);
+  for (size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; i < n; i += step)
+    store1(p + i, 0.f);
 }
 
 // --------------------------------------------------------------------- host
 inline size_t elem_size(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 inline size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+// Workgroups of 256 threads for n items; kernels loop over what is left beyond
+// 2^22 of them (a grid holds fewer than 2^32 threads).
+inline dim3 grid_of(size_t n) {
+  return dim3(static_cast<unsigned>(std::min<size_t>((n + 255) / 256, size_t(1) << 22)));
+}
 inline int width(int O, int act) { return act == MOE_ACT_SWIGLU ? 2 * O : O; }
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -311,17 +367,22 @@ inline BackPlan back_plan(int T, int K, int O, int act, int dtype) {
 }
 
 template <typename D>
-int act_grad(const void* dy, const void* z, int T, int O, int act, const BackPlan& p, void* dz,
-             float* sums, void* dbias, hipStream_t s) {
+void launch_act_grad(const void* dy, const void* z, int T, int O, int act, const BackPlan& p,
+                     void* dz, float* sums, void* dbias, hipStream_t s) {
   typedef typename D::elem E;
   const int W = width(O, act);
-  hipLaunchKernelGGL(act_grad_kernel<D>, dim3((O + COLT * D::V - 1) / (COLT * D::V), p.blocks),
+  if (!dbias) {
+    const size_t chunks = static_cast<size_t>(T) * (O / D::V);
+    hipLaunchKernelGGL(act_grad_kernel<D>, grid_of(chunks), dim3(256), 0, s,
+                       static_cast<const E*>(dy), static_cast<const E*>(z), T, O, act,
+                       static_cast<E*>(dz));
+    return;
+  }
+  hipLaunchKernelGGL(act_grad_sum_kernel<D>, dim3((O + COLT * D::V - 1) / (COLT * D::V), p.blocks),
                      dim3(COLT * ROWT), 0, s, static_cast<const E*>(dy), static_cast<const E*>(z),
                      T, O, act, p.rows, static_cast<E*>(dz), sums);
-  if (dbias)
-    hipLaunchKernelGGL(bias_sum_kernel<E>, dim3((W + 63) / 64), dim3(256), 0, s, sums, p.blocks, W,
-                       static_cast<E*>(dbias));
-  return MOE_OK;
+  hipLaunchKernelGGL(bias_sum_kernel<E>, dim3((W + 63) / 64), dim3(256), 0, s, sums, p.blocks, W,
+                     static_cast<E*>(dbias));
 }
 
 template <typename D>
@@ -333,18 +394,18 @@ int backward(const void* dy, const void* x, const void* w, const void* z, int T,
     if (!dw && !dbias) return MOE_OK;
     const size_t nw = static_cast<size_t>(W) * K;
     if (dw)
-      hipLaunchKernelGGL(zero_kernel<E>, dim3((nw + 255) / 256), dim3(256), 0, s,
+      hipLaunchKernelGGL(zero_kernel<E>, grid_of(nw), dim3(256), 0, s,
                          static_cast<E*>(dw), nw);
     if (dbias)
-      hipLaunchKernelGGL(zero_kernel<E>, dim3((W + 255) / 256), dim3(256), 0, s,
+      hipLaunchKernelGGL(zero_kernel<E>, grid_of(W), dim3(256), 0, s,
                          static_cast<E*>(dbias), static_cast<size_t>(W));
     return launch_status();
   }
   const BackPlan p = back_plan(T, K, O, act, dtype);
   const void* dz = dy;
   if ((act != MOE_ACT_NONE && (dx || dw)) || dbias) {
-    float* sums = dbias ? reinterpret_cast<float*>(ws + p.sums) : nullptr;
-    act_grad<D>(dy, z, T, O, act, p, ws + p.dz, sums, dbias, s);
+    launch_act_grad<D>(dy, z, T, O, act, p, ws + p.dz, reinterpret_cast<float*>(ws + p.sums), dbias,
+                       s);
     if (act != MOE_ACT_NONE) dz = ws + p.dz;
   }
   int rc = MOE_OK;
@@ -401,7 +462,7 @@ using namespace moe::lin;
 
 extern "C" size_t moe_linear_workspace_size(int T, int K, int O, int act, int dtype) {
   if (check(T, K, O, act, dtype) != MOE_OK) return 0;
-  if (T == 0 || is_skinny(T, dtype)) return 256;
+  if (T == 0 || (dtype == MOE_BF16 && skinny_plan(T, K, width(O, act)))) return 256;
   return 256 + part_bytes(T, width(O, act), K, dtype);
 }
 
@@ -419,10 +480,11 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
   const bool glu = act == MOE_ACT_SWIGLU;
   const Epilogue e{bias, residual, z, y, act};
   float* part = static_cast<float*>(workspace);
+  const int rf = dtype == MOE_BF16 ? skinny_plan(T, K, width(O, act)) : 0;
   int r;
-  if (is_skinny(T, dtype)) {
-    const Skinny q{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), T, K, O, e};
-    r = glu ? launch_skinny<true>(q, s) : launch_skinny<false>(q, s);
+  if (rf) {
+    const Skinny q{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), T, K, O, 0, 0, e};
+    r = glu ? launch_skinny<true>(q, rf, s) : launch_skinny<false>(q, rf, s);
   } else if (dtype == MOE_BF16) {
     Mma q{};
     q.r = static_cast<const uint16_t*>(x);

@@ -21,7 +21,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 struct Skinny {
   const uint16_t *x, *w;
-  int T, K, O;  // O: columns of y
+  int T, K, O;        // O: columns of y
+  int panels, parts;  // weight panels, parts of the tokens
   Epilogue e;
 };
 
@@ -34,7 +35,11 @@ __global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
   __shared__ float red[SK_WAVES][RF * 16][17];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
-  const int n0 = blockIdx.x * NC, r = lane & 15, k_lane = (lane >> 4) * 8;
+  const int total = p.panels * p.parts, per = (total + 7) / 8;
+  const int id = blockIdx.x % 8 * per + blockIdx.x / 8;
+  if (id >= total) return;
+  const int n0 = id / p.parts * NC, t0 = id % p.parts * RF * 16;
+  const int r = lane & 15, k_lane = (lane >> 4) * 8;
   // rows past the end repeat the last one; their results are not stored
   const int wr = GLU ? (r < 8 ? min(n0 + r, p.O - 1) : p.O + min(n0 + r - 8, p.O - 1))
                      : min(n0 + r, p.O - 1);
@@ -42,7 +47,7 @@ __global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
   const uint16_t* x[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f)
-    x[f] = p.x + static_cast<size_t>(min(f * 16 + r, p.T - 1)) * p.K + k_lane;
+    x[f] = p.x + static_cast<size_t>(min(t0 + f * 16 + r, p.T - 1)) * p.K + k_lane;
   f32x4 acc[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) acc[f] = f32x4{0, 0, 0, 0};
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
   constexpr int QUADS = NC / 4;
   for (int i = threadIdx.x; i < RF * 16 * QUADS; i += SK_WAVES * MOE_WAVE) {
     const int t = i / QUADS, c = i % QUADS * 4;
-    if (t >= p.T || n0 + c >= p.O) continue;
+    if (t0 + t >= p.T || n0 + c >= p.O) continue;
     float g[4], u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -102,7 +107,7 @@ __global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
         if constexpr (GLU) u[j] += red[v][t][8 + c + j];
       }
     }
-    finish<uint16_t, GLU, 4>(p.e, t, n0 + c, p.O, g, u);
+    finish<uint16_t, GLU, 4>(p.e, t0 + t, n0 + c, p.O, g, u);
   }
 }
 

@@ -92,24 +92,30 @@ __global__ __launch_bounds__(256) void f32_small_kernel(F32Prod p) {
   finish<float, GLU, 4>(p.e, m0 + row, n0 + col, p.N, v[0], v[1]);
 }
 
-// Large outputs: 128 x 128 tiles, 4 waves of 64 x 64, slices of 16 k through
-// two LDS buffers laid out [k][m], the next slice's loads in flight in
-// registers while one is multiplied.  A slice is 32 MFMAs of 64 cycles per
-// wave, so the LDS traffic stays far below the matrix pipe's time.
-template <bool STRIDED>
+// Large outputs: tiles of 64 F x 64 F (F = 1 or 2), 4 waves of 32 F x 32 F,
+// slices of 32 / F k through two LDS buffers laid out [k][m], the next slice's
+// loads in flight in registers while one is multiplied.  A slice is 16 F MFMAs
+// of 64 cycles per wave, so the LDS traffic stays below the matrix pipe's time.
+template <bool STRIDED, bool MIX, int F>
 struct F32Stage {
-  static constexpr int PITCH = 132;  // floats: rows 4 banks apart, 16-byte aligned
+  static constexpr int EXT = 64 * F, BK = 32 / F;
+  static constexpr int PITCH = EXT + 4;  // floats: rows 4 banks apart, 16-byte aligned
+  static constexpr int KQ = BK / 4, MQ = EXT / 4;
   f32x4 v[2];
-  // thread's share: contiguous: rows t / 4 and + 64, k quad t % 4; strided:
-  // k t / 32 and + 8, m quad t % 32
-  __device__ __forceinline__ void fetch(const float* p, size_t ld, int valid, int k0, int kend) {
+  // Thread's share: contiguous: row t / KQ and 256 / KQ on, k quad t % KQ;
+  // strided: k t / MQ and 256 / MQ on, m quad t % MQ.  MIX (gated weights):
+  // every 32 rows are 16 gate rows and the 16 up rows of the same columns.
+  __device__ __forceinline__ void fetch(const float* p, size_t ld, int valid, int k0, int kend,
+                                        size_t up) {
     const int t = threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if constexpr (!STRIDED) {
-        v[i] = quad<false>(p, ld, t / 4 + 64 * i, valid, k0 + t % 4 * 4, kend);
+        const int row = t / KQ + 256 / KQ * i;
+        const int at = MIX ? row / 32 * 16 + row % 16 : row;
+        v[i] = quad<false>(p + (MIX && row % 32 >= 16 ? up : 0), ld, at, valid, k0 + t % KQ * 4, kend);
       } else {
-        const int k = k0 + t / 32 + 8 * i, m = t % 32 * 4;
+        const int k = k0 + t / MQ + 256 / MQ * i, m = t % MQ * 4;
         v[i] = k < kend && m < valid ? *reinterpret_cast<const f32x4*>(p + k * ld + m)
                                      : f32x4{0, 0, 0, 0};
       }
@@ -121,52 +127,44 @@ struct F32Stage {
     for (int i = 0; i < 2; ++i) {
       if constexpr (!STRIDED) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[(t % 4 * 4 + j) * PITCH + t / 4 + 64 * i] = v[i][j];
+        for (int j = 0; j < 4; ++j) s[(t % KQ * 4 + j) * PITCH + t / KQ + 256 / KQ * i] = v[i][j];
       } else {
-        *reinterpret_cast<f32x4*>(s + (t / 32 + 8 * i) * PITCH + t % 32 * 4) = v[i];
+        *reinterpret_cast<f32x4*>(s + (t / MQ + 256 / MQ * i) * PITCH + t % MQ * 4) = v[i];
       }
     }
   }
 };
 
-template <bool RS, bool CS, bool GLU, bool PART>
+template <bool RS, bool CS, int F, bool GLU, bool PART>
 __global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
   static_assert(!GLU || (!CS && !PART), "pairs of gate and up rows: y = x w^T only");
-  constexpr int PITCH = F32Stage<false>::PITCH, BK = 16;
+  typedef F32Stage<RS, false, F> Row;
+  typedef F32Stage<CS, GLU, F> Col;
+  constexpr int PITCH = Row::PITCH, BK = Row::BK, EXT = Row::EXT;
   __shared__ __align__(16) float sr[2][BK * PITCH], sc[2][BK * PITCH];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
   const int wm = wave / 2, wn = wave % 2;
-  constexpr int NC = GLU ? 64 : 128;
-  const int m0 = blockIdx.y * 128, n0 = blockIdx.x * NC;
+  constexpr int NC = GLU ? EXT / 2 : EXT;
+  const int m0 = blockIdx.y * EXT, n0 = blockIdx.x * NC;
   const int k_lo = blockIdx.z * p.per_split, k_hi = min(p.K, k_lo + p.per_split);
   const float* r = p.r + (RS ? m0 : m0 * p.ldr);
   const float* c = p.c + (CS ? n0 : n0 * p.ldc);
   const int mv = p.M - m0, nv = p.N - n0;
-  F32Stage<RS> row;
-  F32Stage<CS> col;
+  Row row;
+  Col col;
   auto fetch = [&](int k0) {
-    row.fetch(r, p.ldr, mv, k0, k_hi);
-    if constexpr (GLU) {  // tile rows 0 .. 63 gate, 64 .. 127 up
-      const int t = threadIdx.x;
-      col.v[0] = quad<false>(c, p.ldc, t / 4, nv, k0 + t % 4 * 4, k_hi);
-      col.v[1] = quad<false>(c + static_cast<size_t>(p.N) * p.ldc, p.ldc, t / 4, nv,
-                             k0 + t % 4 * 4, k_hi);
-    } else {
-      col.fetch(c, p.ldc, nv, k0, k_hi);
-    }
+    row.fetch(r, p.ldr, mv, k0, k_hi, 0);
+    col.fetch(c, p.ldc, nv, k0, k_hi, GLU ? p.N * p.ldc : 0);
   };
-  f32x16 acc[2][2];
+  f32x16 acc[F][F];
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+  for (int x = 0; x < F; ++x)
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
+    for (int y = 0; y < F; ++y)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[x][y][i] = 0.f;
-  const int ml = wm * 64 + (lane & 31), kl = lane >> 5;
-  // GLU: a wave's two column fragments are 32 gate columns and their up columns
-  const int nl = (GLU ? wn * 32 : wn * 64) + (lane & 31);
-  constexpr int YSTEP = GLU ? 64 : 32;
+  const int ml = wm * 32 * F + (lane & 31), nl = wn * 32 * F + (lane & 31), kl = lane >> 5;
   fetch(k_lo);
   int buf = 0;
   for (int k0 = k_lo; k0 < k_hi; k0 += BK, buf ^= 1) {
@@ -177,34 +175,34 @@ __global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
     const float *a = sr[buf], *b = sc[buf];
 #pragma unroll
     for (int k = 0; k < BK; k += 2) {
-      float fr[2], fc[2];
+      float fr[F], fc[F];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) fr[x] = a[(k + kl) * PITCH + ml + 32 * x];
+      for (int x = 0; x < F; ++x) fr[x] = a[(k + kl) * PITCH + ml + 32 * x];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) fc[y] = b[(k + kl) * PITCH + nl + YSTEP * y];
+      for (int y = 0; y < F; ++y) fc[y] = b[(k + kl) * PITCH + nl + 32 * y];
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < F; ++x)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < F; ++y)
           acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x2f32(fc[y], fr[x], acc[x][y], 0, 0, 0);
     }
     // the buffer written next was last read before this iteration's barrier
   }
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int m = m0 + wm * 64 + 32 * x + (lane & 31);
+  for (int x = 0; x < F; ++x) {
+    const int m = m0 + wm * 32 * F + 32 * x + (lane & 31);
     if (m >= p.M) continue;
 #pragma unroll
-    for (int y = 0; y < (GLU ? 1 : 2); ++y)
+    for (int y = 0; y < F; ++y)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + (GLU ? wn * 32 : wn * 64 + 32 * y) + 8 * q + 4 * kl;
+      for (int q = 0; q < (GLU ? 2 : 4); ++q) {
+        const int n = n0 + (wn * 32 * F + 32 * y) / (GLU ? 2 : 1) + 8 * q + 4 * kl;
         if (n >= p.N) continue;
         float g[4], u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           g[i] = acc[x][y][4 * q + i];
-          if constexpr (GLU) u[i] = acc[x][1][4 * q + i];
+          if constexpr (GLU) u[i] = acc[x][y][4 * q + 8 + i];
         }
         if constexpr (PART)
           store4(p.part + (static_cast<size_t>(blockIdx.z) * p.M + m) * p.N + n, g);

@@ -19,21 +19,25 @@ namespace moe {
 namespace lin {
 
 // ------------------------------------------------------------ bf16 product
+// The LDS limit is a per-device function attribute: set once per device.
+inline bool allow_lds(const void* fn, int bytes, std::atomic<bool>* done) {
+  const int dev = current_device();
+  if (dev >= 0 && done[dev].load(std::memory_order_acquire)) return true;
+  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    return false;
+  if (dev >= 0) done[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+inline int grid_of(const Mma& a) { return (a.tm * a.tn * a.splits + 7) / 8 * 8; }
+
 template <bool RS, bool CS, int BM, int BN, int WGS, bool GLU, bool PART>
 int launch_mma(const Mma& a, hipStream_t s) {
   constexpr int lds = (SA * BM + SB * BN) * SLICE * 2;
-  const void* fn = reinterpret_cast<const void*>(mma_kernel<RS, CS, BM, BN, WGS, GLU, PART>);
-  // the LDS limit is a per-device function attribute: set once per device
-  static std::atomic<bool> attr_set[64];
-  const int dev = current_device();
-  if (dev < 0 || !attr_set[dev].load(std::memory_order_acquire)) {
-    if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
-      return MOE_EHIP;
-    if (dev >= 0) attr_set[dev].store(true, std::memory_order_release);
-  }
-  const int total = a.tm * a.tn * a.splits;
-  hipLaunchKernelGGL((mma_kernel<RS, CS, BM, BN, WGS, GLU, PART>), dim3((total + 7) / 8 * 8),
-                     dim3(W * MOE_WAVE), lds, s, a);
+  const auto fn = mma_kernel<RS, CS, BM, BN, WGS, GLU, PART>;
+  static std::atomic<bool> done[64];
+  if (!allow_lds(reinterpret_cast<const void*>(fn), lds, done)) return MOE_EHIP;
+  hipLaunchKernelGGL(fn, dim3(grid_of(a)), dim3(W * MOE_WAVE), lds, s, a);
   return MOE_OK;
 }
 
@@ -74,12 +78,18 @@ struct Tile {
 };
 constexpr Tile TILES[] = {{256, 256}, {256, 192}, {192, 256}, {128, 128}};
 
+// The plan's tiles and splits of a product of W output columns (GLU: gate and
+// up) in `a`; part: room for the partial sums.
+inline void cut(Mma& a, const Plan& p, int W, float* part) {
+  a.per_split = ((a.K + p.splits - 1) / p.splits + 63) / 64 * 64;
+  a.splits = (a.K + a.per_split - 1) / a.per_split;
+  a.tm = (a.M + TILES[p.tile].m - 1) / TILES[p.tile].m;
+  a.tn = (W + TILES[p.tile].n - 1) / TILES[p.tile].n;
+  a.part = part;
+}
+
 template <bool RS, bool CS, bool GLU, bool PART>
-int launch_tile(Mma& a, int tile, hipStream_t s) {
-  const Tile t = TILES[tile];
-  a.tm = (a.M + t.m - 1) / t.m;
-  const int nc = GLU ? t.n / 2 : t.n;
-  a.tn = (a.N + nc - 1) / nc;
+int launch_tile(const Mma& a, int tile, hipStream_t s) {
   switch (tile) {
     case 0: return launch_mma<RS, CS, 256, 256, 1, GLU, PART>(a, s);
     case 1: return launch_mma<RS, CS, 256, 192, 1, GLU, PART>(a, s);
@@ -88,21 +98,22 @@ int launch_tile(Mma& a, int tile, hipStream_t s) {
   }
 }
 
-// Product with the plan's tile and splits; part: room for the partial sums.
+template <typename E, bool GLU>
+void launch_join(const float* part, int splits, int M, int N, const Epilogue& e, hipStream_t s) {
+  const size_t quads = static_cast<size_t>(M) * N / 4;
+  hipLaunchKernelGGL((join_kernel<E, GLU>), dim3((quads + 255) / 256), dim3(256), 0, s, part, splits,
+                     M, N, e);
+}
+
 template <bool RS, bool CS, bool GLU>
-int product(Mma a, Plan p, float* part, hipStream_t s) {
-  a.per_split = ((a.K + p.splits - 1) / p.splits + 63) / 64 * 64;
-  a.splits = (a.K + a.per_split - 1) / a.per_split;
-  a.part = part;
+int product(Mma a, const Plan& p, float* part, hipStream_t s) {
+  const int N = a.N, W = GLU ? 2 * N : N;
+  cut(a, p, W, part);
   if (a.splits == 1) return launch_tile<RS, CS, GLU, false>(a, p.tile, s);
-  const int N = a.N;
-  if (GLU) a.N *= 2;
+  a.N = W;
   const int rc = launch_tile<RS, CS, false, true>(a, p.tile, s);
-  if (rc != MOE_OK) return rc;
-  const size_t quads = static_cast<size_t>(a.M) * N / 4;
-  hipLaunchKernelGGL((join_kernel<uint16_t, GLU>), dim3((quads + 255) / 256), dim3(256), 0, s, part,
-                     a.splits, a.M, N, a.e);
-  return MOE_OK;
+  if (rc == MOE_OK) launch_join<uint16_t, GLU>(part, a.splits, a.M, N, a.e, s);
+  return rc;
 }
 
 // ------------------------------------------------------------ fp32 product
@@ -130,8 +141,7 @@ inline Plan plan_f32(int M, int W, int K, bool strided) {
 }
 
 template <bool RS, bool CS, bool GLU>
-int product_f32(F32Prod a, float* part, hipStream_t s) {
-  const Plan p = plan_f32(a.M, GLU ? 2 * a.N : a.N, a.K, RS || CS);
+int product_f32(F32Prod a, const Plan& p, float* part, hipStream_t s) {
   if (p.tile == 32) {
     hipLaunchKernelGGL((f32_small_kernel<RS, CS, GLU>), dim3((a.N + 31) / 32, (a.M + 31) / 32),
                        dim3(256), 0, s, a);
@@ -155,9 +165,7 @@ int product_f32(F32Prod a, float* part, hipStream_t s) {
     hipLaunchKernelGGL((f32_large_kernel<RS, CS, 1, false, true>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((f32_large_kernel<RS, CS, 2, false, true>), grid, dim3(256), 0, s, a);
-  const size_t quads = static_cast<size_t>(a.M) * N / 4;
-  hipLaunchKernelGGL((join_kernel<float, GLU>), dim3((quads + 255) / 256), dim3(256), 0, s, part,
-                     splits, a.M, N, a.e);
+  launch_join<float, GLU>(part, splits, a.M, N, a.e, s);
   return MOE_OK;
 }
 
@@ -192,11 +200,6 @@ inline Plan plan(int M, int W, int K) {
   }
   return best;
 }
-inline size_t part_bytes(int M, int W, int K, bool strided, int dtype) {
-  const Plan p = dtype == MOE_BF16 ? plan(M, W, K) : plan_f32(M, W, K, strided);
-  return p.splits > 1 ? static_cast<size_t>(p.splits) * M * W * 4 : 0;
-}
-
 // Few tokens: the skinny product or the tiles, whichever is estimated faster.
 // The skinny one is bound by its loads' addresses: a block of 64 k costs a
 // workgroup 0.25 us for the weights and 0.4 us for each 16 tokens (less for
@@ -326,17 +329,9 @@ __global__ __launch_bounds__(COLT * ROWT) void act_grad_sum_kernel(
 }
 
 template <typename E>
-__global__ __launch_bounds__(256) void bias_sum_kernel(const float* __restrict__ part, int blocks,
-                                                       int W, E* __restrict__ dbias) {
-  __shared__ float red[4][64];
-  const int c = threadIdx.x % 64, r = threadIdx.x / 64, o = blockIdx.x * 64 + c;
-  float v = 0.f;
-  if (o < W)
-#pragma unroll 8
-    for (int b = r; b < blocks; b += 4) v += part[static_cast<size_t>(b) * W + o];
-  red[r][c] = v;
-  __syncthreads();
-  if (r == 0 && o < W) store1(dbias + o, red[0][c] + red[1][c] + red[2][c] + red[3][c]);
+__global__ __launch_bounds__(256) void bias_sum_kernel(BiasSum b) {
+  __shared__ float red[256];
+  bias_sum<E>(b, blockIdx.x, red);
 }
 
 template <typename E>
@@ -368,29 +363,41 @@ inline int check(int T, int K, int O, int act, int dtype) {
 }
 
 struct BackPlan {
-  int rows, blocks;                // token rows of an act_grad block, their number
-  size_t dz, sums, parts, bytes;  // offsets, size
+  int rows, blocks;   // token rows of an act_grad block, their number
+  Plan x, w;          // dx, dw
+  bool pair;          // both products in one launch
+  size_t sums, part_x, part_w, bytes;  // offsets (dz at 0), size
 };
 
+inline size_t part_bytes(const Plan& p, int M, int W) {
+  return p.splits > 1 ? up256(static_cast<size_t>(p.splits) * M * W * 4) : 0;
+}
+
 inline BackPlan back_plan(int T, int K, int O, int act, int dtype) {
-  BackPlan p;
+  BackPlan p{};
   const int W = width(O, act);
   p.rows = std::max(ROWT, (T + 255) / 256);
   p.blocks = (T + p.rows - 1) / p.rows;
-  p.dz = 0;
   p.sums = act == MOE_ACT_NONE ? 0 : up256(static_cast<size_t>(T) * W * elem_size(dtype));
-  p.parts = p.sums + up256(static_cast<size_t>(p.blocks) * W * 4);
-  p.bytes = p.parts + 256;
-  if (T > 0) p.bytes += std::max(part_bytes(T, K, W, true, dtype), part_bytes(W, K, T, true, dtype));
+  p.part_x = p.sums + up256(static_cast<size_t>(p.blocks) * W * 4);
+  p.part_w = p.part_x;
+  p.bytes = p.part_x + 256;
+  if (T == 0) return p;
+  const bool bf16 = dtype == MOE_BF16;
+  p.x = bf16 ? plan(T, K, W) : plan_f32(T, K, W, true);
+  p.w = bf16 ? plan(W, K, T) : plan_f32(W, K, T, true);
+  p.pair = p.x.tile == p.w.tile && p.x.tile == (bf16 ? 3 : 32);
+  const size_t bx = part_bytes(p.x, T, K), bw = part_bytes(p.w, W, K);
+  if (p.pair) p.part_w += bx;  // side by side; one after the other otherwise
+  p.bytes += p.pair ? bx + bw : std::max(bx, bw);
   return p;
 }
 
 template <typename D>
 void launch_act_grad(const void* dy, const void* z, int T, int O, int act, const BackPlan& p,
-                     void* dz, float* sums, void* dbias, hipStream_t s) {
+                     void* dz, float* sums, hipStream_t s) {
   typedef typename D::elem E;
-  const int W = width(O, act);
-  if (!dbias) {
+  if (!sums) {
     const size_t chunks = static_cast<size_t>(T) * (O / D::V);
     hipLaunchKernelGGL(act_grad_kernel<D>, grid_of(chunks), dim3(256), 0, s,
                        static_cast<const E*>(dy), static_cast<const E*>(z), T, O, act,
@@ -400,11 +407,55 @@ void launch_act_grad(const void* dy, const void* z, int T, int O, int act, const
   hipLaunchKernelGGL(act_grad_sum_kernel<D>, dim3((O + COLT * D::V - 1) / (COLT * D::V), p.blocks),
                      dim3(COLT * ROWT), 0, s, static_cast<const E*>(dy), static_cast<const E*>(z),
                      T, O, act, p.rows, static_cast<E*>(dz), sums);
-  hipLaunchKernelGGL(bias_sum_kernel<E>, dim3((W + 63) / 64), dim3(256), 0, s, sums, p.blocks, W,
-                     static_cast<E*>(dbias));
 }
 
-template <typename D>
+template <bool PX, bool PW>
+int launch_pair(const Mma& x, const Mma& w, const BiasSum& b, hipStream_t s) {
+  constexpr int lds = (SA + SB) * 128 * SLICE * 2;
+  const auto fn = mma_pair_kernel<PX, PW>;
+  static std::atomic<bool> done[64];
+  if (!allow_lds(reinterpret_cast<const void*>(fn), lds, done)) return MOE_EHIP;
+  const int dw0 = grid_of(x), bias0 = dw0 + grid_of(w);
+  hipLaunchKernelGGL(fn, dim3(bias0 + (b.dbias ? (b.W + 63) / 64 : 0)), dim3(W * MOE_WAVE), lds, s,
+                     x, w, b, dw0, bias0);
+  return MOE_OK;
+}
+
+// dx = dz w and dw = dz^T x (either may be absent: null y), and the bias's last
+// sum where the two share a launch; b.dbias is cleared then.
+inline int products(Mma x, Mma w, const BackPlan& p, BiasSum& b, float* part_x, float* part_w,
+                    hipStream_t s) {
+  if (!(p.pair && x.e.y && w.e.y)) {
+    int rc = x.e.y ? product<false, true, false>(x, p.x, part_x, s) : MOE_OK;
+    if (w.e.y && rc == MOE_OK) rc = product<true, true, false>(w, p.w, part_w, s);
+    return rc;
+  }
+  cut(x, p.x, x.N, part_x);
+  cut(w, p.w, w.N, part_w);
+  const bool px = x.splits > 1, pw = w.splits > 1;
+  const int rc = px ? (pw ? launch_pair<true, true>(x, w, b, s) : launch_pair<true, false>(x, w, b, s))
+                    : (pw ? launch_pair<false, true>(x, w, b, s) : launch_pair<false, false>(x, w, b, s));
+  b.dbias = nullptr;
+  if (px && rc == MOE_OK) launch_join<uint16_t, false>(part_x, x.splits, x.M, x.N, x.e, s);
+  if (pw && rc == MOE_OK) launch_join<uint16_t, false>(part_w, w.splits, w.M, w.N, w.e, s);
+  return rc;
+}
+
+inline int products(const F32Prod& x, const F32Prod& w, const BackPlan& p, BiasSum& b,
+                    float* part_x, float* part_w, hipStream_t s) {
+  if (!(p.pair && x.e.y && w.e.y)) {
+    int rc = x.e.y ? product_f32<false, true, false>(x, p.x, part_x, s) : MOE_OK;
+    if (w.e.y && rc == MOE_OK) rc = product_f32<true, true, false>(w, p.w, part_w, s);
+    return rc;
+  }
+  const int nx = (x.N + 31) / 32, dw0 = nx * ((x.M + 31) / 32), bias0 = dw0 + nx * ((w.M + 31) / 32);
+  hipLaunchKernelGGL(f32_pair_kernel, dim3(bias0 + (b.dbias ? (b.W + 63) / 64 : 0)), dim3(256), 0, s,
+                     x, w, b, nx, dw0, bias0);
+  b.dbias = nullptr;
+  return MOE_OK;
+}
+
+template <typename D, typename P>
 int backward(const void* dy, const void* x, const void* w, const void* z, int T, int K, int O,
              int act, int dtype, void* dx, void* dw, void* dbias, char* ws, hipStream_t s) {
   typedef typename D::elem E;
@@ -413,64 +464,36 @@ int backward(const void* dy, const void* x, const void* w, const void* z, int T,
     if (!dw && !dbias) return MOE_OK;
     const size_t nw = static_cast<size_t>(W) * K;
     if (dw)
-      hipLaunchKernelGGL(zero_kernel<E>, grid_of(nw), dim3(256), 0, s,
-                         static_cast<E*>(dw), nw);
+      hipLaunchKernelGGL(zero_kernel<E>, grid_of(nw), dim3(256), 0, s, static_cast<E*>(dw), nw);
     if (dbias)
-      hipLaunchKernelGGL(zero_kernel<E>, grid_of(W), dim3(256), 0, s,
-                         static_cast<E*>(dbias), static_cast<size_t>(W));
+      hipLaunchKernelGGL(zero_kernel<E>, grid_of(W), dim3(256), 0, s, static_cast<E*>(dbias),
+                         static_cast<size_t>(W));
     return launch_status();
   }
   const BackPlan p = back_plan(T, K, O, act, dtype);
   const void* dz = dy;
+  BiasSum b{reinterpret_cast<float*>(ws + p.sums), p.blocks, W, dbias};
   if ((act != MOE_ACT_NONE && (dx || dw)) || dbias) {
-    launch_act_grad<D>(dy, z, T, O, act, p, ws + p.dz, reinterpret_cast<float*>(ws + p.sums), dbias,
+    launch_act_grad<D>(dy, z, T, O, act, p, ws, dbias ? reinterpret_cast<float*>(ws + p.sums) : nullptr,
                        s);
-    if (act != MOE_ACT_NONE) dz = ws + p.dz;
+    if (act != MOE_ACT_NONE) dz = ws;
   }
-  int rc = MOE_OK;
-  float* part = reinterpret_cast<float*>(ws + p.parts);
-  if (dtype == MOE_BF16) {
-    Mma q{};
-    q.N = K;
-    q.ldr = W;
-    q.ldc = K;
-    q.r = static_cast<const uint16_t*>(dz);
-    if (dx) {
-      q.c = static_cast<const uint16_t*>(w);
-      q.M = T;
-      q.K = W;
-      q.e.y = dx;
-      rc = product<false, true, false>(q, plan(T, K, W), part, s);
-    }
-    if (dw && rc == MOE_OK) {
-      q.c = static_cast<const uint16_t*>(x);
-      q.M = W;
-      q.K = T;
-      q.e.y = dw;
-      rc = product<true, true, false>(q, plan(W, K, T), part, s);
-    }
-  } else {
-    F32Prod q{};
-    q.N = K;
-    q.ldr = W;
-    q.ldc = K;
-    q.r = static_cast<const float*>(dz);
-    if (dx) {
-      q.c = static_cast<const float*>(w);
-      q.M = T;
-      q.K = W;
-      q.e.y = dx;
-      rc = product_f32<false, true, false>(q, part, s);
-    }
-    if (dw && rc == MOE_OK) {
-      q.c = static_cast<const float*>(x);
-      q.M = W;
-      q.K = T;
-      q.e.y = dw;
-      rc = product_f32<true, true, false>(q, part, s);
-    }
-  }
-  return rc == MOE_OK ? launch_status() : rc;
+  P qx{};
+  qx.r = static_cast<const E*>(dz);
+  qx.ldr = W;
+  qx.ldc = qx.N = K;
+  P qw = qx;
+  qx.c = static_cast<const E*>(w);
+  qx.M = qw.K = T;
+  qx.K = qw.M = W;
+  qx.e.y = dx;
+  qw.c = static_cast<const E*>(x);
+  qw.e.y = dw;
+  const int rc = products(qx, qw, p, b, reinterpret_cast<float*>(ws + p.part_x),
+                          reinterpret_cast<float*>(ws + p.part_w), s);
+  if (rc != MOE_OK) return rc;
+  if (b.dbias) hipLaunchKernelGGL(bias_sum_kernel<E>, dim3((W + 63) / 64), dim3(256), 0, s, b);
+  return launch_status();
 }
 
 }  // namespace lin
@@ -482,7 +505,8 @@ using namespace moe::lin;
 extern "C" size_t moe_linear_workspace_size(int T, int K, int O, int act, int dtype) {
   if (check(T, K, O, act, dtype) != MOE_OK) return 0;
   if (T == 0 || (dtype == MOE_BF16 && skinny_plan(T, K, width(O, act)))) return 256;
-  return 256 + part_bytes(T, width(O, act), K, false, dtype);
+  const int W = width(O, act);
+  return 256 + part_bytes(dtype == MOE_BF16 ? plan(T, W, K) : plan_f32(T, W, K, false), T, W);
 }
 
 extern "C" int moe_linear(const void* x, const void* w, const void* bias, const void* residual,
@@ -524,7 +548,9 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
     q.N = O;
     q.K = K;
     q.e = e;
-    r = glu ? product_f32<false, false, true>(q, part, s) : product_f32<false, false, false>(q, part, s);
+    const Plan p = plan_f32(T, width(O, act), K, false);
+    r = glu ? product_f32<false, false, true>(q, p, part, s)
+            : product_f32<false, false, false>(q, p, part, s);
   }
   return r == MOE_OK ? launch_status() : r;
 }
@@ -551,6 +577,6 @@ extern "C" int moe_linear_backward(const void* dy, const void* x, const void* w,
   char* ws = static_cast<char*>(workspace);
   hipStream_t s = as_stream(stream);
   if (dtype == MOE_BF16)
-    return backward<Bf16>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
-  return backward<F32>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
+    return backward<Bf16, Mma>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
+  return backward<F32, F32Prod>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
 }

@@ -192,5 +192,27 @@ __device__ __forceinline__ void finish(const Epilogue& e, int m, int n, int N, f
   store_v<V>(static_cast<E*>(e.y) + at, v);
 }
 
+// ----------------------------------------------------------- bias gradient
+// Column sums of [blocks][W] partial sums, 64 columns per workgroup of 256
+// threads; red: 256 floats of LDS.
+struct BiasSum {
+  const float* part;
+  int blocks, W;
+  void* dbias;
+};
+
+template <typename E>
+__device__ __forceinline__ void bias_sum(const BiasSum& b, int block, float* red) {
+  const int c = threadIdx.x % 64, r = threadIdx.x / 64, o = block * 64 + c;
+  float v = 0.f;
+  if (o < b.W)
+#pragma unroll 8
+    for (int i = r; i < b.blocks; i += 4) v += b.part[static_cast<size_t>(i) * b.W + o];
+  red[threadIdx.x] = v;
+  __syncthreads();
+  if (r == 0 && o < b.W)
+    store1(static_cast<E*>(b.dbias) + o, (red[c] + red[64 + c]) + (red[128 + c] + red[192 + c]));
+}
+
 }  // namespace lin
 }  // namespace moe

@@ -40,13 +40,15 @@ __device__ __forceinline__ f32x4 quad(const float* p, size_t ld, int m, int mend
 // registers (lane: row l % 32; MFMA j of a turn takes k = j and j + 4), the
 // waves' sums joined through LDS.  Bound by latency: with 64 workgroups a
 // larger tile would leave the card empty.
+constexpr int SMALL_LDS = 4 * 32 * 33;  // floats per output matrix
+
 template <bool RS, bool CS, bool GLU>
-__global__ __launch_bounds__(256) void f32_small_kernel(F32Prod p) {
+__device__ __forceinline__ void f32_small_tile(const F32Prod& p, int bx, int by, float* lds) {
   constexpr int H = GLU ? 2 : 1, TURNS = 4;
-  __shared__ float red[H][4][32][33];
+  float(*red)[4][32][33] = reinterpret_cast<float(*)[4][32][33]>(lds);
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
-  const int m0 = blockIdx.y * 32, n0 = blockIdx.x * 32;
+  const int m0 = by * 32, n0 = bx * 32;
   const int m = m0 + (lane & 31), n = n0 + (lane & 31);
   f32x16 acc[H];
 #pragma unroll
@@ -90,6 +92,29 @@ __global__ __launch_bounds__(256) void f32_small_kernel(F32Prod p) {
       v[h][i] = (red[h][0][row][col + i] + red[h][1][row][col + i]) +
                 (red[h][2][row][col + i] + red[h][3][row][col + i]);
   finish<float, GLU, 4>(p.e, m0 + row, n0 + col, p.N, v[0], v[1]);
+}
+
+template <bool RS, bool CS, bool GLU>
+__global__ __launch_bounds__(256) void f32_small_kernel(F32Prod p) {
+  __shared__ float lds[(GLU ? 2 : 1) * SMALL_LDS];
+  f32_small_tile<RS, CS, GLU>(p, blockIdx.x, blockIdx.y, lds);
+}
+
+// Both products of a small backward pass and the bias gradient's last sum in
+// one launch: workgroups from dw0 on are dw's, from bias0 on the bias's; nx:
+// tiles along the columns, K for both.
+__global__ __launch_bounds__(256) void f32_pair_kernel(F32Prod dx, F32Prod dw, BiasSum b, int nx,
+                                                       int dw0, int bias0) {
+  __shared__ float lds[SMALL_LDS];
+  int block = blockIdx.x;
+  if (block < dw0) {
+    f32_small_tile<false, true, false>(dx, block % nx, block / nx, lds);
+  } else if (block < bias0) {
+    block -= dw0;
+    f32_small_tile<true, true, false>(dw, block % nx, block / nx, lds);
+  } else {
+    bias_sum<float>(b, block - bias0, lds);
+  }
 }
 
 // Large outputs: tiles of 64 F x 64 F (F = 1 or 2), 4 waves of 32 F x 32 F,

@@ -158,10 +158,10 @@ struct Reader {
 // Tiles that run side by side on one XCD (workgroups go round-robin over the
 // 8 XCDs, so each gets one contiguous range of the list) form blocks of
 // GROUP tile rows, which share the operands' slices in that XCD's L2.
-__device__ __forceinline__ bool tile_of(const Mma& a, int& mt, int& nt, int& split) {
+__device__ __forceinline__ bool tile_of(const Mma& a, int p, int& mt, int& nt, int& split) {
   constexpr int GROUP = 4;
   const int tiles = a.tm * a.tn, total = tiles * a.splits;
-  const int p = blockIdx.x, q = (total + 7) / 8;
+  const int q = (total + 7) / 8;
   const int L = (p % 8) * q + p / 8;
   if (L >= total) return false;
   split = L / tiles;
@@ -199,10 +199,9 @@ __device__ __forceinline__ void spread_reads() {
   if constexpr (NMF > N) __builtin_amdgcn_sched_group_barrier(0x0008, NMF - N, 0);
 }
 
-template <bool RS, bool CS, int BM, int BN, int WGS, bool GLU, bool PART>
-__global__ __launch_bounds__(W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(WGS, WGS)))
-void mma_kernel(Mma a) {
-  extern __shared__ __align__(16) unsigned char smem[];
+// Workgroup `block` of a product; smem: the ring.
+template <bool RS, bool CS, int BM, int BN, bool GLU, bool PART>
+__device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char* smem) {
   static_assert(!GLU || (!CS && !PART), "pairs of gate and up rows: y = x w^T only");
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
   static_assert(TM % 32 == 0 && TN % 32 == 0, "whole fragments");
@@ -218,7 +217,7 @@ void mma_kernel(Mma a) {
   constexpr int NFR = FM * (RS ? 2 : 1) + FN * (CS ? 2 : 1);  // LDS reads per 16 k
 
   int mt, nt, split;
-  if (!tile_of(a, mt, nt, split)) return;
+  if (!tile_of(a, block, mt, nt, split)) return;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
   const int wm = wave / WN, wn = wave % WN;
@@ -390,6 +389,26 @@ void mma_kernel(Mma a) {
       }
     }
   }
+}
+
+template <bool RS, bool CS, int BM, int BN, int WGS, bool GLU, bool PART>
+__global__ __launch_bounds__(W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(WGS, WGS)))
+void mma_kernel(Mma a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  mma_tile<RS, CS, BM, BN, GLU, PART>(a, blockIdx.x, smem);
+}
+
+// Both products of a small backward pass and the bias gradient's last sum in
+// one launch: workgroups from dw0 on are dw's, from bias0 on the bias's.  Each
+// alone leaves most CUs empty or waits for memory.
+template <bool PX, bool PW>
+__global__ __launch_bounds__(W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void mma_pair_kernel(Mma dx, Mma dw, BiasSum b, int dw0, int bias0) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int block = blockIdx.x;
+  if (block < dw0) mma_tile<false, true, 128, 128, false, PX>(dx, block, smem);
+  else if (block < bias0) mma_tile<true, true, 128, 128, false, PW>(dw, block - dw0, smem);
+  else bias_sum<uint16_t>(b, block - bias0, reinterpret_cast<float*>(smem));
 }
 
 }  // namespace lin

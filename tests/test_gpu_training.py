@@ -174,6 +174,69 @@ def test_linear_backward(B, i, dtype):
             assert torch.equal(alone[n], outs[n]), n
 
 
+# Output rows, output columns, reduction: each tile that the products choose on
+# 256 compute units, whole and with the reduction split (bf16: 256 x 256, 256 x
+# 192, 192 x 256, 128 x 128; fp32: 128 x 128, 64 x 64), with edges inside tiles
+# and slices.
+LARGE = [(4440, 2704, 136), (2048, 4096, 8192), (3738, 3232, 64), (8804, 136, 3096),
+         (1711, 6952, 64), (264, 5936, 3920), (8000, 392, 64), (5104, 72, 728), (136, 64, 496),
+         (1100, 1544, 264)]
+
+
+@pytest.mark.parametrize("m,w,k", LARGE)
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_linear_every_tile(B, m, w, k, dtype):
+    for act, O in (("silu", w), ("swiglu", w // 16 * 8)):
+        if dtype == F32 and m * w * k > 1 << 34:
+            continue
+        print(f"[gpu-test] linear {m} {k} {O} {act} {dtype}", flush=True)
+        g, x, wt, b, r = _linear_inputs(m, k, O, act, dtype, 7, True, True)
+        ws = torch.full((B.moe_linear_workspace_size(m, k, O, act, dtype),), 0xFF, dtype=torch.uint8,
+                        device="cuda")
+        ybuf, y, pad = _guard((m, O), dtype)
+        zbuf, z, _ = _guard((m, wt.shape[0]), dtype)
+        B.moe_linear(x, wt, ws, bias=b, residual=r, act=act, z=z, y=y)
+        yr, zr, ey, ez = R.linear(R.f64(x), R.f64(wt), R.f64(b), R.f64(r), act, dtype)
+        _near(z, zr, ez, "z")
+        _near(y, yr, ey, "y")
+        assert _untouched(ybuf, pad) and _untouched(zbuf, pad)
+
+
+@pytest.mark.parametrize("m,w,k", LARGE)
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_linear_backward_every_tile(B, m, w, k, dtype):
+    """T, O chosen so that dx (first) and dw (second) have these sizes."""
+    for T, O, act in ((m, k, "none"), (k, m // 8 * 8, "silu")):
+        if dtype == F32 and m * w * k > 1 << 34:
+            continue
+        print(f"[gpu-test] linear backward {T} {w} {O} {act} {dtype}", flush=True)
+        g, x, wt, _, _ = _linear_inputs(T, w, O, act, dtype, 8, False, False)
+        dy, z = _rand(g, (T, O), 0.5, dtype), _rand(g, (T, O), 1.0, dtype)
+        ws = torch.full((B.moe_linear_backward_workspace_size(T, w, O, act, dtype),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+        bufs = {"dx": _guard((T, w), dtype), "dw": _guard((O, w), dtype), "db": _guard((O,), dtype)}
+        B.moe_linear_backward(dy, x, wt, ws, z=z, act=act, dx=bufs["dx"][1], dw=bufs["dw"][1],
+                              dbias=bufs["db"][1])
+        want = R.linear_backward(R.f64(dy), R.f64(x), R.f64(wt), R.f64(z), act, dtype)
+        for n, (v, e) in want.items():
+            _near(bufs[n][1], v, e, n)
+            assert _untouched(bufs[n][0], bufs[n][2]), n
+
+
+@pytest.mark.parametrize("T,K,O", [(1, 14336, 4096), (16, 14336, 4096), (40, 1264, 72), (70, 4096, 512),
+                                   (100, 608, 4488), (127, 480, 4264), (128, 4096, 1024)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_linear_few_tokens_wide_weights(B, T, K, O, act):
+    g, x, w, b, r = _linear_inputs(T, K, O, act, BF16, 9, True, True)
+    ws = torch.full((B.moe_linear_workspace_size(T, K, O, act, BF16),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    ybuf, y, pad = _guard((T, O), BF16)
+    B.moe_linear(x, w, ws, bias=b, residual=r, act=act, y=y)
+    yr, _, ey, _ = R.linear(R.f64(x), R.f64(w), R.f64(b), R.f64(r), act, BF16)
+    _near(y, yr, ey, "y")
+    assert _untouched(ybuf, pad)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_linear_backward_without_tokens_writes_zeros(B, dtype):
     x, w = torch.empty(0, 64, dtype=dtype, device="cuda"), torch.ones(48, 64, dtype=dtype, device="cuda")

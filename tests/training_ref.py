@@ -28,6 +28,14 @@ def f64(t) -> np.ndarray | None:
     return None if t is None else t.detach().to(torch.float64).cpu().numpy()
 
 
+def product(a, b):
+    """a @ b in 64 bits, on the GPU where it is large."""
+    if a.shape[0] * a.shape[1] * b.shape[1] > 1 << 31 and torch.cuda.is_available():
+        return (torch.from_numpy(np.ascontiguousarray(a)).cuda()
+                @ torch.from_numpy(np.ascontiguousarray(b)).cuda()).cpu().numpy()
+    return a @ b
+
+
 # --------------------------------------------------------------------- linear
 def act_value(z, act):
     if act == "relu":
@@ -54,8 +62,8 @@ def linear(x, w, bias, residual, act, dtype):
     """(y, z, bound of y, bound of z); arguments fp64."""
     K = x.shape[1]
     b = 0.0 if bias is None else bias
-    z = x @ w.T + b
-    ez = (K + 2) * U * (np.abs(x) @ np.abs(w).T + np.abs(b))
+    z = product(x, w.T) + b
+    ez = (K + 2) * U * (product(np.abs(x), np.abs(w).T) + np.abs(b))
     if act == "swiglu":
         O = w.shape[0] // 2
         g, u = z[:, :O], z[:, O:]
@@ -97,8 +105,8 @@ def linear_backward(dy, x, w, z, act, dtype):
     T, W = dz.shape
     out = {}
     for name, a, ea, b, n in (("dx", dz, ez, w, W), ("dw", dz.T, ez.T, x, T)):
-        v = a @ b
-        err = ea @ np.abs(b) + (n + 2) * U * ((np.abs(a) + ea) @ np.abs(b))
+        v = product(a, b)
+        err = product(ea + (n + 2) * U * (np.abs(a) + ea), np.abs(b))
         out[name] = (v, err * (1 + h) + h * np.abs(v))
     v = dz.sum(0)
     err = e.sum(0) + (T + 2) * U * (np.abs(dz) + e).sum(0)

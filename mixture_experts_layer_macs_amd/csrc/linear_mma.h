@@ -181,24 +181,6 @@ struct Staging {
   static_assert(WM * XC * 32 * PITCH * 4 <= RING, "fits the ring");
 };
 
-// Scheduling groups of one 16-k step: one LDS read after each of the first
-// MFMAs (several if there are more reads than MFMAs), the rest of the MFMAs
-// behind them to cover the last reads' latency.
-template <int PER, int N>
-__device__ __forceinline__ void spread_groups() {
-  if constexpr (N > 0) {
-    __builtin_amdgcn_sched_group_barrier(0x0008, 1, 0);    // MFMA
-    __builtin_amdgcn_sched_group_barrier(0x0100, PER, 0);  // LDS read
-    spread_groups<PER, N - 1>();
-  }
-}
-template <int NMF, int NFR>
-__device__ __forceinline__ void spread_reads() {
-  constexpr int PER = (NFR + NMF - 1) / NMF, N = (NFR + PER - 1) / PER;
-  spread_groups<PER, N>();
-  if constexpr (NMF > N) __builtin_amdgcn_sched_group_barrier(0x0008, NMF - N, 0);
-}
-
 // Workgroup `block` of a product; smem: the ring.
 template <bool RS, bool CS, int BM, int BN, bool GLU, bool PART>
 __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char* smem) {
@@ -214,7 +196,6 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
   constexpr int KK = SLICE / 16;
   static_assert(KK % 2 == 0, "fragment sets alternate");
   constexpr int NMF = FM * FN;
-  constexpr int NFR = FM * (RS ? 2 : 1) + FN * (CS ? 2 : 1);  // LDS reads per 16 k
 
   int mt, nt, split;
   if (!tile_of(a, block, mt, nt, split)) return;
@@ -266,28 +247,32 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[x][y][r] = 0.f;
   bf16x8 fr[2][FM], fc[2][FN];
-  // Fragments of 16 k in the order in which the MFMAs need them (row 0, every
-  // column, the other rows), with `more` requests spread over them.
-  auto read = [&](int t, int kk, int more, auto request) {
-    lds_cbyte* A = lds0 + (t % SA) * Row::BYTES;
-    lds_cbyte* B = lds0 + B_BASE + (t % SB) * Col::BYTES;
-#pragma unroll
-    for (int f = 0; f < FM + FN; ++f) {
-      if (f >= 1 && f <= FN) fc[kk & 1][f - 1] = ColR::read(B, co[f - 1], kk, lane);
-      else fr[kk & 1][f ? f - FN : 0] = RowR::read(A, ro[f ? f - FN : 0], kk, lane);
-#pragma unroll
-      for (int q = f * more / (FM + FN); q < (f + 1) * more / (FM + FN); ++q) request(q);
-    }
+  // Fragment f of 16 k of slice t, in the order in which the MFMAs need them:
+  // row 0, every column, the other rows.
+  auto read = [&](int t, int kk, int f) {
+    if (f >= 1 && f <= FN)
+      fc[kk & 1][f - 1] =
+          ColR::read(lds0 + B_BASE + (t % SB) * Col::BYTES, co[f - 1], kk, lane);
+    else
+      fr[kk & 1][f ? f - FN : 0] = RowR::read(lds0 + (t % SA) * Row::BYTES, ro[f ? f - FN : 0], kk, lane);
   };
-  // 16 k of MFMAs with the LDS reads placed above, one after each of the first.
-  auto mma = [&](int kk) {
+  // The MFMAs of 16 k, in this order with the reads of the next 16 k (slice tr)
+  // behind the first of them and `requests` requests of the ring between them:
+  // a run of requests, from four waves at once, holds up the MFMAs behind it.
+  auto step = [&](int kk, int tr, int requests, auto request) {
 #pragma unroll
-    for (int x = 0; x < FM; ++x)
+    for (int i = 0; i < NMF; ++i) {
+      const int x = i / FN, y = i % FN;
+      acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[kk & 1][y], fr[kk & 1][x], acc[x][y],
+                                                         0, 0, 0);
+      constexpr int NF = FM + FN, PER = (NF + NMF - 1) / NMF;
 #pragma unroll
-      for (int y = 0; y < FN; ++y)
-        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[kk & 1][y], fr[kk & 1][x],
-                                                           acc[x][y], 0, 0, 0);
-    spread_reads<NMF, NFR>();
+      for (int f = i * PER; f < (i + 1) * PER && f < NF; ++f) read(tr, (kk + 1) % KK, f);
+#pragma unroll
+      for (int q = 0; q < requests; ++q)
+        if ((2 * q + 1) * NMF / (2 * requests) == i) request(q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
   // Before the last 16 k of slice t are multiplied, every wave has its
@@ -295,13 +280,9 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
   // behind the barrier row slice t + SA and, under the next slice's first
   // MFMAs, column slice t + SB are requested into the stages of slice t, and
   // slice t + 1's first fragments are read under the last MFMAs, so no LDS
-  // latency shows at the slice boundary.  The requests go between the LDS
-  // reads, one at a time: in one run they hold up the MFMAs behind them (the
-  // four waves' 64 requests of a 256 x 256 slice take the address unit half
-  // the slice's time).  Row slice t + 1 and column slice t + 1 come before row
+  // latency shows at the slice boundary.  Row slice t + 1 and column slice t + 1 come before row
   // slices t + 2 .. t + SA - 1 and column slices t + 2 .. t + SB - 1 in the
   // order of requests; only those may still be outstanding at the wait.
-  auto nothing = [](int) {};
 #pragma unroll
   for (int t = 0; t < SB - 1; ++t) {
     if (t < SA - 1) load_rows(t);
@@ -310,18 +291,17 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
   load_rows(SA - 1);
   wait_vmcnt<(SA - 1) * Row::Q + (SB - 2) * Col::Q>();
   wg_barrier();
-  read(0, 0, 0, nothing);
+#pragma unroll
+  for (int f = 0; f < FM + FN; ++f) read(0, 0, f);
+  constexpr int CQ = (Col::Q + KK - 2) / (KK - 1);  // column requests of one step
   for (int t = 0; t < nk; ++t) {
 #pragma unroll
-    for (int kk = 0; kk + 1 < KK; ++kk) {
-      if (kk == 0) read(t, 1, Col::Q, [&](int q) { load_col(t + SB - 1, q); });
-      else read(t, kk + 1, 0, nothing);
-      mma(kk);
-    }
+    for (int kk = 0; kk + 1 < KK; ++kk)
+      step(kk, t, max(0, min(CQ, Col::Q - kk * CQ)),
+           [&](int q) { load_col(t + SB - 1, kk * CQ + q); });
     wait_vmcnt<(SA - 2) * Row::Q + (SB - 2) * Col::Q>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    read(t + 1, 0, Row::Q, [&](int q) { load_row(t + SA, q); });
-    mma(KK - 1);
+    step(KK - 1, t + 1, Row::Q, [&](int q) { load_row(t + SA, q); });
   }
   wait_vmcnt<0>();  // no load may land after the workgroup ends
 

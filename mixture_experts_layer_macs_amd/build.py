@@ -9,6 +9,7 @@ Packed fp32 instructions are disabled for all device code.
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -42,16 +43,32 @@ def _flags(src: str) -> list:
     return f
 
 
+# Kernels whose loops wait for counted vector-memory instructions: a register
+# spilled to scratch memory would add instructions to the count.
+COUNTED = {"linear.hip": "mma_"}
+
+
+def _check_scratch(src: str, remarks: str) -> None:
+    for name, size in re.findall(r"Function Name: (\S+).*?ScratchSize \[bytes/lane\]: (\d+)",
+                                 remarks, flags=re.S):
+        if COUNTED[src] in name and int(size) != 0:
+            raise RuntimeError(f"{src}: {name} uses {size} bytes of scratch memory per lane; its "
+                               "counted waits need every value in registers")
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
-        cmd = [cc, *_flags(src), "-c", os.path.join(CSRC, src), "-o", obj]
+        report = ["-Rpass-analysis=kernel-resource-usage"] if src in COUNTED else []
+        cmd = [cc, *_flags(src), *report, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")
+        if report:
+            _check_scratch(src, r.stderr)
         if verbose and r.stderr.strip():
             print(r.stderr, file=sys.stderr)
         return obj

@@ -173,10 +173,10 @@ int product_f32(F32Prod a, const Plan& p, float* part, hipStream_t s) {
 // Tile and splits of a bf16 product of M x W outputs: the least time by a
 // model fitted to 4 tiles and up to 16 splits of 50 shapes of all four operand
 // layouts (136 .. 8192 rows, 64 .. 14336 columns, reductions of 64 .. 8192; 9 %
-// rms off, its choice 2 % above the best of each shape in the mean).  Times in
-// us.  Large tiles take a CU each, in rounds: 1.32 per slice of a 256 x 256
-// tile and 8.6 for its output, in proportion to the area, and 3.5 to start;
-// 128 x 128 tiles, up to two on a CU at once, 0.45 per slice and 2.2 for the
+// rms off, its choice 1.5 % above the best of each shape in the mean).  Times
+// in us.  Large tiles take a CU each, in rounds: 1.25 per slice of a 256 x 256
+// tile and 10.1 for its output, in proportion to the area, and 2.3 to start;
+// 128 x 128 tiles, up to two on a CU at once, 0.43 per slice and 2.0 for the
 // output each.  Partial sums cost a launch and their traffic; the column
 // operand streams at 4.5 TB/s at best.
 inline Plan plan(int M, int W, int K) {
@@ -190,11 +190,11 @@ inline Plan plan(int M, int W, int K) {
       const int per = ((K + want - 1) / want + 63) / 64, splits = (K + per * 64 - 1) / (per * 64);
       if (splits != want) continue;
       const double rounds = static_cast<double>((tiles * splits + cus - 1) / cus);
-      const double out = splits > 1 ? 0.63 : 1.0;  // partial sums are stored as they are
-      double us = t < 3 ? rounds * (per * 1.32 * area + 8.6 * area * out + 3.5)
-                        : rounds * (per * 0.45 + 2.2 * out) + 2.3;
+      const double out = splits > 1 ? 0.65 : 1.0;  // partial sums are stored as they are
+      double us = t < 3 ? rounds * (per * 1.25 * area + 10.1 * area * out + 2.3) + 1.0
+                        : rounds * (per * 0.43 + 2.0 * out) + 3.3;
       us = std::max(us, static_cast<double>(W) * K * (2 / 4.5e6));
-      if (splits > 1) us += 3.6 + static_cast<double>(splits) * M * W * (4 / 4.0e6);
+      if (splits > 1) us += 3.3 + splits * (0.4 + static_cast<double>(M) * W * (4 / 3.9e6));
       if (us < best.us) best = Plan{t, splits, us};
     }
   }

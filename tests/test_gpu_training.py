@@ -178,9 +178,9 @@ def test_linear_backward(B, i, dtype):
 # 256 compute units, whole and with the reduction split (bf16: 256 x 256, 256 x
 # 192, 192 x 256, 128 x 128; fp32: 128 x 128, 64 x 64), with edges inside tiles
 # and slices.
-LARGE = [(4440, 2704, 136), (2048, 4096, 8192), (3738, 3232, 64), (8804, 136, 3096),
-         (1711, 6952, 64), (264, 5936, 3920), (8000, 392, 64), (5104, 72, 728), (136, 64, 496),
-         (1100, 1544, 264)]
+LARGE = [(4104, 3080, 512), (2048, 4096, 8192), (3738, 3232, 64), (2304, 2304, 8192),
+         (1711, 6952, 64), (1536, 2048, 8192), (144, 64, 856), (8000, 392, 64), (5104, 72, 728),
+         (136, 64, 496), (1100, 1544, 264)]
 
 
 @pytest.mark.parametrize("m,w,k", LARGE)

@@ -166,7 +166,10 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
   __shared__ double s_prob[WAVES][COLS];
   __shared__ double s_z[WAVES];
   __shared__ int32_t s_n[WAVES];
-  const int lane = lane_id(), wave = threadIdx.x / MOE_WAVE, gl = lane & (GL - 1);
+  const int lane = lane_id(), gl = lane & (GL - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
+  // the token of a lane's group; GL == 64: the same for the wave, in scalar registers
+  const int sub = GL == MOE_WAVE ? 0 : lane / GL;
   for (int j = threadIdx.x; j < N; j += NTHR) s_count[j] = 0;
   __syncthreads();
   constexpr int D = KPL <= 4 ? 4 : KPL <= 8 ? 2 : 1;
@@ -178,25 +181,29 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
     pd[i] = 0.0;
   }
   double zsq = 0.0;
+  float zrun = 0.f;
   int n = 0, since = 0, idnext[D];
-  uint8_t onnext[D];
+  uint32_t onnext[D];
+  // every load of a request is unconditional (a branch around one waits for
+  // all that are in flight): without a mask, bytes that are not looked at
+  const uint8_t* mask_or_any = mask ? mask : reinterpret_cast<const uint8_t*>(logits);
   const int step = gridDim.x * WAVES * TPW;
   auto request = [&](int t, int d) {
     const int u = min(t, T - 1);  // past the end: a token that is not used
-    onnext[d] = mask ? mask[u] : 1;
+    onnext[d] = mask_or_any[u];
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
       const int j = gl + GL * i;
       znext[d][i] = logits[static_cast<size_t>(u) * N + min(j, N - 1)];
     }
-    idnext[d] = gl < k ? ids[static_cast<size_t>(u) * k + gl] : -1;
+    idnext[d] = ids[static_cast<size_t>(u) * k + min(gl, k - 1)];
   };
   auto work = [&](int t, int d) {
     float z[KPL], top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < KPL; ++i) z[i] = gl + GL * i < N ? znext[d][i] : -INFINITY;
     int id = idnext[d];
-    const bool on = t < T && onnext[d] != 0;
+    const bool on = t < T && (mask == nullptr || onnext[d] != 0);
     request(t + D * step, d);
 #pragma unroll
     for (int i = 0; i < KPL; ++i) top = fmaxf(top, z[i]);
@@ -215,14 +222,14 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
       sum += z[i];
     }
     sum = group_sum<GL>(sum);
-    const float inv = __builtin_amdgcn_rcpf(sum), l = top + logf(sum);
+    const float inv = __builtin_amdgcn_rcpf(sum), l = top + __logf(sum);
+    if (some) {  // padding may hold NaN
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) pf[i] += some ? z[i] * inv : 0.f;  // padding may hold NaN
-    if (gl == 0 && t < T) {
-      lse[t] = some ? l : on ? -INFINITY : 0.f;
-      n += on;
-      if (some) zsq += static_cast<double>(l) * l;
+      for (int i = 0; i < KPL; ++i) pf[i] += z[i] * inv;
+      zrun += l * l;
     }
+    n += on;
+    if (gl == 0 && t < T) lse[t] = some ? l : on ? -INFINITY : 0.f;
     if (++since == 32) {  // short fp32 runs, long sums in fp64
       since = 0;
 #pragma unroll
@@ -230,15 +237,22 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
         pd[i] += pf[i];
         pf[i] = 0.f;
       }
+      zsq += zrun;
+      zrun = 0.f;
     }
   };
-  const int t0 = (blockIdx.x * WAVES + wave) * TPW + lane / GL;
+  const int t0 = (blockIdx.x * WAVES + wave) * TPW;
   if (T > 0) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) request(t0 + d * step, d);
-    for (int tb = t0 - lane / GL; tb < T; tb += D * step)
+    for (int d = 0; d < D; ++d) request(t0 + sub + d * step, d);
+    for (int tb = t0; tb < T; tb += D * step)
 #pragma unroll
-      for (int d = 0; d < D; ++d) work(tb + lane / GL + d * step, d);
+      for (int d = 0; d < D; ++d) work(tb + sub + d * step, d);
+  }
+  zsq += zrun;
+  if (gl != 0) {  // every lane of a group counted its tokens
+    zsq = 0.0;
+    n = 0;
   }
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
@@ -321,27 +335,31 @@ __global__ __launch_bounds__(GNTHR) void grad_kernel(
     base[i] = j < N ? static_cast<float>(db * inv * inv * N / k * counts[j]) : 0.f;
   }
   const float zc = static_cast<float>(2.0 * dzl * inv);
+  const int sub = GL == MOE_WAVE ? 0 : lane / GL;
   const int step = gridDim.x * GWAVES * TPW, t0 = (blockIdx.x * GWAVES + wave) * TPW;
-  float znext[KPL], lnext, dgnext = 0.f;
-  int idnext = -1;
-  uint8_t onnext;
+  // unconditional loads, as above; without d_gates, values that are not used
+  const uint8_t* mask_or_any = mask ? mask : reinterpret_cast<const uint8_t*>(logits);
+  const int32_t* id_or_any = d_gates ? ids : reinterpret_cast<const int32_t*>(logits);
+  const float* dg_or_any = d_gates ? d_gates : logits;
+  float znext[KPL], lnext, dgnext;
+  int idnext;
+  uint32_t onnext;
   auto request = [&](int t) {
     const int u = min(t, T - 1);  // past the end: a token that is not used
-    onnext = mask ? mask[u] : 1;
+    onnext = mask_or_any[u];
     lnext = lse[u];
 #pragma unroll
     for (int i = 0; i < KPL; ++i)
       znext[i] = logits[static_cast<size_t>(u) * N + min(gl + GL * i, N - 1)];
-    if (d_gates && gl < k) {
-      idnext = ids[static_cast<size_t>(u) * k + gl];
-      dgnext = d_gates[static_cast<size_t>(u) * k + gl];
-    }
+    // k <= N: the substitute's T x k elements lie inside the logits
+    idnext = id_or_any[static_cast<size_t>(u) * k + min(gl, k - 1)];
+    dgnext = dg_or_any[static_cast<size_t>(u) * k + min(gl, k - 1)];
   };
-  request(t0 + lane / GL);
+  request(t0 + sub);
   for (int tb = t0; tb < T; tb += step) {
-    const int t = tb + lane / GL;
+    const int t = tb + sub;
     const float l = lnext;
-    const bool on = onnext != 0 && l != -INFINITY;
+    const bool on = (mask == nullptr || onnext != 0) && l != -INFINITY;
     int id = idnext;
     float dg = dgnext;
     float p[KPL], u[KPL];

@@ -8,6 +8,7 @@
 // act "swiglu" takes W [2O,K], gate rows first: y = silu(z[:, :O]) z[:, O:].
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "common.h"
 #include "linear_common.h"
@@ -129,7 +130,8 @@ inline Plan plan_f32(int M, int W, int K, bool strided) {
     for (int want = 1; want <= (tile == 32 ? 1 : 8); ++want) {
       const int per = ((K + want - 1) / want + 31) / 32 * 32, splits = (K + per - 1) / per;
       if (splits != want) continue;
-      const double load = tiles * splits / cu_count();
+      double load = tiles * splits / cu_count();
+      if (load <= 4) load = std::ceil(load);  // the fullest CU sets the time
       const double alone = tile == 32 ? (strided ? 0.011 : 0.009) : tile == 64 ? 0.028 : 0.084;
       const double shared = tile == 32 ? alone : tile == 64 ? 0.025 : 0.068;
       double us = 2.8 + std::min(K, per) * std::max(alone, load * shared);

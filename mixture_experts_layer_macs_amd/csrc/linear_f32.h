@@ -118,8 +118,8 @@ __global__ __launch_bounds__(256) void f32_pair_kernel(F32Prod dx, F32Prod dw, B
 }
 
 // Large outputs: tiles of 64 F x 64 F (F = 1 or 2), 4 waves of 32 F x 32 F,
-// slices of 32 / F k through two LDS buffers laid out [k][m], the next slice's
-// loads in flight in registers while one is multiplied.  A slice is 16 F MFMAs
+// slices of 32 / F k through two LDS buffers laid out [k][m], the next two
+// slices' loads in flight in registers while one is multiplied.  A slice is 16 F MFMAs
 // of 64 cycles per wave, so the LDS traffic stays below the matrix pipe's time.
 template <bool STRIDED, bool MIX, int F>
 struct F32Stage {
@@ -176,11 +176,11 @@ __global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
   const float* r = p.r + (RS ? m0 : m0 * p.ldr);
   const float* c = p.c + (CS ? n0 : n0 * p.ldc);
   const int mv = p.M - m0, nv = p.N - n0;
-  Row row;
-  Col col;
-  auto fetch = [&](int k0) {
-    row.fetch(r, p.ldr, mv, k0, k_hi, 0);
-    col.fetch(c, p.ldc, nv, k0, k_hi, GLU ? p.N * p.ldc : 0);
+  Row row[2];
+  Col col[2];
+  auto fetch = [&](int set, int k0) {
+    row[set].fetch(r, p.ldr, mv, k0, k_hi, 0);
+    col[set].fetch(c, p.ldc, nv, k0, k_hi, GLU ? p.N * p.ldc : 0);
   };
   f32x16 acc[F][F];
 #pragma unroll
@@ -190,28 +190,33 @@ __global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[x][y][i] = 0.f;
   const int ml = wm * 32 * F + (lane & 31), nl = wn * 32 * F + (lane & 31), kl = lane >> 5;
-  fetch(k_lo);
-  int buf = 0;
-  for (int k0 = k_lo; k0 < k_hi; k0 += BK, buf ^= 1) {
-    row.put(sr[buf]);
-    col.put(sc[buf]);
-    __syncthreads();
-    if (k0 + BK < k_hi) fetch(k0 + BK);
-    const float *a = sr[buf], *b = sc[buf];
+  // Slices past the end fetch zeros without touching memory.
+  fetch(0, k_lo);
+  fetch(1, k_lo + BK);
+  for (int k0 = k_lo; k0 < k_hi; k0 += 2 * BK) {
 #pragma unroll
-    for (int k = 0; k < BK; k += 2) {
-      float fr[F], fc[F];
+    for (int set = 0; set < 2; ++set) {
+      if (set && k0 + BK >= k_hi) break;
+      row[set].put(sr[set]);
+      col[set].put(sc[set]);
+      __syncthreads();
+      fetch(set, k0 + (set + 2) * BK);
+      const float *a = sr[set], *b = sc[set];
 #pragma unroll
-      for (int x = 0; x < F; ++x) fr[x] = a[(k + kl) * PITCH + ml + 32 * x];
+      for (int k = 0; k < BK; k += 2) {
+        float fr[F], fc[F];
 #pragma unroll
-      for (int y = 0; y < F; ++y) fc[y] = b[(k + kl) * PITCH + nl + 32 * y];
+        for (int x = 0; x < F; ++x) fr[x] = a[(k + kl) * PITCH + ml + 32 * x];
 #pragma unroll
-      for (int x = 0; x < F; ++x)
+        for (int y = 0; y < F; ++y) fc[y] = b[(k + kl) * PITCH + nl + 32 * y];
 #pragma unroll
-        for (int y = 0; y < F; ++y)
-          acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x2f32(fc[y], fr[x], acc[x][y], 0, 0, 0);
+        for (int x = 0; x < F; ++x)
+#pragma unroll
+          for (int y = 0; y < F; ++y)
+            acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x2f32(fc[y], fr[x], acc[x][y], 0, 0, 0);
+      }
+      // the buffer written next was last read before this slice's barrier
     }
-    // the buffer written next was last read before this iteration's barrier
   }
 #pragma unroll
   for (int x = 0; x < F; ++x) {

@@ -635,8 +635,9 @@ int moe_combine_dropout(const void* out_rows, const int32_t* slot_row,
  * (the residual's gradient is dy).  The m dy of a row stays in fp32.
  *
  * dy          [T,H] (dtype).
- * d_out_rows  [T*k,H] out (dtype): the rows that a slot names; the others
- *             are left as they were.  May be NULL.
+ * d_out_rows  [T*k,H] out (dtype): the rows that a slot names (each is named
+ *             by one slot, as moe_dispatch writes slot_row); the others are
+ *             left as they were.  May be NULL.
  * d_gates     f32[T,k] out: 0 for dropped slots.  May be NULL, not both.
  * out_rows may be NULL without d_gates.  Errors and alignment as
  * moe_combine_dropout.  One launch; T == 0 enqueues nothing.

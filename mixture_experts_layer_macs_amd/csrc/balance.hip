@@ -7,8 +7,12 @@
 //   z loss  = (1/n) sum_t lse_t^2
 //   dz_tj   = p_tj (u_tj - sum_i p_ti u_ti) + dL/dz_loss 2 lse_t p_tj / n,
 //   u_tj    = dL/dbalance N c_j / (k n^2) + sum_{s: id_ts = j} dL/dgate_ts
-// (the counts carry no gradient).  Both passes read the logits once; a wave
-// owns a token, its N logits in registers.
+// (the counts carry no gradient).  Both passes read the logits once, a token's
+// N logits in the registers of a group of 8 to 64 lanes.
+//
+// Measured: 65521 tokens, 256 experts: loss 21.7 us (67 MB, 3.1 TB/s) and 6.9
+// for the second launch, gradient 32.8 us (134 MB, 4.1 TB/s); a large copy
+// runs at 4.8 TB/s.  128 tokens, 128 experts: 8.4 and 4.0 us, latency.
 #include <algorithm>
 #include <type_traits>
 

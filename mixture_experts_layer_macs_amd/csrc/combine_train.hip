@@ -12,7 +12,12 @@
 //
 // Both passes are bound by HBM: the k expert rows of a token are read (and in
 // the backward pass written) once.  A power-of-two group of threads owns a
-// token, 16 bytes of a row per thread and step.
+// token, 16 bytes of a row per thread and step, up to 8 rows in flight; the
+// mask's integer work runs while they are.
+//
+// Measured, 8192 tokens of 8 rows of 2048 bf16, p = 0.1: forward with residual
+// 63 us (322 MB, 5.1 TB/s; a plain read of 268 MB takes 59), the same without
+// dropout; backward 111 us (543 MB, 4.9 TB/s; a large copy runs at 4.8).
 #include "common.h"
 
 namespace moe {
@@ -164,8 +169,7 @@ __global__ __launch_bounds__(NTHR) void forward_kernel(
   }
 }
 
-// Sum of v over the tpt threads of a token (a power of two); red: LDS, one
-// float per wave and slot.  Every thread of the workgroup takes part.
+// Sum of v over the threads of a token (tpt, a power of two) in this wave.
 __device__ __forceinline__ float wave_part(float v, int tpt) {
   for (int m = 1; m < tpt && m < MOE_WAVE; m *= 2) v += __shfl_xor(v, m, MOE_WAVE);
   return v;

@@ -125,12 +125,13 @@ int product(Mma a, const Plan& p, float* part, hipStream_t s) {
 // with 32 x 32, 34 with 128 x 128 in four splits; 512^3: 7.3, 10.3 and 15.4.
 inline Plan plan_f32(int M, int W, int K, bool strided) {
   Plan best{32, 1, 1e30};
+  const double cus = cu_count();
   for (int tile = 32; tile <= 128; tile *= 2) {
     const double tiles = static_cast<double>((M + tile - 1) / tile) * ((W + tile - 1) / tile);
     for (int want = 1; want <= (tile == 32 ? 1 : 8); ++want) {
       const int per = ((K + want - 1) / want + 31) / 32 * 32, splits = (K + per - 1) / per;
       if (splits != want) continue;
-      double load = tiles * splits / cu_count();
+      double load = tiles * splits / cus;
       if (load <= 4) load = std::ceil(load);  // the fullest CU sets the time
       const double alone = tile == 32 ? (strided ? 0.011 : 0.009) : tile == 64 ? 0.028 : 0.084;
       const double shared = tile == 32 ? alone : tile == 64 ? 0.025 : 0.068;
@@ -209,15 +210,16 @@ inline Plan plan(int M, int W, int K) {
 // best (sweep of 7 weights of 256 x 4096 .. 14336 x 4096, 1 .. 512 tokens).
 // 768 x 2048: 3.9 us for 1 token, 6.1 for 128 (tiles: 9.6); 4096 x 14336: 24
 // for 1 token, but 145 for 128, where two splits of 128 x 128 tiles take 36.
-// Returns the fragments of 16 tokens per workgroup; 0: tiles.
-inline int skinny_plan(int T, int K, int W) {
+// least: the tiles' estimate.  Returns the fragments of 16 tokens per
+// workgroup; 0: tiles.
+inline int skinny_plan(int T, int K, int W, double least) {
   int best = 0;
   if (T > 128) return best;
-  double least = plan(T, W, K).us;
+  const double cus = cu_count();
   for (int rf = 1; rf <= 8; rf *= 2) {
     if (rf > 1 && T <= rf * 8) break;  // half the fragments would be empty
     const double wgs = static_cast<double>((W + 15) / 16) * ((T + rf * 16 - 1) / (rf * 16));
-    const double turns = std::max(1.0, wgs / cu_count()) * K / 512.0;
+    const double turns = std::max(1.0, wgs / cus) * K / 512.0;
     const double full = 0.25 + 0.75 * std::min(1.0, T / (16.0 * rf));
     const double us = 3.0 + std::max(turns * 0.25, static_cast<double>(W) * K * (2 / 5.5e6)) +
                       turns * 0.4 * rf * full;
@@ -266,7 +268,8 @@ __device__ __forceinline__ void act_grad(const E* dy, const E* z, int O, int act
 }
 
 // dz rounded to the element type, the operand of both products: 16 bytes of
-// dy's columns per thread.  Bound by HBM: dy and z read, dz written once.
+// dy's columns per thread.  Bound by HBM: dy and z read, dz written once (8192 x
+// 768 swiglu: 13 us, 63 MB, 4.8 TB/s).
 template <typename D>
 __global__ __launch_bounds__(256) void act_grad_kernel(const typename D::elem* __restrict__ dy,
                                                        const typename D::elem* __restrict__ z,
@@ -375,6 +378,26 @@ inline size_t part_bytes(const Plan& p, int M, int W) {
   return p.splits > 1 ? up256(static_cast<size_t>(p.splits) * M * W * 4) : 0;
 }
 
+struct ForwardPlan {
+  Plan p;
+  int rf;  // of the skinny product; 0: tiles
+  size_t bytes;
+};
+
+inline ForwardPlan forward_plan(int T, int K, int O, int act, int dtype) {
+  ForwardPlan f{Plan{}, 0, 256};
+  if (T == 0) return f;
+  const int W = width(O, act);
+  if (dtype == MOE_BF16) {
+    f.p = plan(T, W, K);
+    f.rf = skinny_plan(T, K, W, f.p.us);
+  } else {
+    f.p = plan_f32(T, W, K, false);
+  }
+  if (!f.rf) f.bytes += part_bytes(f.p, T, W);
+  return f;
+}
+
 inline BackPlan back_plan(int T, int K, int O, int act, int dtype) {
   BackPlan p{};
   const int W = width(O, act);
@@ -458,8 +481,8 @@ inline int products(const F32Prod& x, const F32Prod& w, const BackPlan& p, BiasS
 }
 
 template <typename D, typename P>
-int backward(const void* dy, const void* x, const void* w, const void* z, int T, int K, int O,
-             int act, int dtype, void* dx, void* dw, void* dbias, char* ws, hipStream_t s) {
+int backward(const BackPlan& p, const void* dy, const void* x, const void* w, const void* z, int T,
+             int K, int O, int act, void* dx, void* dw, void* dbias, char* ws, hipStream_t s) {
   typedef typename D::elem E;
   const int W = width(O, act);
   if (T == 0) {  // sums over no tokens
@@ -472,7 +495,6 @@ int backward(const void* dy, const void* x, const void* w, const void* z, int T,
                          static_cast<size_t>(W));
     return launch_status();
   }
-  const BackPlan p = back_plan(T, K, O, act, dtype);
   const void* dz = dy;
   BiasSum b{reinterpret_cast<float*>(ws + p.sums), p.blocks, W, dbias};
   if ((act != MOE_ACT_NONE && (dx || dw)) || dbias) {
@@ -506,9 +528,7 @@ using namespace moe::lin;
 
 extern "C" size_t moe_linear_workspace_size(int T, int K, int O, int act, int dtype) {
   if (check(T, K, O, act, dtype) != MOE_OK) return 0;
-  if (T == 0 || (dtype == MOE_BF16 && skinny_plan(T, K, width(O, act)))) return 256;
-  const int W = width(O, act);
-  return 256 + part_bytes(dtype == MOE_BF16 ? plan(T, W, K) : plan_f32(T, W, K, false), T, W);
+  return forward_plan(T, K, O, act, dtype).bytes;
 }
 
 extern "C" int moe_linear(const void* x, const void* w, const void* bias, const void* residual,
@@ -520,16 +540,16 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
   for (const void* q : {x, w, bias, residual, static_cast<const void*>(z),
                         static_cast<const void*>(y), static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MOE_EINVAL;
-  if (workspace_bytes < moe_linear_workspace_size(T, K, O, act, dtype)) return MOE_EINVAL;
+  const ForwardPlan f = forward_plan(T, K, O, act, dtype);
+  if (workspace_bytes < f.bytes) return MOE_EINVAL;
   hipStream_t s = as_stream(stream);
   const bool glu = act == MOE_ACT_SWIGLU;
   const Epilogue e{bias, residual, z, y, act};
   float* part = static_cast<float*>(workspace);
-  const int rf = dtype == MOE_BF16 ? skinny_plan(T, K, width(O, act)) : 0;
   int r;
-  if (rf) {
+  if (f.rf) {
     const Skinny q{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), T, K, O, 0, 0, e};
-    r = glu ? launch_skinny<true>(q, rf, s) : launch_skinny<false>(q, rf, s);
+    r = glu ? launch_skinny<true>(q, f.rf, s) : launch_skinny<false>(q, f.rf, s);
   } else if (dtype == MOE_BF16) {
     Mma q{};
     q.r = static_cast<const uint16_t*>(x);
@@ -539,8 +559,8 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
     q.N = O;
     q.K = K;
     q.e = e;
-    const Plan p = plan(T, width(O, act), K);
-    r = glu ? product<false, false, true>(q, p, part, s) : product<false, false, false>(q, p, part, s);
+    r = glu ? product<false, false, true>(q, f.p, part, s)
+            : product<false, false, false>(q, f.p, part, s);
   } else {
     F32Prod q{};
     q.r = static_cast<const float*>(x);
@@ -550,9 +570,8 @@ extern "C" int moe_linear(const void* x, const void* w, const void* bias, const 
     q.N = O;
     q.K = K;
     q.e = e;
-    const Plan p = plan_f32(T, width(O, act), K, false);
-    r = glu ? product_f32<false, false, true>(q, p, part, s)
-            : product_f32<false, false, false>(q, p, part, s);
+    r = glu ? product_f32<false, false, true>(q, f.p, part, s)
+            : product_f32<false, false, false>(q, f.p, part, s);
   }
   return r == MOE_OK ? launch_status() : r;
 }
@@ -574,11 +593,11 @@ extern "C" int moe_linear_backward(const void* dy, const void* x, const void* w,
   for (const void* q : {dy, x, w, z, static_cast<const void*>(dx), static_cast<const void*>(dw),
                         static_cast<const void*>(dbias), static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MOE_EINVAL;
-  if (T > 0 && workspace_bytes < moe_linear_backward_workspace_size(T, K, O, act, dtype))
-    return MOE_EINVAL;
+  const BackPlan p = back_plan(T, K, O, act, dtype);
+  if (T > 0 && workspace_bytes < p.bytes) return MOE_EINVAL;
   char* ws = static_cast<char*>(workspace);
   hipStream_t s = as_stream(stream);
   if (dtype == MOE_BF16)
-    return backward<Bf16, Mma>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
-  return backward<F32, F32Prod>(dy, x, w, z, T, K, O, act, dtype, dx, dw, dbias, ws, s);
+    return backward<Bf16, Mma>(p, dy, x, w, z, T, K, O, act, dx, dw, dbias, ws, s);
+  return backward<F32, F32Prod>(p, dy, x, w, z, T, K, O, act, dx, dw, dbias, ws, s);
 }

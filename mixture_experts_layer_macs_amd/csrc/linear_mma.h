@@ -16,6 +16,12 @@
 //
 // v_mfma_f32_32x32x16_bf16 with the column operand as A: a lane ends with four
 // consecutive output columns of one row.
+//
+// Bound by the matrix pipe at the clock that its power allows (1.6 to 1.75 GHz
+// in a long product, 77 % of its cycles busy; what is left is waiting for the
+// ring).  Measured: 8192 x 2048 -> 768 swiglu with z kept 47 us (1.10 PFLOP/s);
+// 4096 x 4096 -> 14336 410 us (1.17 PFLOP/s; the library's plain product 406),
+// 445 with gelu.
 #pragma once
 
 #include "common.h"

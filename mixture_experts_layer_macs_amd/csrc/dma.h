@@ -70,15 +70,4 @@ __device__ __forceinline__ void wait_vmcnt() {
 // only by the DMA loads, whose completion each wave has already waited for.
 __device__ __forceinline__ void wg_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
-// Scheduling groups of one sub-slice: its NMF MFMAs split as evenly as
-// possible over its NFR fragment reads, one read after each group.
-template <int NMF, int NFR, int I = 0>
-__device__ __forceinline__ void interleave_groups() {
-  if constexpr (I < NFR) {
-    __builtin_amdgcn_sched_group_barrier(0x0008, NMF / NFR + (I < NMF % NFR ? 1 : 0), 0);
-    __builtin_amdgcn_sched_group_barrier(0x0100, 1, 0);  // DS read
-    interleave_groups<NMF, NFR, I + 1>();
-  }
-}
-
 }  // namespace moe

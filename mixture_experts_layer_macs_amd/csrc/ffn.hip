@@ -260,6 +260,17 @@ __device__ __forceinline__ void locate_regs(const Args& a, const TileRegs& tr, i
 // The DMA helpers (buffer resource, direct-to-LDS load, counted waits) are
 // in dma.h.
 
+// Scheduling groups of one sub-slice: its NMF MFMAs split as evenly as
+// possible over its NFR fragment reads, one read after each group.
+template <int NMF, int NFR, int I = 0>
+__device__ __forceinline__ void interleave_groups() {
+  if constexpr (I < NFR) {
+    __builtin_amdgcn_sched_group_barrier(0x0008, NMF / NFR + (I < NMF % NFR ? 1 : 0), 0);
+    __builtin_amdgcn_sched_group_barrier(0x0100, 1, 0);  // DS read
+    interleave_groups<NMF, NFR, I + 1>();
+  }
+}
+
 // The tile of expert j, rows m0 .. m0 + BM - 1 of its Mj rows (dispatch rows
 // from row0), column tile nt, computed by WM x WN waves (4 or 8) with an
 // S-stage ring in smem (the dynamic LDS block).  All five values are the

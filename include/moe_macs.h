@@ -535,7 +535,7 @@ int moe_linear(const void* x, const void* w, const void* bias,
  *           without dx).
  * z         moe_linear's z; unused and may be NULL for MOE_ACT_NONE.
  * dx        [T,K], dw as w, dbias [O] ([2O]): out (dtype), overwritten; each
- *           may be NULL to skip it, not all three.
+ *           may be NULL to skip it, not all three (T == 0: any).
  * dz is rounded to dtype for the two products (bf16 operands, fp32 sums);
  * dbias sums the unrounded values in fp32.  T == 0 writes zeros to dw and
  * dbias.  Workspace of moe_linear_backward_workspace_size() bytes (scratch
@@ -638,7 +638,8 @@ int moe_combine_dropout(const void* out_rows, const int32_t* slot_row,
  * d_out_rows  [T*k,H] out (dtype): the rows that a slot names (each is named
  *             by one slot, as moe_dispatch writes slot_row); the others are
  *             left as they were.  May be NULL.
- * d_gates     f32[T,k] out: 0 for dropped slots.  May be NULL, not both.
+ * d_gates     f32[T,k] out: 0 for dropped slots.  May be NULL, not both
+ *             (T == 0: any).
  * out_rows may be NULL without d_gates.  Errors and alignment as
  * moe_combine_dropout.  One launch; T == 0 enqueues nothing.
  */

@@ -311,9 +311,8 @@ extern "C" int moe_combine_backward(const void* dy, const void* out_rows,
                                     void* d_out_rows, float* d_gates, void* stream) {
   Drop drop;
   const int rc = check(T, k, H, dtype, p, rng, &drop);
-  if (rc != MOE_OK) return rc;
+  if (rc != MOE_OK || T == 0) return rc;  // empty outputs may have null addresses
   if (!d_out_rows && !d_gates) return MOE_EINVAL;
-  if (T == 0) return MOE_OK;
   if (!dy || !slot_row || !topk_gates || (d_gates && !out_rows)) return MOE_EINVAL;
   if (!aligned16(dy) || !aligned16(out_rows) || !aligned16(d_out_rows)) return MOE_EINVAL;
   hipStream_t s = as_stream(stream);

@@ -590,9 +590,9 @@ extern "C" int moe_linear_backward(const void* dy, const void* x, const void* w,
                                    void* stream) {
   const int rc = check(T, K, O, act, dtype);
   if (rc != MOE_OK) return rc;
-  if (!dx && !dw && !dbias) return MOE_EINVAL;
-  if (T > 0 && (!dy || (act != MOE_ACT_NONE && !z) || (dx && !w) || (dw && !x) || !workspace))
-    return MOE_EINVAL;
+  if (T > 0 && ((!dx && !dw && !dbias) || !dy || (act != MOE_ACT_NONE && !z) || (dx && !w) ||
+                (dw && !x) || !workspace))
+    return MOE_EINVAL;  // without tokens dx is empty and its address may be null
   for (const void* q : {dy, x, w, z, static_cast<const void*>(dx), static_cast<const void*>(dw),
                         static_cast<const void*>(dbias), static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MOE_EINVAL;

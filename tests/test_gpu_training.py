@@ -271,6 +271,27 @@ def test_linear_backward_without_tokens_writes_zeros(B, dtype):
     assert (dw == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_backward_calls_without_tokens(B, dtype):
+    """An empty batch through the binding: each empty gradient alone and all of
+    them; the sums over tokens are zeros."""
+    e = lambda *s: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+    w, ws = torch.ones(48, 64, dtype=dtype, device="cuda"), B.new_workspace(0, "cuda")
+    dx, _, _ = B.moe_linear_backward(e(0, 48), e(0, 64), w, ws, dx=e(0, 64))
+    assert dx.shape == (0, 64)
+    dw, db = torch.ones_like(w), torch.ones(48, dtype=dtype, device="cuda")
+    B.moe_linear_backward(e(0, 48), e(0, 64), w, ws, z=e(0, 48), act="gelu", dx=e(0, 64), dw=dw, dbias=db)
+    assert (dw == 0).all() and (db == 0).all()
+    S, G = torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda")
+    for dr, dg in ((e(0, 64), None), (None, torch.empty_like(G)), (e(0, 64), torch.empty_like(G))):
+        B.moe_combine_backward(e(0, 64), e(0, 64), S, G, d_out_rows=dr, d_gates=dg)
+    assert B.moe_combine_dropout(e(0, 64), S, G, residual=e(0, 64)).shape == (0, 64)
+    out = B.moe_balance_loss(torch.empty(0, 16, device="cuda"), S, B.new_workspace(
+        B.moe_balance_workspace_size(0, 16), "cuda"))
+    assert B.moe_router_backward(torch.empty(0, 16, device="cuda"), S, out["lse"], out["counts"],
+                                 d_gates=G, dtype=dtype).shape == (0, 16)
+
+
 def test_linear_gradient_against_the_kernels_own_differences(B):
     """The fp32 forward kernel's difference quotient along a direction equals
     the 64-bit one up to the forward's rounding over 2h."""

@@ -133,6 +133,20 @@ def test_combine_refusals(lib, kw, rc):
                                     a["out"], a["out2"], None) == rc
 
 
+def test_no_tokens_with_empty_outputs(lib):
+    """An empty tensor has a null address: without tokens, outputs of T rows may
+    be null and nothing is asked of them."""
+    assert _linear_bwd(lib, T=0, dy=None, x=None, z=None, dx=None, dw=None, db=None, size=0, ws=None) == OK
+    assert lib.moe_combine_backward(None, None, None, None, 0.0, None, 0, 2, 64, BF16, None, None,
+                                    None) == OK
+    assert lib.moe_combine_backward(None, None, None, None, 0.5, None, 0, 2, 64, F32, None, None,
+                                    None) == OK
+    # the other arguments are looked at all the same
+    assert _linear_bwd(lib, T=0, K=60, dx=None, dw=None, db=None) == EUNSUP
+    assert lib.moe_combine_backward(None, None, None, None, 1.0, None, 0, 2, 64, BF16, None, None,
+                                    None) == EINVAL
+
+
 def test_binding_refuses_host_tensors_and_names():
     from mixture_experts_layer_macs_amd import binding as B
     x, w = torch.zeros(4, 64), torch.zeros(32, 64)

@@ -49,9 +49,14 @@ COUNTED = {"linear.hip": "mma_"}
 
 
 def _check_scratch(src: str, remarks: str) -> None:
-    for name, size in re.findall(r"Function Name: (\S+).*?ScratchSize \[bytes/lane\]: (\d+)",
-                                 remarks, flags=re.S):
-        if COUNTED[src] in name and int(size) != 0:
+    found = [(name, size) for name, size in re.findall(
+        r"Function Name: (\S+).*?ScratchSize \[bytes/lane\]: (\d+)", remarks, flags=re.S)
+        if COUNTED[src] in name]
+    if not found:  # a renamed kernel, or remarks in another form
+        raise RuntimeError(f"{src}: the compiler's remarks name no kernel {COUNTED[src]!r}, so its use "
+                           "of scratch memory is not known")
+    for name, size in found:
+        if int(size) != 0:
             raise RuntimeError(f"{src}: {name} uses {size} bytes of scratch memory per lane; its "
                                "counted waits need every value in registers")
 

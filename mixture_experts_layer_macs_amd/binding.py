@@ -604,17 +604,26 @@ def moe_linear_backward(dy, x, w, workspace, z=None, act="none", dx=None, dw=Non
                         dbias=None):
     """Fills those of dx [T,K], dw (as w) and dbias [rows of w] that are given
     with the gradients of moe_linear; z is moe_linear's (not needed for act
-    "none")."""
-    code, dt, d = _act(act), _elem(x.dtype), x.dtype
-    T, K, O, W = _linear_shapes(x, w, act)
+    "none").  x may be None without dw, and w without dx (not both: K is
+    theirs)."""
+    code, dt, d = _act(act), _elem(dy.dtype), dy.dtype
+    T, O = dy.shape
+    W = 2 * O if act == "swiglu" else O
+    if x is None and w is None:
+        raise ValueError("x or w is needed")
+    K = (w if x is None else x).shape[1]
     if z is None and code != 0 and T > 0:
         raise ValueError(f"act {act!r} needs moe_linear's z")
     if dx is None and dw is None and dbias is None:
         raise ValueError("no gradient asked for")
-    here = _here(x, "x")
+    if dx is not None and w is None:
+        raise ValueError("dx needs w")
+    if dw is not None and x is None:
+        raise ValueError("dw needs x")
+    here = _here(dy, "dy")
     _check(_lib.moe_linear_backward(
-        _arg(dy, d, "dy", (T, O), here), _arg(x, d, "x", (T, K), here),
-        _arg(w, d, "w", (W, K), here), _arg_opt(z, d, "z", (T, W), here), T, K, O, code, dt,
+        _arg(dy, d, "dy", (T, O), here), _arg_opt(x, d, "x", (T, K), here),
+        _arg_opt(w, d, "w", (W, K), here), _arg_opt(z, d, "z", (T, W), here), T, K, O, code, dt,
         _arg_opt(dx, d, "dx", (T, K), here), _arg_opt(dw, d, "dw", (W, K), here),
         _arg_opt(dbias, d, "dbias", (W,), here), *_work(workspace, here), _raw_stream(here)),
         "moe_linear_backward")
@@ -648,17 +657,25 @@ def moe_balance_loss(logits, slot_ids, workspace, token_mask=None, out=None):
 
 
 def moe_router_backward(logits, topk_ids, lse, counts, d_losses=None, token_mask=None,
-                        d_gates=None, dlogits=None, dtype=torch.float32):
+                        d_gates=None, dlogits=None, dtype=torch.float32, k=None):
     """Gradient of the router's logits through moe_balance_loss (d_losses [2])
-    and through the gates (d_gates [T,k]); dtype is that of a new dlogits."""
+    and through the gates (d_gates [T,k]); dtype is that of a new dlogits.
+    topk_ids may be None without d_gates; k, the slots per token, is needed
+    then."""
     T, N = logits.shape
-    k = topk_ids.shape[1]
+    if topk_ids is not None:
+        k = topk_ids.shape[1]
+    elif d_gates is not None:
+        raise ValueError("d_gates needs topk_ids")
+    elif k is None:
+        raise ValueError("without topk_ids, k is needed")
     f32, i32 = torch.float32, torch.int32
     here = _here(logits, "logits")
     if dlogits is None:
         dlogits = _empty((T, N), dtype, logits)
     _check(_lib.moe_router_backward(
-        _arg(logits, f32, "logits", (T, N), here), _arg(topk_ids, i32, "topk_ids", (T, k), here),
+        _arg(logits, f32, "logits", (T, N), here),
+        _arg_opt(topk_ids, i32, "topk_ids", (T, k), here),
         _arg_opt(token_mask, torch.uint8, "token_mask", (T,), here),
         _arg(lse, f32, "lse", (T,), here), _arg(counts, i32, "counts", (N + 1,), here),
         _arg_opt(d_losses, f32, "d_losses", (2,), here),
@@ -695,14 +712,17 @@ def moe_combine_dropout(out_rows, slot_row, topk_gates, p=0.0, rng=None, residua
 def moe_combine_backward(dy, out_rows, slot_row, topk_gates, p=0.0, rng=None,
                          d_out_rows=None, d_gates=None):
     """Fills those of d_out_rows [T*k,H] (rows that a slot names) and d_gates
-    [T,k] that are given with the gradients of moe_combine_dropout."""
+    [T,k] that are given with the gradients of moe_combine_dropout.  out_rows
+    may be None without d_gates."""
     T, k = slot_row.shape
-    H, d = out_rows.shape[1], out_rows.dtype
+    H, d = dy.shape[1], dy.dtype
     if d_out_rows is None and d_gates is None:
         raise ValueError("no gradient asked for")
-    dt, here = _elem(d), _here(out_rows, "out_rows")
+    if d_gates is not None and out_rows is None:
+        raise ValueError("d_gates needs out_rows")
+    dt, here = _elem(d), _here(dy, "dy")
     _check(_lib.moe_combine_backward(
-        _arg(dy, d, "dy", (T, H), here), _arg(out_rows, d, "out_rows", (T * k, H), here),
+        _arg(dy, d, "dy", (T, H), here), _arg_opt(out_rows, d, "out_rows", (T * k, H), here),
         _arg(slot_row, torch.int32, "slot_row", (T, k), here),
         _arg(topk_gates, torch.float32, "topk_gates", (T, k), here), p, _rng(rng, p, here), T, k,
         H, dt, _arg_opt(d_out_rows, d, "d_out_rows", (T * k, H), here),

@@ -692,6 +692,35 @@ def test_tuning_steps_captured_with_one_workspace(B):
     assert not torch.equal(seen[0], seen[2])  # another offset, another mask
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_gradients_without_the_inputs_they_do_not_need(B, dtype):
+    """dx without x, dw and dbias without w, d_out_rows without out_rows, the
+    losses' gradient without topk_ids: the same bits as with them."""
+    T, K, O = 70, 72, 136
+    g, x, w, _, _ = _linear_inputs(T, K, O, "silu", dtype, 21, False, False)
+    dy, z = _rand(g, (T, O), 0.5, dtype), _rand(g, (T, O), 1.0, dtype)
+    ws = B.new_workspace(B.moe_linear_backward_workspace_size(T, K, O, "silu", dtype), "cuda")
+    e = torch.empty_like
+    for names, xa, wa in ((("dx",), None, w), (("dw", "dbias"), x, None), (("dbias",), None, w)):
+        full = {n: {"dx": e(x), "dw": e(w), "dbias": e(w[:, 0])}[n] for n in names}
+        part = {n: e(t) for n, t in full.items()}
+        B.moe_linear_backward(dy, x, w, ws, z=z, act="silu", **full)
+        B.moe_linear_backward(dy, xa, wa, ws, z=z, act="silu", **part)
+        assert all(torch.equal(full[n], part[n]) for n in names)
+    g, rows, slot_row, gates = _combine_inputs(9, 64, 3, dtype, 4)
+    S, G, dyc = torch.from_numpy(slot_row).cuda(), torch.from_numpy(gates).cuda(), _rand(g, (9, 64), 1.0, dtype)
+    a, b = torch.zeros_like(rows), torch.zeros_like(rows)
+    B.moe_combine_backward(dyc, rows, S, G, d_out_rows=a)
+    B.moe_combine_backward(dyc, None, S, G, d_out_rows=b)
+    assert torch.equal(a, b)
+    _, logits, ids = _balance_inputs(33, 20, 3, 6)
+    L, ids = torch.from_numpy(logits).cuda(), torch.from_numpy(ids).cuda()
+    out = B.moe_balance_loss(L, ids, B.new_workspace(B.moe_balance_workspace_size(33, 20), "cuda"))
+    dl = torch.tensor([0.5, 0.25], device="cuda")
+    assert torch.equal(B.moe_router_backward(L, ids, out["lse"], out["counts"], dl, dtype=dtype),
+                       B.moe_router_backward(L, None, out["lse"], out["counts"], dl, dtype=dtype, k=3))
+
+
 def test_binding_refusals_on_the_gpu(B):
     x, w = torch.zeros(4, 64, device="cuda"), torch.zeros(32, 64, device="cuda")
     ws = B.new_workspace(1 << 16, "cuda")

@@ -174,6 +174,26 @@ def test_binding_refuses_host_tensors_and_names():
         B.moe_router_backward(x, slot_row, torch.zeros(4), torch.zeros(65, dtype=torch.int32))
 
 
+def test_binding_names_the_input_that_a_gradient_needs():
+    from mixture_experts_layer_macs_amd import binding as B
+    dy, x, w = torch.zeros(4, 32), torch.zeros(4, 64), torch.zeros(32, 64)
+    ws = torch.zeros(1 << 10, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="dx needs w"):
+        B.moe_linear_backward(dy, x, None, ws, dx=x)
+    with pytest.raises(ValueError, match="dw needs x"):
+        B.moe_linear_backward(dy, None, w, ws, dw=w)
+    with pytest.raises(ValueError, match="x or w"):
+        B.moe_linear_backward(dy, None, None, ws, dbias=dy[0])
+    slot_row, gates = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    with pytest.raises(ValueError, match="d_gates needs out_rows"):
+        B.moe_combine_backward(x, None, slot_row, gates, d_gates=gates)
+    lse, counts = torch.zeros(4), torch.zeros(65, dtype=torch.int32)
+    with pytest.raises(ValueError, match="d_gates needs topk_ids"):
+        B.moe_router_backward(x, None, lse, counts, d_gates=gates, k=2)
+    with pytest.raises(ValueError, match="k is needed"):
+        B.moe_router_backward(x, None, lse, counts)
+
+
 def test_generator_known_answers():
     """The published test vectors of Philox4x32-10 (zero, all ones, digits of pi)."""
     assert R.philox(0, 0, 0) == [0x6627e8d5, 0xe169c58d, 0xbc57ac4c, 0x9b00dbd8]

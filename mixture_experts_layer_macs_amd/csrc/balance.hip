@@ -8,11 +8,13 @@
 //   dz_tj   = p_tj (u_tj - sum_i p_ti u_ti) + dL/dz_loss 2 lse_t p_tj / n,
 //   u_tj    = dL/dbalance N c_j / (k n^2) + sum_{s: id_ts = j} dL/dgate_ts
 // (the counts carry no gradient).  Both passes read the logits once, a token's
-// N logits in the registers of a group of 8 to 64 lanes.
+// N logits in the registers of a group of 8 to 64 lanes.  Sums over tokens are
+// fp64 from the first term on, in a fixed order (the additions run beside the
+// loads: fp32 runs of 32 tokens were no faster).
 //
-// Measured: 65521 tokens, 256 experts: loss 21.7 us (67 MB, 3.1 TB/s) and 6.9
-// for the second launch, gradient 32.8 us (134 MB, 4.1 TB/s); a large copy
-// runs at 4.8 TB/s.  128 tokens, 128 experts: 8.4 and 4.0 us, latency.
+// Measured: 65521 tokens, 256 experts: loss 22.2 us (67 MB, 3.0 TB/s) and 9.8
+// for the second launch, gradient 32.6 us (134 MB, 4.1 TB/s); a large copy
+// runs at 4.8 TB/s.  128 tokens, 128 experts: 8.6 and 4.0 us, latency.
 #include <algorithm>
 #include <type_traits>
 
@@ -50,7 +52,7 @@ __device__ __forceinline__ float group_max(float v) {
 // Partial sums of the workgroups, in the workspace, and the outputs.
 struct Part {
   double* zsq;     // [G]
-  float* prob;     // [G][pitch], zeros behind column N
+  double* prob;    // [G][pitch], zeros behind column N
   int32_t* count;  // [G][pitch]
   int32_t* n;      // [G]
   float *losses, *mean_prob;
@@ -81,13 +83,14 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 // The workgroups' sums to the outputs, one workgroup: a thread owns four
 // columns of every R-th partial row, 8 rows in flight.  What it reads was
 // written on other XCDs, so a dependent round costs a trip to memory (one
-// column per thread and as many rounds took 23 us at G = N = 256).
+// column per thread and as many rounds took 23 us at G = N = 256; now 9.8, what
+// one CU takes to read 768 KB.  Parts rounded to fp32 took 6.9).
 __global__ __launch_bounds__(NTHR) void finish_kernel(Part p) {
   __shared__ double s_p[NTHR][4];
   __shared__ int s_c[NTHR][4];
   __shared__ double red[WAVES], s_z;
   __shared__ int s_n;
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  typedef double f64x4 __attribute__((ext_vector_type(4)));
   typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
   const int tid = threadIdx.x;
   if (tid < MOE_WAVE) {
@@ -111,12 +114,12 @@ __global__ __launch_bounds__(NTHR) void finish_kernel(Part p) {
   int count[4] = {};
   if (c < p.N) {
     for (int g0 = r; g0 < p.G; g0 += 8 * R) {
-      f32x4 f[8];
+      f64x4 f[8];
       i32x4 m[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const size_t at = static_cast<size_t>(min(g0 + u * R, p.G - 1)) * p.pitch + c;
-        f[u] = *reinterpret_cast<const f32x4*>(p.prob + at);
+        f[u] = *reinterpret_cast<const f64x4*>(p.prob + at);
         m[u] = *reinterpret_cast<const i32x4*>(p.count + at);
       }
 #pragma unroll
@@ -124,7 +127,7 @@ __global__ __launch_bounds__(NTHR) void finish_kernel(Part p) {
         const bool in = g0 + u * R < p.G;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sum[i] += in ? f[u][i] : 0.f;
+          sum[i] += in ? f[u][i] : 0.0;
           count[i] += in ? m[u][i] : 0;
         }
       }
@@ -177,16 +180,9 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
   for (int j = threadIdx.x; j < N; j += NTHR) s_count[j] = 0;
   __syncthreads();
   constexpr int D = KPL <= 4 ? 4 : KPL <= 8 ? 2 : 1;
-  float pf[KPL], znext[D][KPL];
-  double pd[KPL];
-#pragma unroll
-  for (int i = 0; i < KPL; ++i) {
-    pf[i] = 0.f;
-    pd[i] = 0.0;
-  }
-  double zsq = 0.0;
-  float zrun = 0.f;
-  int n = 0, since = 0, idnext[D];
+  float znext[D][KPL];
+  double pd[KPL] = {}, zsq = 0.0;
+  int n = 0, idnext[D];
   uint32_t onnext[D];
   // every load of a request is unconditional (a branch around one waits for
   // all that are in flight): without a mask, bytes that are not looked at
@@ -232,21 +228,11 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
     const float inv = __builtin_amdgcn_rcpf(sum), l = shift + __logf(sum);
     if (some) {  // padding may hold NaN
 #pragma unroll
-      for (int i = 0; i < KPL; ++i) pf[i] += z[i] * inv;
-      zrun += l * l;
+      for (int i = 0; i < KPL; ++i) pd[i] += z[i] * inv;
+      zsq += static_cast<double>(l) * l;
     }
     n += on;
     if (gl == 0 && t < T) lse[t] = some ? l : on ? -INFINITY : 0.f;
-    if (++since == 32) {  // short fp32 runs, long sums in fp64
-      since = 0;
-#pragma unroll
-      for (int i = 0; i < KPL; ++i) {
-        pd[i] += pf[i];
-        pf[i] = 0.f;
-      }
-      zsq += zrun;
-      zrun = 0.f;
-    }
   };
   const int t0 = (blockIdx.x * WAVES + wave) * TPW;
   if (T > 0) {
@@ -256,16 +242,13 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
 #pragma unroll
       for (int d = 0; d < D; ++d) work(tb + sub + d * step, d);
   }
-  zsq += zrun;
   if (gl != 0) {  // every lane of a group counted its tokens
     zsq = 0.0;
     n = 0;
   }
 #pragma unroll
-  for (int i = 0; i < KPL; ++i) {
-    pd[i] += pf[i];
+  for (int i = 0; i < KPL; ++i)
     for (int m = GL; m < MOE_WAVE; m *= 2) pd[i] += __shfl_xor(pd[i], m, MOE_WAVE);
-  }
   zsq = wave_sum_f64(zsq);
   n = wave_sum(n);
   if (lane == 0) {
@@ -303,7 +286,7 @@ __global__ __launch_bounds__(NTHR) void loss_kernel(const float* __restrict__ lo
       part.counts[j] = c;
       dot += v * invn * c;
     } else if (!alone) {
-      part.prob[g * part.pitch + j] = j < N ? static_cast<float>(v) : 0.f;
+      part.prob[g * part.pitch + j] = j < N ? v : 0.0;
       part.count[g * part.pitch + j] = c;
     }
   }
@@ -445,7 +428,7 @@ inline int blocks(int T, int N) {
 
 inline size_t up4(int n) { return (static_cast<size_t>(n) + 3) & ~size_t(3); }
 
-inline size_t part_bytes(int G, int N) { return static_cast<size_t>(G) * (up4(N) * 8 + 12) + 64; }
+inline size_t part_bytes(int G, int N) { return static_cast<size_t>(G) * (up4(N) * 12 + 12) + 64; }
 
 }  // namespace bal
 }  // namespace moe
@@ -470,7 +453,7 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* slot_ids,
     return MOE_EINVAL;
   Part p;
   p.pitch = static_cast<int>(up4(N));
-  p.prob = static_cast<float*>(workspace);
+  p.prob = static_cast<double*>(workspace);
   p.count = reinterpret_cast<int32_t*>(p.prob + static_cast<size_t>(G) * p.pitch);
   p.zsq = reinterpret_cast<double*>(p.count + static_cast<size_t>(G) * p.pitch);
   p.n = reinterpret_cast<int32_t*>(p.zsq + G);

@@ -440,6 +440,33 @@ def test_balance_shows_a_row_of_nan(B, T, N, k):
     assert torch.equal(bad["counts"], good["counts"])
 
 
+@pytest.mark.parametrize("T,N,k", [(100, 5, 2), (100, 24, 3), (100, 200, 8), (1500, 31, 2), (1500, 200, 8),
+                                   (9001, 120, 4), (20000, 12, 4), (3000, 1000, 8)])
+def test_balance_sums_over_tokens_in_64_bits(B, T, N, k):
+    """T times the same token: T fp32 values of 24 bits sum exactly in fp64, so
+    the means are that token's own probabilities bit for bit; the losses, with
+    one more rounding in fp64 each, are off by at most a step."""
+    _, logits, ids = _balance_inputs(1, N, k, 3, drop=False)
+    one = torch.from_numpy(logits).cuda(), torch.from_numpy(ids).cuda()
+    many = tuple(t.repeat(T, 1) for t in one)
+    a, b = (B.moe_balance_loss(L, S, B.new_workspace(B.moe_balance_workspace_size(L.shape[0], N), "cuda"))
+            for L, S in (one, many))
+    assert torch.equal(a["mean_prob"], b["mean_prob"])
+    assert (b["lse"] == a["lse"]).all() and torch.equal(b["counts"], a["counts"] * T)
+    assert np.all(np.abs(R.f64(a["losses"]) - R.f64(b["losses"])) <= 2 * R.U * R.f64(a["losses"]))
+
+
+def test_balance_z_loss_of_large_scores(B):
+    """logsumexps of 8e18: the sum of some squares passes fp32's range, their
+    mean, 6.4e37, does not."""
+    T, N = 100000, 40
+    L = torch.full((T, N), 8e18, device="cuda")
+    S = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    out = B.moe_balance_loss(L, S, B.new_workspace(B.moe_balance_workspace_size(T, N), "cuda"))
+    want = R.f64(L[0, 0]) ** 2  # log 40 is far below a step of 8e18
+    assert abs(float(out["losses"][1]) - want) <= R.U * want
+
+
 def test_balance_without_tokens(B):
     ws = torch.full((B.moe_balance_workspace_size(0, 16),), 0xFF, dtype=torch.uint8, device="cuda")
     out = B.moe_balance_loss(torch.empty(0, 16, device="cuda"),

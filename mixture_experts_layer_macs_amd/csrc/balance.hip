@@ -13,7 +13,7 @@
 // loads: fp32 runs of 32 tokens were no faster).
 //
 // Measured: 65521 tokens, 256 experts: loss 22.2 us (67 MB, 3.0 TB/s) and 9.8
-// for the second launch, gradient 32.6 us (134 MB, 4.1 TB/s); a large copy
+// for the second launch, gradient 34.0 us (134 MB, 3.9 TB/s); a large copy
 // runs at 4.8 TB/s.  128 tokens, 128 experts: 8.6 and 4.0 us, latency.
 #include <algorithm>
 #include <type_traits>
@@ -388,16 +388,22 @@ __global__ __launch_bounds__(GNTHR) void grad_kernel(
         }
       }
     }
-    float dot = 0.f;
+    // lse is rounded to fp32, which costs every p of a token the same factor, up
+    // to |lse| 2^-24 off 1: the probabilities are those of the row's own sum
+    float dot = 0.f, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < KPL; ++i) dot += p[i] * u[i];
-    const float shift = zc * l - group_sum<GL>(dot);
+    for (int i = 0; i < KPL; ++i) {
+      dot += p[i] * u[i];
+      sum += p[i];
+    }
+    const float inv_sum = __builtin_amdgcn_rcpf(group_sum<GL>(sum));
+    const float shift = zc * l - group_sum<GL>(dot) * inv_sum;
     if (t < T) {
 #pragma unroll
       for (int i = 0; i < KPL; ++i)
         if (gl + GL * i < N)
           store_elem(&dlogits[static_cast<size_t>(t) * N + gl + GL * i],
-                     on ? p[i] * (u[i] + shift) : 0.f);
+                     on ? p[i] * inv_sum * (u[i] + shift) : 0.f);
     }
   }
 }

@@ -467,6 +467,42 @@ def test_balance_z_loss_of_large_scores(B):
     assert abs(float(out["losses"][1]) - want) <= R.U * want
 
 
+@pytest.mark.parametrize("T,N,k", [(9, 5, 2), (40, 16, 4), (40, 30, 3), (300, 64, 8), (65, 130, 8), (33, 300, 8),
+                                   (9, 1000, 8)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_router_backward_of_scores_far_from_zero(B, T, N, k, dtype):
+    """The gradient depends on differences of scores: a common offset (whose
+    logsumexp is rounded to a step of 2^-9) costs nothing.  Differences of scores
+    and logsumexp are exact or rounded once, and the exponential's argument once
+    more: |z - lse| 2^-23 of each p, a few units of the exponential and the
+    reciprocal, N-term sums; dlogits holds three such factors."""
+    g, logits, ids = _balance_inputs(T, N, k, 11)
+    for offset in (30000.0, -30000.0):
+        z = logits + np.float32(offset)
+        dg = g.normal(size=(T, k)).astype(np.float32)
+        for dl in ((0.5, 0.0), (0.0, 0.25)):  # the z loss's term, 2 lse p / n, is far larger than the other
+            dl = np.array(dl, np.float32)
+            L, S, DL, DG = (torch.from_numpy(a).cuda() for a in (z, ids, dl, dg))
+            out = B.moe_balance_loss(L, S, B.new_workspace(B.moe_balance_workspace_size(T, N), "cuda"))
+            dz = B.moe_router_backward(L, S, out["lse"], out["counts"], DL, None, DG, dtype=dtype)
+            r = R.balance(z.astype(np.float64), ids, None, dl.astype(np.float64), dg.astype(np.float64))
+            span = np.abs(z - r["lse"][:, None]).max()
+            e = (R.ACT + N / 16 + 2 * span) * R.U
+            _near(dz, r["dlogits"], 6 * e * r["scale"] + 1.01 * R.half(dtype) * np.abs(r["dlogits"]), "dlogits")
+
+
+def test_router_backward_of_the_lowest_scores(B):
+    """A token whose scores are all the type's lowest value is a uniform one."""
+    T, N, k = 6, 24, 2
+    L = torch.full((T, N), torch.finfo(F32).min, device="cuda")
+    S = torch.zeros(T, k, dtype=torch.int32, device="cuda")
+    DG = torch.full((T, k), 0.5, device="cuda")
+    out = B.moe_balance_loss(L, S, B.new_workspace(B.moe_balance_workspace_size(T, N), "cuda"))
+    dz = R.f64(B.moe_router_backward(L, S, out["lse"], out["counts"], d_gates=DG))
+    want = np.where(np.arange(N) == 0, (1 - 1 / N) / N, -1 / N / N)  # p_j (u_j - sum p u), u_0 = 1
+    assert np.all(np.abs(dz - want) <= 6 * (R.ACT + N / 16) * R.U / N)
+
+
 def test_balance_without_tokens(B):
     ws = torch.full((B.moe_balance_workspace_size(0, 16),), 0xFF, dtype=torch.uint8, device="cuda")
     out = B.moe_balance_loss(torch.empty(0, 16, device="cuda"),

@@ -266,7 +266,7 @@ __device__ __forceinline__ void act_grad(const E* dy, const E* z, int O, int act
     for (int i = 0; i < V; ++i) g[i] = a[i] <= 0.f ? 0.f : g[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) g[i] *= act_slope(act, a[i]);
+    for (int i = 0; i < V; ++i) g[i] *= act_slope<E>(act, a[i]);
   }
 }
 

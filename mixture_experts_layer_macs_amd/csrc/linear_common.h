@@ -90,44 +90,73 @@ __device__ __forceinline__ float sigmoid(float a) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-a));
 }
 
-// The normal distribution function Phi(a) and, in *density, exp(-a^2/2): the
-// rational form 7.1.26 of Abramowitz and Stegun for erfc (erf within 1.5e-7),
-// which shares its exponential with the density.  These instructions are what
-// a wide layer's epilogue costs: 36 us of 445 for a 4096 x 14336 output.
-__device__ __forceinline__ float normal_cdf(float a, float* density) {
-  const float x = fabsf(a) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
-  const float e = __expf(-x * x);
-  float p = 1.061405429f;
-  p = p * t - 1.453152027f;
-  p = p * t + 1.421413741f;
-  p = p * t - 0.284496736f;
-  p = p * t + 0.254829592f;
-  const float tail = 0.5f * p * t * e;
+// Phi(-m) of the normal distribution for m >= 0 and, in *density, exp(-m^2/2):
+//   Phi(-m) = exp(-m^2/2) t Q(t),  t = 1 / (1 + c m),
+// Q a least-maximum fit of the relative error on 0 <= m <= 13.5, where fp32's
+// range ends.  bf16 results take 6 coefficients (5e-6; half a step is 4e-3),
+// fp32 ones 9 (5e-8; with the exponential's rounded argument, m^2 2^-23).  The
+// tail is relative to itself, not to 1, so that gelu of -4 is as exact as that
+// of 4; it shares its exponential with the density.  These instructions are
+// what a wide layer's epilogue costs: 36 us of 445 for a 4096 x 14336 output.
+template <typename E>
+__device__ __forceinline__ float normal_tail(float m, float* density) {
+  constexpr bool WIDE = sizeof(E) == 4;
+  const float t = __builtin_amdgcn_rcpf(1.f + (WIDE ? 0.25f : 0.31f) * m);
+  const float e = __builtin_amdgcn_exp2f(m * m * -0.72134752f);  // -1 / (2 ln 2)
+  float p;
+  if constexpr (WIDE) {
+    p = 0.0262954589f;
+    p = p * t - 0.155636474f;
+    p = p * t + 0.30207628f;
+    p = p * t - 0.212748349f;
+    p = p * t + 0.206696898f;
+    p = p * t + 0.030758867f;
+    p = p * t + 0.104321837f;
+    p = p * t + 0.0984327942f;
+    p = p * t + 0.099802658f;
+  } else {
+    p = -0.0739291459f;
+    p = p * t + 0.180450365f;
+    p = p * t + 0.0157446899f;
+    p = p * t + 0.133429796f;
+    p = p * t + 0.120441273f;
+    p = p * t + 0.123860702f;
+  }
   *density = e;
-  return a >= 0.f ? 1.f - tail : tail;
+  return p * t * e;
 }
 
+constexpr float TAIL_END = 16.f;  // exp(-m^2/2) is 0 in fp32 from 14 on
+
+__device__ __forceinline__ float relu(float z) { return z < 0.f ? 0.f : z; }  // NaN stays
+
+// E: the type that the result is rounded to
+template <typename E>
 __device__ __forceinline__ float act_value(int act, float z) {
   float e;
   switch (act) {
-    case MOE_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
+    case MOE_ACT_RELU: return relu(z);
     case MOE_ACT_SILU: return z * sigmoid(z);
-    case MOE_ACT_GELU: return z * normal_cdf(z, &e);
+    case MOE_ACT_GELU: {  // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
+      const float m = fminf(fabsf(z), TAIL_END);
+      return relu(z) - m * normal_tail<E>(m, &e);
+    }
     default: return z;
   }
 }
 
+template <typename E>
 __device__ __forceinline__ float act_slope(int act, float z) {
   switch (act) {
     case MOE_ACT_SILU: {
       const float s = sigmoid(z);
       return s * (1.f + z * (1.f - s));
     }
-    case MOE_ACT_GELU: {
+    case MOE_ACT_GELU: {  // Phi(z) + z phi(z)
+      const float m = fabsf(z) > TAIL_END ? TAIL_END : fabsf(z);  // NaN stays
       float e;
-      const float c = normal_cdf(z, &e);
-      return c + z * 0.39894228040143268f * e;
+      const float tail = normal_tail<E>(m, &e), rise = m * 0.39894228040143268f * e;
+      return z < 0.f ? tail - rise : 1.f - tail + rise;
     }
     default: return 1.f;
   }
@@ -172,13 +201,13 @@ __device__ __forceinline__ void finish(const Epilogue& e, int m, int n, int N, f
   } else {
     if (e.act == MOE_ACT_GELU) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_value(MOE_ACT_GELU, g[i]);
+      for (int i = 0; i < V; ++i) v[i] = act_value<E>(MOE_ACT_GELU, g[i]);
     } else if (e.act == MOE_ACT_SILU) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_value(MOE_ACT_SILU, g[i]);
+      for (int i = 0; i < V; ++i) v[i] = act_value<E>(MOE_ACT_SILU, g[i]);
     } else if (e.act == MOE_ACT_RELU) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_value(MOE_ACT_RELU, g[i]);
+      for (int i = 0; i < V; ++i) v[i] = act_value<E>(MOE_ACT_RELU, g[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = g[i];

@@ -3,6 +3,7 @@ through the binding, against the 64-bit definitions of training_ref."""
 import numpy as np
 import pytest
 import torch
+from scipy.special import ndtr
 
 import training_ref as R
 from gpu_util import load_binding, needs_gpu
@@ -141,6 +142,49 @@ def test_activations_at_extreme_values(B, dtype):
         assert np.all(np.abs(y[fin] - want[fin][:, None]) <=
                       (2 * R.half(dtype) * np.abs(want) + R.ACT * R.U * (np.abs(z) + 1))[fin][:, None] + 1e-30)
         assert np.all(y[12] == np.inf)
+
+
+def _act_of(B, z, act, dtype):
+    """act(z) of the kernels for a vector z that the type holds: products by 1 and 0."""
+    x = torch.zeros(len(z), 8, dtype=dtype, device="cuda")
+    x[:, 0] = z
+    w = torch.zeros(8, 8, dtype=dtype, device="cuda")
+    w[:, 0] = 1
+    ws = B.new_workspace(B.moe_linear_workspace_size(len(z), 8, 8, act, dtype), "cuda")
+    y = B.moe_linear(x, w, ws, act=act)
+    assert (y == y[:, :1]).logical_or(y.isnan()).all()
+    return R.f64(y[:, 0])
+
+
+def _slope_of(B, z, act, dtype):
+    """act'(z) of the kernels: the bias gradient of one token with dy = 1."""
+    n = len(z)
+    one, x = torch.ones(1, n, dtype=dtype, device="cuda"), torch.zeros(1, 8, dtype=dtype, device="cuda")
+    ws = B.new_workspace(B.moe_linear_backward_workspace_size(1, 8, n, act, dtype), "cuda")
+    db = torch.empty(n, dtype=dtype, device="cuda")
+    B.moe_linear_backward(one, x, None, ws, z=z[None].contiguous(), act=act, dbias=db)
+    return R.f64(db)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_gelu_is_exact_relative_to_itself(B, dtype):
+    """The tail m Phi(-m), m = |z|, is relative to itself.  Roundings in units of
+    U = 2^-24: the exponent's m^2/2 three times (1.5 m^2), the exponential 2, the
+    argument of the fit 3 times its condition 3.2, its last steps 3 times their
+    amplification 2.5, the products 3; 32 in all.  On top of it the fit's own
+    error, 5e-6 for bf16 and 6e-8 for fp32, and half a step of the output."""
+    z = torch.linspace(-12.5, 12.5, 2000, dtype=torch.float64).to(dtype).cuda()
+    zd = R.f64(z)
+    rel = (1.5 * zd ** 2 + 32) * R.U + (5e-6 if dtype == BF16 else 6e-8)
+    tail, rise = ndtr(-np.abs(zd)), np.abs(zd) * np.exp(-zd ** 2 / 2) / np.sqrt(2 * np.pi)
+    want = np.where(zd < 0, zd * tail, zd - zd * tail)
+    pos, h = (zd > 0) * 2 * R.U, 1.01 * R.half(dtype)
+    _near(torch.from_numpy(_act_of(B, z, "gelu", dtype)), want,
+          rel * np.abs(zd) * tail + pos * np.abs(zd) + h * np.abs(want) + 1e-37, "gelu")
+    want = np.where(zd < 0, tail - rise, 1 - tail + rise)
+    # two terms, of which the second has two more roundings
+    _near(torch.from_numpy(_slope_of(B, z, "gelu", dtype)), want,
+          (rel + 4 * R.U) * (tail + rise) + pos + h * np.abs(want) + 1e-37, "gelu'")
 
 
 BACK = [(1, 64, 72), (2, 2056, 24), (7, 136, 264), (33, 200, 128), (64, 64, 64), (130, 264, 520),

@@ -507,6 +507,8 @@ int moe_combine(const void* out_rows, const int32_t* slot_row,
  * residual  [T,O]  (dtype); may be NULL; may equal y (in place).
  * act       MOE_ACT_NONE; _RELU; _SILU a/(1+e^-a); _GELU a Phi(a) with the
  *           normal distribution function Phi (the erf form); _SWIGLU.
+ *           At -inf relu, silu and gelu are 0, and their slopes are 0 there
+ *           and 1 at +inf; NaN stays NaN.
  * dtype     MOE_BF16 (bf16 products, fp32 accumulation and epilogue, y and z
  *           rounded once) or MOE_F32.
  * z         [T,O] ([T,2O]) out: the product before the activation, for

@@ -90,6 +90,20 @@ __device__ __forceinline__ float sigmoid(float a) {
   return __builtin_amdgcn_rcpf(1.f + __expf(-a));
 }
 
+// Outside +-SILU_END sigmoid is 0 or 1 in fp32.  Its factor a is held there
+// where an infinite one would give inf * 0 for a limit of 0; NaN stays.
+constexpr float SILU_END = 128.f;
+
+__device__ __forceinline__ float silu(float a) {
+  const float z = a < -SILU_END ? -SILU_END : a;
+  return z * sigmoid(z);
+}
+// silu'(a), s = sigmoid(a)
+__device__ __forceinline__ float silu_slope(float a, float s) {
+  const float z = a < -SILU_END ? -SILU_END : a > SILU_END ? SILU_END : a;
+  return s * (1.f + z * (1.f - s));
+}
+
 // Phi(-m) of the normal distribution for m >= 0 and, in *density, exp(-m^2/2):
 //   Phi(-m) = exp(-m^2/2) t Q(t),  t = 1 / (1 + c m),
 // Q a least-maximum fit of the relative error on 0 <= m <= 13.5, where fp32's
@@ -136,7 +150,7 @@ __device__ __forceinline__ float act_value(int act, float z) {
   float e;
   switch (act) {
     case MOE_ACT_RELU: return relu(z);
-    case MOE_ACT_SILU: return z * sigmoid(z);
+    case MOE_ACT_SILU: return silu(z);
     case MOE_ACT_GELU: {  // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
       const float m = fminf(fabsf(z), TAIL_END);
       return relu(z) - m * normal_tail<E>(m, &e);
@@ -148,10 +162,7 @@ __device__ __forceinline__ float act_value(int act, float z) {
 template <typename E>
 __device__ __forceinline__ float act_slope(int act, float z) {
   switch (act) {
-    case MOE_ACT_SILU: {
-      const float s = sigmoid(z);
-      return s * (1.f + z * (1.f - s));
-    }
+    case MOE_ACT_SILU: return silu_slope(z, sigmoid(z));
     case MOE_ACT_GELU: {  // Phi(z) + z phi(z)
       const float m = fabsf(z) > TAIL_END ? TAIL_END : fabsf(z);  // NaN stays
       float e;
@@ -197,7 +208,7 @@ __device__ __forceinline__ void finish(const Epilogue& e, int m, int n, int N, f
   float v[V];
   if constexpr (GLU) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+    for (int i = 0; i < V; ++i) v[i] = silu(g[i]) * u[i];
   } else {
     if (e.act == MOE_ACT_GELU) {
 #pragma unroll

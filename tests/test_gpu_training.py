@@ -187,6 +187,48 @@ def test_gelu_is_exact_relative_to_itself(B, dtype):
           (rel + 4 * R.U) * (tail + rise) + pos + h * np.abs(want) + 1e-37, "gelu'")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_activations_reach_their_limits(B, act, dtype):
+    """From -100 on the activations and their slopes are 0 (z e^z and z phi(z) lie
+    below fp32's range), from 100 on z and 1, infinities included; NaN shows."""
+    low = torch.tensor([-100.0, -128.0, -129.0, -1e3, -1e4, -1e30, torch.finfo(dtype).min, -float("inf")], dtype=dtype)
+    z = torch.cat([low, -low]).cuda()
+    want = torch.cat([torch.zeros_like(low), -low])
+    assert np.array_equal(np.abs(_act_of(B, z, act, dtype)), R.f64(want))
+    assert np.array_equal(np.abs(_slope_of(B, z, act, dtype)), np.repeat([0.0, 1.0], 8))
+    z[3] = z[12] = float("nan")
+    nan = np.isin(np.arange(16), [3, 12])
+    assert np.array_equal(np.isnan(_act_of(B, z, act, dtype)), nan)
+    if act != "relu":  # a unit of NaN passes dy on
+        assert np.array_equal(np.isnan(_slope_of(B, z, act, dtype)), nan)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_swiglu_of_closed_and_open_gates(B, dtype):
+    """A gate far below 0 closes its column and its gradients, whatever dy is;
+    one far above passes the up half; the others do not change."""
+    inf, big = float("inf"), torch.finfo(dtype).max
+    t = lambda *v: torch.tensor(v, dtype=dtype, device="cuda")  # noqa: E731
+    x, w = torch.zeros(1, 8, dtype=dtype, device="cuda"), torch.zeros(16, 8, dtype=dtype, device="cuda")
+    x[0, 0] = 1
+    w[:8, 0], w[8:, 0] = t(-big, -1e30, -200.0, -1.0, 0.0, 2.0, 200.0, 1e30), 3.0
+    ws = B.new_workspace(B.moe_linear_workspace_size(1, 8, 8, "swiglu", dtype), "cuda")
+    y, g = R.f64(B.moe_linear(x, w, ws, act="swiglu"))[0], R.f64(w[:8, 0])
+    want = 3 * R.act_value(g, "silu")
+    assert (y[:3] == 0).all()
+    assert np.all(np.abs(y - want) <= 1.01 * R.half(dtype) * np.abs(want) + 3 * R.ACT * R.U * (np.abs(want) + 1))
+    z = torch.cat([t(-inf, -1e30, -200.0, -1.0, 0.0, 2.0, 200.0, inf), t(3.0).repeat(8)])[None]
+    ws = B.new_workspace(B.moe_linear_backward_workspace_size(1, 8, 8, "swiglu", dtype), "cuda")
+    for scale in (1.0, big):
+        db = torch.empty(16, dtype=dtype, device="cuda")
+        B.moe_linear_backward(t(scale).repeat(8)[None], x, None, ws, z=z, act="swiglu", dbias=db)
+        db = R.f64(db)
+        assert (db[:3] == 0).all() and (db[8:11] == 0).all()
+        if scale == 1:
+            assert (db[6:8] == 3).all() and db[14] == 200 and db[15] == np.inf and np.isfinite(db[:15]).all()
+
+
 BACK = [(1, 64, 72), (2, 2056, 24), (7, 136, 264), (33, 200, 128), (64, 64, 64), (130, 264, 520),
         (251, 136, 264), (256, 512, 256), (300, 1032, 72), (777, 328, 264), (1030, 136, 776),
         (2100, 264, 136), (4100, 64, 40)]

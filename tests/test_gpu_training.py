@@ -323,6 +323,41 @@ def test_linear_few_tokens_wide_weights(B, T, K, O, act):
     assert _untouched(ybuf, pad)
 
 
+# Kernels that the sizes above do not reach: the skinny product of gated weights
+# for more than 16 tokens, split fp32 tiles, 128 x 128 tiles without a partner,
+# both products of a small backward pass split.
+VARIANTS = [(29, 944, 2040, "swiglu", BF16), (40, 200, 2920, "swiglu", BF16), (70, 760, 2488, "swiglu", BF16),
+            (67, 1124, 3324, "none", F32)]
+BACK_VARIANTS = [(154, 49600, 8, "none", BF16), (1, 49592, 72, "swiglu", BF16), (849, 8, 840, "none", BF16),
+                 (3143, 304, 1192, "swiglu", BF16)]
+
+
+@pytest.mark.parametrize("T,K,O,act,dtype", VARIANTS)
+def test_linear_other_variants(B, T, K, O, act, dtype):
+    g, x, w, b, r = _linear_inputs(T, K, O, act, dtype, 15, True, True)
+    ws = torch.full((B.moe_linear_workspace_size(T, K, O, act, dtype),), 0xFF, dtype=torch.uint8, device="cuda")
+    (ybuf, y, pad), (zbuf, z, _) = _guard((T, O), dtype), _guard((T, w.shape[0]), dtype)
+    B.moe_linear(x, w, ws, bias=b, residual=r, act=act, z=z, y=y)
+    yr, zr, ey, ez = R.linear(R.f64(x), R.f64(w), R.f64(b), R.f64(r), act, dtype)
+    _near(z, zr, ez, "z")
+    _near(y, yr, ey, "y")
+    assert _untouched(ybuf, pad) and _untouched(zbuf, pad)
+
+
+@pytest.mark.parametrize("T,K,O,act,dtype", BACK_VARIANTS)
+def test_linear_backward_other_variants(B, T, K, O, act, dtype):
+    g, x, w, _, _ = _linear_inputs(T, K, O, act, dtype, 16, False, False)
+    W = w.shape[0]
+    dy, z = _rand(g, (T, O), 0.5, dtype), _rand(g, (T, W), 1.0, dtype)
+    ws = torch.full((B.moe_linear_backward_workspace_size(T, K, O, act, dtype),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    bufs = {"dx": _guard((T, K), dtype), "dw": _guard((W, K), dtype), "db": _guard((W,), dtype)}
+    B.moe_linear_backward(dy, x, w, ws, z=z, act=act, dx=bufs["dx"][1], dw=bufs["dw"][1], dbias=bufs["db"][1])
+    for n, (v, e) in R.linear_backward(R.f64(dy), R.f64(x), R.f64(w), R.f64(z), act, dtype).items():
+        _near(bufs[n][1], v, e, n)
+        assert _untouched(bufs[n][0], bufs[n][2]), n
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_relu_shows_nan_and_closes_to_infinity(B, dtype):
     T, K, O = 5, 16, 24

@@ -107,15 +107,16 @@ __device__ __forceinline__ float silu_slope(float a, float s) {
 // Phi(-m) of the normal distribution for m >= 0 and, in *density, exp(-m^2/2):
 //   Phi(-m) = exp(-m^2/2) t Q(t),  t = 1 / (1 + c m),
 // Q a least-maximum fit of the relative error on 0 <= m <= 13.5, where fp32's
-// range ends.  bf16 results take 6 coefficients (5e-6; half a step is 4e-3),
-// fp32 ones 9 (5e-8; with the exponential's rounded argument, m^2 2^-23).  The
+// range ends.  bf16 results take 7 coefficients (8e-7, 7 units of fp32 where the
+// tail is 1/2: the bias gradient sums unrounded slopes), fp32 ones 9 (5e-8;
+// with the exponential's rounded argument, m^2 2^-23).  The
 // tail is relative to itself, not to 1, so that gelu of -4 is as exact as that
 // of 4; it shares its exponential with the density.  These instructions are
 // what a wide layer's epilogue costs: 36 us of 445 for a 4096 x 14336 output.
 template <typename E>
 __device__ __forceinline__ float normal_tail(float m, float* density) {
   constexpr bool WIDE = sizeof(E) == 4;
-  const float t = __builtin_amdgcn_rcpf(1.f + (WIDE ? 0.25f : 0.31f) * m);
+  const float t = __builtin_amdgcn_rcpf(1.f + (WIDE ? 0.25f : 0.36f) * m);
   const float e = __builtin_amdgcn_exp2f(m * m * -0.72134752f);  // -1 / (2 ln 2)
   float p;
   if constexpr (WIDE) {
@@ -129,12 +130,13 @@ __device__ __forceinline__ float normal_tail(float m, float* density) {
     p = p * t + 0.0984327942f;
     p = p * t + 0.099802658f;
   } else {
-    p = -0.0739291459f;
-    p = p * t + 0.180450365f;
-    p = p * t + 0.0157446899f;
-    p = p * t + 0.133429796f;
-    p = p * t + 0.120441273f;
-    p = p * t + 0.123860702f;
+    p = 0.0473445766f;
+    p = p * t - 0.180751696f;
+    p = p * t + 0.182297647f;
+    p = p * t + 0.025623776f;
+    p = p * t + 0.140057445f;
+    p = p * t + 0.141710669f;
+    p = p * t + 0.143717438f;
   }
   *density = e;
   return p * t * e;

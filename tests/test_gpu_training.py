@@ -413,6 +413,31 @@ def test_backward_calls_without_tokens(B, dtype):
                                  d_gates=G, dtype=dtype).shape == (0, 16)
 
 
+@pytest.mark.parametrize("T,K,O,act", [(1030, 136, 776, "gelu"), (2048, 1024, 384, "swiglu"), (70, 72, 136, "silu")])
+def test_linear_backward_rounds_dz_once_and_nothing_else(B, T, K, O, act):
+    """dx and dw are the products of dz rounded to bf16: off them by fp32 sums and
+    half a step of the result, and by a step of dz where its fp32 value (within e
+    of the exact one) may round to either side; the same inputs give the same bits."""
+    g, x, w, _, _ = _linear_inputs(T, K, O, act, BF16, 31, False, False)
+    W = w.shape[0]
+    dy, z = _rand(g, (T, O), 0.5, BF16), _rand(g, (T, W), 1.0, BF16)
+    ws = B.new_workspace(B.moe_linear_backward_workspace_size(T, K, O, act, BF16), "cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    B.moe_linear_backward(dy, x, w, ws, z=z, act=act, dx=dx, dw=dw)
+    dz, e = R.act_grad(R.f64(dy), R.f64(z), act)
+    lo, mid, hi = (R.f64(torch.from_numpy(v).to(BF16)) for v in (dz - e, dz, dz + e))
+    step, h = hi - lo, 1.01 * R.half(BF16)
+    for got, a, s, b, n in ((dx, mid, step, R.f64(w), W), (dw, mid.T, step.T, R.f64(x), T)):
+        v = R.product(a, b)
+        err = R.product((n + 2) * R.U * (np.abs(a) + s) + s, np.abs(b))
+        _near(got, v, err * (1 + h) + h * np.abs(v), "dx" if got is dx else "dw")
+    first = dx.clone(), dw.clone()
+    ws.fill_(0xFF)
+    B.moe_linear(x, w, ws[:256].new_zeros(B.moe_linear_workspace_size(T, K, O, act, BF16)), act=act)
+    B.moe_linear_backward(dy, x, w, ws, z=z, act=act, dx=dx, dw=dw)
+    assert torch.equal(first[0], dx) and torch.equal(first[1], dw)
+
+
 def test_linear_gradient_against_the_kernels_own_differences(B):
     """The fp32 forward kernel's difference quotient along a direction equals
     the 64-bit one up to the forward's rounding over 2h."""

@@ -538,8 +538,10 @@ int moe_linear(const void* x, const void* w, const void* bias,
  * z         moe_linear's z; unused and may be NULL for MOE_ACT_NONE.
  * dx        [T,K], dw as w, dbias [O] ([2O]): out (dtype), overwritten; each
  *           may be NULL to skip it, not all three (T == 0: any).
- * dz is rounded to dtype for the two products (bf16 operands, fp32 sums);
- * dbias sums the unrounded values in fp32.  T == 0 writes zeros to dw and
+ * dz is rounded to dtype for the two products (bf16 operands, fp32 sums), which
+ * in bf16 makes the error of dx and dw 1.4 times that of rounding them alone;
+ * dbias sums the unrounded values in fp32.  The outputs must not overlap the
+ * inputs.  T == 0 writes zeros to dw and
  * dbias.  Workspace of moe_linear_backward_workspace_size() bytes (scratch
  * only), limits and errors as moe_linear.
  */
@@ -642,8 +644,8 @@ int moe_combine_dropout(const void* out_rows, const int32_t* slot_row,
  *             left as they were.  May be NULL.
  * d_gates     f32[T,k] out: 0 for dropped slots.  May be NULL, not both
  *             (T == 0: any).
- * out_rows may be NULL without d_gates.  Errors and alignment as
- * moe_combine_dropout.  One launch; T == 0 enqueues nothing.
+ * out_rows may be NULL without d_gates.  The outputs must not overlap the
+ * inputs.  Errors and alignment as moe_combine_dropout.  One launch; T == 0 enqueues nothing.
  */
 int moe_combine_backward(const void* dy, const void* out_rows,
                          const int32_t* slot_row, const float* topk_gates,

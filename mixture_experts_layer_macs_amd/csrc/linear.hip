@@ -163,8 +163,8 @@ __device__ __forceinline__ void act_grad(const E* dy, const E* z, int O, int act
     load_v<V>(z + O, up);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float d = g[i] * silu(a[i]);
-      g[i] *= up[i] * silu_slope(a[i], sigmoid(a[i]));
+      const float sg = sigmoid(a[i]), d = g[i] * silu(a[i], sg);
+      g[i] *= up[i] * silu_slope(a[i], sg);
       up[i] = d;
     }
   } else if (act == MOE_ACT_RELU) {  // a closed unit passes nothing, whatever dy is

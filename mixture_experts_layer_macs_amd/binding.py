@@ -664,6 +664,8 @@ def moe_router_backward(logits, topk_ids, lse, counts, d_losses=None, token_mask
     then."""
     T, N = logits.shape
     if topk_ids is not None:
+        if k not in (None, topk_ids.shape[1]):
+            raise ValueError(f"k is {k}, but topk_ids has {topk_ids.shape[1]} slots per token")
         k = topk_ids.shape[1]
     elif d_gates is not None:
         raise ValueError("d_gates needs topk_ids")

@@ -192,6 +192,8 @@ def test_binding_names_the_input_that_a_gradient_needs():
         B.moe_router_backward(x, None, lse, counts, d_gates=gates, k=2)
     with pytest.raises(ValueError, match="k is needed"):
         B.moe_router_backward(x, None, lse, counts)
+    with pytest.raises(ValueError, match="2 slots per token"):
+        B.moe_router_backward(x, slot_row, lse, counts, k=3)
 
 
 def test_generator_known_answers():

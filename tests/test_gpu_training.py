@@ -741,6 +741,93 @@ def test_combine_without_dropout_is_moe_combine(B):
         assert torch.equal(B.moe_combine_dropout(rows, S, G), B.moe_combine(rows, S, G))
 
 
+# --------------------------------------------------- offsets beyond 32 bits
+FAR = 64  # rows looked at, at either end of the long arrays
+
+
+def _ends(T):
+    return torch.cat([torch.arange(FAR), torch.arange(T - FAR, T)]).cuda()
+
+
+def test_linear_with_more_than_2_31_elements(B):
+    """Rows beyond 2^31 elements of y, z, dy and dz; dy is 0 but for the rows at
+    the ends, so that dw and dbias are those rows' sums."""
+    T, K, O, act = 1 << 20, 64, 2056, "silu"
+    at = _ends(T)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, K, generator=gen, device="cuda").to(BF16)
+    w = (torch.randn(O, K, generator=gen, device="cuda") / 8).to(BF16)
+    ws = B.new_workspace(max(B.moe_linear_workspace_size(T, K, O, act, BF16),
+                             B.moe_linear_backward_workspace_size(T, K, O, act, BF16)), "cuda")
+    z = torch.empty(T, O, dtype=BF16, device="cuda")
+    y = B.moe_linear(x, w, ws, act=act, z=z)
+    yr, zr, ey, ez = R.linear(R.f64(x[at]), R.f64(w), None, None, act, BF16)
+    _near(z[at], zr, ez, "z")
+    _near(y[at], yr, ey, "y")
+    dy = y.zero_()
+    dy[at] = torch.randn(2 * FAR, O, generator=gen, device="cuda").to(BF16)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(O, dtype=BF16, device="cuda")
+    B.moe_linear_backward(dy, x, w, ws, z=z, act=act, dx=dx, dw=dw, dbias=db)
+    r = R.linear_backward(R.f64(dy[at]), R.f64(x[at]), R.f64(w), R.f64(z[at]), act, BF16)
+    _near(dx[at], *r["dx"], "dx")
+    _near(dw, *r["dw"], "dw")  # the zeros between the ends add no rounding
+    _near(db, *r["db"], "db")
+    dx[at] = 0
+    assert not dx.any()
+
+
+def test_combine_with_more_than_2_31_elements(B):
+    T, k, H, p = 140000, 8, 2048, 0.25
+    at = _ends(T)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    S = torch.arange(T * k, dtype=torch.int32, device="cuda").flip(0).view(T, k)  # the last rows first
+    G = torch.rand(T, k, generator=gen, device="cuda")
+    rows = torch.zeros(T * k, H, dtype=BF16, device="cuda")
+    named = S[at].long().reshape(-1)
+    rows[named] = torch.randn(len(named), H, generator=gen, device="cuda").to(BF16)
+    dy = torch.randn(T, H, generator=gen, device="cuda").to(BF16)
+    rng = torch.tensor([8, 9], dtype=torch.int64, device="cuda")
+    y = B.moe_combine_dropout(rows, S, G, p, rng)
+    d_rows, dg = torch.empty_like(rows), torch.empty_like(G)
+    B.moe_combine_backward(dy, rows, S, G, p, rng, d_out_rows=d_rows, d_gates=dg)
+    blocks = H // 4
+    keep = np.stack([[wd >= int(p * 2 ** 32) for b in range(t * blocks, (t + 1) * blocks) for wd in R.philox(8, 9, b)]
+                     for t in at.tolist()])
+    m = keep / (1 - p)
+    local = np.arange(2 * FAR * k, dtype=np.int32).reshape(2 * FAR, k)
+    sub, gd = R.f64(rows[named]), R.f64(G[at])
+    want, e = R.combine(sub, local, gd, None, m, BF16)
+    _near(y[at], want, e, "y")
+    wr, er, wg, eg = R.combine_backward(R.f64(dy[at]), sub, local, gd, m, BF16)
+    _near(d_rows[named], wr, er, "d_rows")
+    _near(dg[at], wg, eg, "d_gates")
+
+
+def test_router_losses_of_the_largest_batch(B):
+    """2^20 tokens of 1024 experts (2^32 bytes of scores): the gates' gradient of
+    the tokens at the ends, counts and means of all of them."""
+    T, N, k = 1 << 20, 1024, 2
+    at = _ends(T)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    L = torch.randn(T, N, generator=gen, device="cuda")
+    S = torch.randint(0, N, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+    DG = torch.randn(T, k, generator=gen, device="cuda")
+    out = B.moe_balance_loss(L, S, B.new_workspace(B.moe_balance_workspace_size(T, N), "cuda"))
+    assert torch.equal(out["counts"][:N].long(), torch.bincount(S.reshape(-1), minlength=N))
+    assert int(out["counts"][N]) == T
+    lse = torch.logsumexp(L.double(), 1)
+    e = (R.ACT + N / 16 + 12) * R.U  # |z| < 6: the bound of the small batches
+    assert float((out["lse"].double() - lse).abs().max()) <= e + R.U * float(lse.max())
+    mean = torch.zeros(N, dtype=torch.float64, device="cuda")
+    for i in range(0, T, 1 << 17):
+        mean += torch.exp(L[i:i + (1 << 17)].double() - lse[i:i + (1 << 17), None]).sum(0)
+    mean /= T
+    assert float(((out["mean_prob"].double() - mean).abs() / mean).max()) <= 2 * e
+    dz = B.moe_router_backward(L, S, out["lse"], out["counts"], d_gates=DG)
+    r = R.balance(R.f64(L[at]), S[at].cpu().numpy(), None, None, R.f64(DG[at]))
+    _near(dz[at], r["dlogits"], 6 * e * r["scale"] + R.U * np.abs(r["dlogits"]) * 1.01, "dlogits")
+
+
 # ------------------------------------------------- together, streams, graphs
 class _Step:
     """One tuning step of a router and a shared expert beside frozen routed

@@ -90,7 +90,7 @@ __global__ __launch_bounds__(NTHR) void finish_kernel(Part p) {
   __shared__ int s_c[NTHR][4];
   __shared__ double red[WAVES], s_z;
   __shared__ int s_n;
-  typedef double f64x4 __attribute__((ext_vector_type(4)));
+  typedef double f64x2 __attribute__((ext_vector_type(2)));  // the workspace starts at 16 bytes
   typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
   const int tid = threadIdx.x;
   if (tid < MOE_WAVE) {
@@ -114,12 +114,13 @@ __global__ __launch_bounds__(NTHR) void finish_kernel(Part p) {
   int count[4] = {};
   if (c < p.N) {
     for (int g0 = r; g0 < p.G; g0 += 8 * R) {
-      f64x4 f[8];
+      f64x2 f[8][2];
       i32x4 m[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const size_t at = static_cast<size_t>(min(g0 + u * R, p.G - 1)) * p.pitch + c;
-        f[u] = *reinterpret_cast<const f64x4*>(p.prob + at);
+        f[u][0] = *reinterpret_cast<const f64x2*>(p.prob + at);
+        f[u][1] = *reinterpret_cast<const f64x2*>(p.prob + at + 2);
         m[u] = *reinterpret_cast<const i32x4*>(p.count + at);
       }
 #pragma unroll
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(NTHR) void finish_kernel(Part p) {
         const bool in = g0 + u * R < p.G;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          sum[i] += in ? f[u][i] : 0.0;
+          sum[i] += in ? f[u][i / 2][i % 2] : 0.0;
           count[i] += in ? m[u][i] : 0;
         }
       }

@@ -602,6 +602,19 @@ def test_balance_sums_over_tokens_in_64_bits(B, T, N, k):
     assert np.all(np.abs(R.f64(a["losses"]) - R.f64(b["losses"])) <= 2 * R.U * R.f64(a["losses"]))
 
 
+@pytest.mark.parametrize("N", [5, 40, 257])
+def test_balance_workspace_at_16_bytes(B, N):
+    T, k = 3000, 3
+    _, logits, ids = _balance_inputs(T, N, k, 12)
+    L, S = torch.from_numpy(logits).cuda(), torch.from_numpy(ids).cuda()
+    n = B.moe_balance_workspace_size(T, N)
+    a = B.moe_balance_loss(L, S, B.new_workspace(n, "cuda"))
+    buf = torch.full((n + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    b = B.moe_balance_loss(L, S, buf[16:16 + n])
+    assert all(torch.equal(a[m], b[m]) for m in a)
+    assert (buf[:16] == 0xFF).all() and (buf[16 + n:] == 0xFF).all()
+
+
 def test_balance_z_loss_of_large_scores(B):
     """logsumexps of 8e18: the sum of some squares passes fp32's range, their
     mean, 6.4e37, does not."""

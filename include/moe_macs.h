@@ -653,6 +653,159 @@ int moe_combine_backward(const void* dy, const void* out_rows,
                          int dtype, void* d_out_rows, float* d_gates,
                          void* stream);
 
+/*
+ * moe_grouped_linear -- the routed experts' matrix products over the dispatched
+ * rows, for training: for row r of expert e with token t = row_token[r],
+ *   z_r = W_e x_t;   y_r = act(z_r)
+ * e.g. the two halves of the experts of MACS §3.1 Eq. 1 with z kept: the
+ * gate-up half is MOE_ACT_SWIGLU on w13 with row_token, the down half a plain
+ * product of its y with w2.
+ *
+ * x               [T,K] (dtype) gathered through row_token; without row_token
+ *                 (NULL) x holds the rows themselves and T = R.
+ * row_token       i32[R] moe_dispatch's output, ids in [0,T); may be NULL.
+ * expert_offsets  i32[N+1] moe_dispatch's output: ascending from 0; rows of
+ *                 expert e are [expert_offsets[e], expert_offsets[e+1]), an
+ *                 expert may have none.
+ * w               [N,O,K] (dtype), MOE_ACT_SWIGLU: [N,2O,K] (w13's layout).
+ * act, dtype      as moe_linear.
+ * z               [R,O] ([R,2O]) out: the product before the activation, for
+ *                 moe_grouped_linear_backward; may be NULL.
+ * y               [R,O]  out.
+ * The M = expert_offsets[N] <= R first rows of y and z are written, the others
+ * left as they were.  Workspace of moe_grouped_linear_workspace_size() bytes
+ * (scratch only; no initialisation).  Limits: 1 <= N <= 1024, R and T at most
+ * MOE_GROUPED_MAX_ROWS, 1 <= K, O <= MOE_LINEAR_MAX_DIM, multiples of 8
+ * (MOE_BF16) or 4 (MOE_F32) and, with row_token, x of at most 2 GiB, else
+ * MOE_EUNSUP (MOE_EINVAL for sizes out of range); every array but the two index
+ * arrays starts at a multiple of 16 bytes, else MOE_EINVAL.  The outputs must not
+ * overlap the inputs.  R == 0 enqueues nothing.
+ */
+#define MOE_GROUPED_MAX_ROWS (1 << 23)
+size_t moe_grouped_linear_workspace_size(int R, int N, int K, int O, int act,
+                                         int dtype);
+int moe_grouped_linear(const void* x, const int32_t* row_token,
+                       const int32_t* expert_offsets, const void* w, int T,
+                       int R, int N, int K, int O, int act, int dtype, void* z,
+                       void* y, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * moe_grouped_linear_backward -- the gradients of moe_grouped_linear:
+ *   dz = dy * act'(z);   dx_r = dz_r W_e;   dW_e = sum over e's rows of dz_r x_t^T
+ *
+ * dy        [R,O] (dtype), e.g. moe_combine_backward's d_out_rows.
+ * x, row_token, expert_offsets, w: as moe_grouped_linear (x and row_token may
+ *           be NULL without dw, w without dx).
+ * z         moe_grouped_linear's z; unused and may be NULL for MOE_ACT_NONE.
+ * dx        [R,K] out (dtype): one row per dispatched row, the M first ones
+ *           written.  A token's gradient is the sum of its rows: moe_combine
+ *           with gates of one.
+ * dw        as w, out (dtype), overwritten; zeros for an expert without rows.
+ * dx or dw may be NULL to skip it, not both (R == 0: any).
+ * dz is rounded to dtype for the two products, as in moe_linear_backward.
+ * R == 0 writes zeros to dw.  Workspace of
+ * moe_grouped_linear_backward_workspace_size() bytes (scratch only), limits
+ * and errors as moe_grouped_linear.
+ */
+size_t moe_grouped_linear_backward_workspace_size(int R, int N, int K, int O,
+                                                  int act, int dtype);
+int moe_grouped_linear_backward(const void* dy, const void* x,
+                                const int32_t* row_token,
+                                const int32_t* expert_offsets, const void* w,
+                                const void* z, int T, int R, int N, int K, int O,
+                                int act, int dtype, void* dx, void* dw,
+                                void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * moe_norm -- the norm in front of the layer, with the residual sum:
+ *   s = x + residual (rounded to dtype);   y = (s - mean) rstd weight + bias
+ * with the row's mean and rstd = 1 / sqrt(mean((s - mean)^2) + eps);
+ * MOE_NORM_RMS takes mean = 0.
+ *
+ * x, residual  [T,H] (dtype); residual may be NULL.
+ * weight, bias [H] (dtype); bias may be NULL.
+ * eps          finite, >= 0.  A row of variance 0 with eps == 0 gives NaN.
+ * sum          [T,H] out: s; required with residual, unused and may be NULL
+ *              without; may equal x or residual (in place).
+ * y            [T,H] out; may equal x (in place) when nothing else reads it.
+ * mean, rstd   f32[T] out, for moe_norm_backward; each may be NULL.
+ * Statistics are fp32, the variance from the centred values.
+ * Limits: 1 <= H <= MOE_LINEAR_MAX_DIM, a multiple of 8 (MOE_BF16) or 4
+ * (MOE_F32), else MOE_EUNSUP; arrays of H columns start at a multiple of 16
+ * bytes, else MOE_EINVAL.  T == 0 enqueues nothing.  One launch.
+ */
+enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 };
+int moe_norm(const void* x, const void* residual, const void* weight,
+             const void* bias, int T, int H, int kind, double eps, int dtype,
+             void* sum, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * moe_norm_backward -- the gradients of moe_norm.  With h = (s - mean) rstd and
+ * u = dy weight,
+ *   dx      = rstd (u - mean(u) - h mean(u h)) + dsum
+ *   dweight = sum_t dy h;   dbias = sum_t dy
+ * (means along the row; MOE_NORM_RMS leaves out mean(u)).  dx is the gradient of
+ * x and of residual alike.
+ *
+ * dy        [T,H] (dtype).
+ * s         [T,H] (dtype) moe_norm's sum, or x where it had no residual.
+ * weight    [H] (dtype); may be NULL without dx.
+ * mean      f32[T] moe_norm's; unused and may be NULL for MOE_NORM_RMS.
+ * rstd      f32[T] moe_norm's.
+ * dsum      [T,H] (dtype) gradient that reaches s past the norm (the residual
+ *           stream); may be NULL.
+ * dx        [T,H] out (dtype); may equal dsum or dy (in place).
+ * dweight, dbias  [H] out (dtype), overwritten.
+ * Outputs may be NULL to skip them, not all (T == 0: any).  Sums over
+ * tokens are taken in a fixed order in fp32 and, over workgroups, fp64.
+ * Workspace of moe_norm_backward_workspace_size() bytes, at a multiple of 16
+ * bytes (scratch only).  Limits and errors as moe_norm.  T == 0 writes zeros to
+ * dweight and dbias.
+ */
+size_t moe_norm_backward_workspace_size(int T, int H, int dtype);
+int moe_norm_backward(const void* dy, const void* s, const void* weight,
+                      const float* mean, const float* rstd, const void* dsum,
+                      int T, int H, int kind, int dtype, void* dx, void* dweight,
+                      void* dbias, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * moe_grad_clip -- the norm of many gradients together, and their scaling:
+ *   norm = sqrt(sum over all elements of all tensors of g^2)
+ *   out  = g min(1, max_norm / norm)
+ * The tensors are described by a table that the caller makes once with
+ * moe_grad_table (host code, no device work), copies to the device and keeps
+ * as long as the tensors.
+ *
+ * moe_grad_table: grads, outs (host arrays of n device addresses, a gradient and
+ * where its scaled value goes; outs[i] == grads[i] scales in place), elements
+ * (host i64[n], >= 0), dtypes (host i32[n], MOE_F32 or MOE_BF16, may differ from
+ * tensor to tensor) -> table, host i64[MOE_GRAD_TABLE_WORDS * (n + 1)], and
+ * *blocks.  Addresses are multiples of the element size, and outs[i] and
+ * grads[i] equal modulo 16.  MOE_EINVAL for these, for NULL addresses
+ * of tensors that are not empty, for n outside [0, 2^20] and for tensors
+ * that overlap another one's output.
+ *
+ * table     i64, the device copy.
+ * max_norm  > 0; +inf: the norm alone, nothing is scaled or copied.
+ * norm      f32[1] out.  Squares are summed in fp64 in a fixed order, so that
+ *           no gradient of the type's range overflows.
+ * Where the norm is at most max_norm, and where it is not finite (an
+ * infinite or NaN gradient, for the caller to see in norm), the factor is 1: in
+ * place nothing changes.  Workspace of moe_grad_clip_workspace_size() bytes, at
+ * a multiple of 16 bytes (scratch only).  n == 0 gives norm 0.
+ */
+#define MOE_GRAD_TABLE_WORDS 4
+int moe_grad_table(const void* const* grads, void* const* outs,
+                   const int64_t* elements, const int32_t* dtypes, int n,
+                   int64_t* table, int64_t* blocks);
+size_t moe_grad_clip_workspace_size(int64_t blocks);
+int moe_grad_clip(const int64_t* table, int n, int64_t blocks, double max_norm,
+                  float* norm, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
 #ifdef __cplusplus
 }
 #endif

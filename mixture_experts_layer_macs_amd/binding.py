@@ -27,6 +27,8 @@ MOE_F32, MOE_BF16, MOE_BF16_PANELS = 0, 1, 2
 FLAG_SERE, FLAG_MACS, FLAG_DROP = 1, 2, 4
 WEIGHT_ONE = 65536
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
+NORMS = {"layer": 0, "rms": 1}
+GRAD_TABLE_WORDS = 4
 
 _ERR = {MOE_EINVAL: "MOE_EINVAL (bad argument)",
         MOE_EUNSUP: "MOE_EUNSUP (unsupported type or shape)",
@@ -82,6 +84,17 @@ _SIGS = {
     "moe_router_backward": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_combine_dropout": (_I, [_P, _P, _P, _P, _D, _P, _I, _I, _I, _I, _P, _P]),
     "moe_combine_backward": (_I, [_P, _P, _P, _P, _D, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_grouped_linear_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moe_grouped_linear": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_grouped_linear_backward_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moe_grouped_linear_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P,
+                                         _P, _SZ, _P]),
+    "moe_norm": (_I, [_P, _P, _P, _P, _I, _I, _I, _D, _I, _P, _P, _P, _P, _P]),
+    "moe_norm_backward_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_norm_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "moe_grad_table": (_I, [_P, _P, _P, _P, _I, _P, _P]),
+    "moe_grad_clip_workspace_size": (_SZ, [ctypes.c_int64]),
+    "moe_grad_clip": (_I, [_P, _I, ctypes.c_int64, _D, _P, _P, _SZ, _P]),
 }
 
 
@@ -731,6 +744,187 @@ def moe_combine_backward(dy, out_rows, slot_row, topk_gates, p=0.0, rng=None,
         _arg_opt(d_gates, torch.float32, "d_gates", (T, k), here), _raw_stream(here)),
         "moe_combine_backward")
     return d_out_rows, d_gates
+
+
+# ------------------------------------- experts' training, norm and clipping
+def moe_grouped_linear_workspace_size(R, N, K, O, act, dtype) -> int:
+    return int(_lib.moe_grouped_linear_workspace_size(R, N, K, O, _act(act), _elem(dtype)))
+
+
+def moe_grouped_linear_backward_workspace_size(R, N, K, O, act, dtype) -> int:
+    return int(_lib.moe_grouped_linear_backward_workspace_size(R, N, K, O, _act(act), _elem(dtype)))
+
+
+def moe_grouped_linear(x, w, expert_offsets, workspace, row_token=None, act="none", z=None, y=None):
+    """act(x_t w_e^T) of every dispatched row; z, if given, receives the product
+    before the activation for moe_grouped_linear_backward.  w is [N,O,K], or
+    [N,2O,K] (gate rows, then up rows) for act "swiglu"; row_token [R] gathers
+    the rows from x [T,K], without it x holds them.  Rows of y behind the last
+    expert's stay as they were."""
+    code, dt, d = _act(act), _elem(x.dtype), x.dtype
+    N, W, K = w.shape
+    if act == "swiglu" and W % 2:
+        raise ValueError("swiglu weights need an even number of rows (gate, then up)")
+    O = W // 2 if act == "swiglu" else W
+    T = x.shape[0]
+    R = T if row_token is None else row_token.shape[0]
+    here = _here(x, "x")
+    if y is None:
+        y = _empty((R, O), d, x)
+    _check(_lib.moe_grouped_linear(
+        _arg(x, d, "x", (T, K), here), _arg_opt(row_token, torch.int32, "row_token", (R,), here),
+        _arg(expert_offsets, torch.int32, "expert_offsets", (N + 1,), here),
+        _arg(w, d, "w", (N, W, K), here), T, R, N, K, O, code, dt,
+        _arg_opt(z, d, "z", (R, W), here), _arg(y, d, "y", (R, O), here), *_work(workspace, here),
+        _raw_stream(here)), "moe_grouped_linear")
+    return y
+
+
+def moe_grouped_linear_backward(dy, x, w, expert_offsets, workspace, row_token=None, z=None,
+                                act="none", dx=None, dw=None):
+    """Fills those of dx [R,K] (one row per dispatched row) and dw (as w) that are
+    given with the gradients of moe_grouped_linear; z is moe_grouped_linear's
+    (not needed for act "none").  x may be None without dw, and w without dx."""
+    code, dt, d = _act(act), _elem(dy.dtype), dy.dtype
+    R, O = dy.shape
+    W = 2 * O if act == "swiglu" else O
+    N = expert_offsets.shape[0] - 1
+    if dx is None and dw is None:
+        raise ValueError("no gradient asked for")
+    if dx is not None and w is None:
+        raise ValueError("dx needs w")
+    if dw is not None and x is None:
+        raise ValueError("dw needs x")
+    if z is None and code != 0 and R > 0:
+        raise ValueError(f"act {act!r} needs moe_grouped_linear's z")
+    K = (w if x is None else x).shape[-1]
+    T = R if x is None else x.shape[0]
+    here = _here(dy, "dy")
+    _check(_lib.moe_grouped_linear_backward(
+        _arg(dy, d, "dy", (R, O), here), _arg_opt(x, d, "x", (T, K), here),
+        _arg_opt(row_token, torch.int32, "row_token", (R,), here),
+        _arg(expert_offsets, torch.int32, "expert_offsets", (N + 1,), here),
+        _arg_opt(w, d, "w", (N, W, K), here), _arg_opt(z, d, "z", (R, W), here), T, R, N, K, O, code,
+        dt, _arg_opt(dx, d, "dx", (R, K), here), _arg_opt(dw, d, "dw", (N, W, K), here),
+        *_work(workspace, here), _raw_stream(here)), "moe_grouped_linear_backward")
+    return dx, dw
+
+
+def _kind(kind: str) -> int:
+    if kind not in NORMS:
+        raise ValueError(f"unknown norm {kind!r}, expected one of {sorted(NORMS)}")
+    return NORMS[kind]
+
+
+def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, total=None, y=None,
+             mean=None, rstd=None):
+    """(s - mean) rstd weight + bias of the sum s = x + residual (x without
+    residual); kind "rms" takes mean = 0.  total, needed with residual,
+    receives s; mean and rstd [T], if given, the statistics for
+    moe_norm_backward."""
+    code, dt, d = _kind(kind), _elem(x.dtype), x.dtype
+    T, H = x.shape
+    f32 = torch.float32
+    if residual is not None and total is None:
+        raise ValueError("residual needs total, where the sum goes")
+    here = _here(x, "x")
+    if y is None:
+        y = _empty((T, H), d, x)
+    _check(_lib.moe_norm(
+        _arg(x, d, "x", (T, H), here), _arg_opt(residual, d, "residual", (T, H), here),
+        _arg(weight, d, "weight", (H,), here), _arg_opt(bias, d, "bias", (H,), here), T, H, code, eps,
+        dt, _arg_opt(total, d, "total", (T, H), here), _arg(y, d, "y", (T, H), here),
+        _arg_opt(mean, f32, "mean", (T,), here), _arg_opt(rstd, f32, "rstd", (T,), here),
+        _raw_stream(here)), "moe_norm")
+    return y
+
+
+def moe_norm_backward_workspace_size(T, H, dtype) -> int:
+    return int(_lib.moe_norm_backward_workspace_size(T, H, _elem(dtype)))
+
+
+def moe_norm_backward(dy, s, weight, rstd, workspace, mean=None, dtotal=None, kind="layer", dx=None,
+                      dweight=None, dbias=None):
+    """Fills those of dx [T,H], dweight [H] and dbias [H] that are given with the
+    gradients of moe_norm; s is its total (x without residual), mean (not for
+    kind "rms") and rstd its statistics, dtotal the gradient that reaches the
+    sum past the norm.  weight may be None without dx."""
+    code, dt, d = _kind(kind), _elem(dy.dtype), dy.dtype
+    T, H = dy.shape
+    f32 = torch.float32
+    if dx is None and dweight is None and dbias is None:
+        raise ValueError("no gradient asked for")
+    if dx is not None and weight is None:
+        raise ValueError("dx needs weight")
+    if mean is None and code == 0 and T > 0:
+        raise ValueError('kind "layer" needs mean')
+    here = _here(dy, "dy")
+    _check(_lib.moe_norm_backward(
+        _arg(dy, d, "dy", (T, H), here), _arg(s, d, "s", (T, H), here),
+        _arg_opt(weight, d, "weight", (H,), here), _arg_opt(mean, f32, "mean", (T,), here),
+        _arg(rstd, f32, "rstd", (T,), here), _arg_opt(dtotal, d, "dtotal", (T, H), here), T, H, code,
+        dt, _arg_opt(dx, d, "dx", (T, H), here), _arg_opt(dweight, d, "dweight", (H,), here),
+        _arg_opt(dbias, d, "dbias", (H,), here), *_work(workspace, here), _raw_stream(here)),
+        "moe_norm_backward")
+    return dx, dweight, dbias
+
+
+class GradList:
+    """The gradients of one clipping call and where their scaled values go
+    (outs; without it they are scaled in place), as the table that moe_grad_clip
+    reads on the GPU.  Made once and kept as long as the tensors are used: it
+    holds on to the memory that they have now, on one device.  fp32 and bf16
+    tensors may be mixed.  Making it copies to the GPU and synchronises, so it
+    is made outside a graph capture."""
+
+    def __init__(self, grads, outs=None):
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, but {len(outs)} outputs")
+        if not grads:
+            raise ValueError("no gradients")
+        for i, (t, o) in enumerate(zip(grads, outs)):
+            _dev(t, (torch.float32, torch.bfloat16), f"gradient {i}")
+            _dev(o, t.dtype, f"output {i}", t.shape)
+            if t.device != grads[0].device or o.device != grads[0].device:
+                raise ValueError(f"gradient {i} is not on {grads[0].device}")
+        n = self.n = len(grads)
+        self.device = grads[0].device
+        self._held = [t.untyped_storage() for t in grads + outs]
+        host = torch.empty((n + 1, GRAD_TABLE_WORDS), dtype=torch.int64)
+        blocks = ctypes.c_int64()
+        a = (_P * n)(*[t.data_ptr() for t in grads])
+        o = (_P * n)(*[t.data_ptr() for t in outs])
+        count = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+        types = (ctypes.c_int32 * n)(*[_elem(t.dtype) for t in grads])
+        rc = _lib.moe_grad_table(a, o, count, types, n, host.data_ptr(), ctypes.byref(blocks))
+        if rc == MOE_EINVAL:
+            raise ValueError("moe_grad_table: a tensor overlaps another one's output, or it and its "
+                             "output start at different places modulo 16 bytes")
+        _check(rc, "moe_grad_table")
+        self.blocks = blocks.value
+        self.table = host.to(self.device)
+
+
+def moe_grad_clip_workspace_size(blocks) -> int:
+    return int(_lib.moe_grad_clip_workspace_size(blocks))
+
+
+def moe_grad_clip(grads, max_norm, workspace, norm=None):
+    """Scales the gradients of a GradList so that their norm together is at most
+    max_norm (inf: computes the norm alone); returns norm [1], fp32, on the GPU.
+    Where the norm is not finite nothing is scaled."""
+    if not isinstance(grads, GradList):
+        raise TypeError("grads must be a GradList")
+    here = _here(grads.table, "grads")
+    if norm is None:
+        norm = _empty((1,), torch.float32, grads.table)
+    _check(_lib.moe_grad_clip(
+        _arg(grads.table, torch.int64, "grads", (grads.n + 1, GRAD_TABLE_WORDS), here), grads.n,
+        grads.blocks, max_norm, _arg(norm, torch.float32, "norm", (1,), here),
+        *_work(workspace, here), _raw_stream(here)), "moe_grad_clip")
+    return norm
 
 
 # ------------------------------------------------------------- one layer

@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libmoe_macs.so")
 SOURCES = ["route.hip", "sere.hip", "capacity.hip", "dispatch.hip",
            "routing_fused.hip", "ffn.hip", "combine.hip", "entropy.hip",
            "router.hip", "similarity.hip", "linear.hip", "balance.hip",
-           "combine_train.hip"]
+           "combine_train.hip", "grouped.hip", "norm.hip", "grad_clip.hip"]
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 

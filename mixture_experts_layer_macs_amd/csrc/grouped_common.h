@@ -1,0 +1,60 @@
+// Ragged groups of rows: which expert and which of its rows a tile of a grouped
+// product covers, found on the device from the expert offsets.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+namespace grp {
+
+struct Groups {
+  const int32_t* offsets;  // [N+1]
+  int N, R;                // R: rows that the arrays hold
+};
+
+struct Span {
+  int lo, hi;  // rows of an expert
+};
+
+// Held inside [0, R] whatever the offsets are, so that no row outside the
+// arrays is touched.
+__device__ __forceinline__ Span span_of(const Groups& g, int e) {
+  const int lo = max(0, min(g.offsets[e], g.R));
+  return {lo, max(lo, min(g.offsets[e + 1], g.R))};
+}
+
+struct RowTile {
+  int e, lo, hi;  // the expert and its rows
+  int tile;       // tile among the expert's; e == -1: past the last tile
+  int before;     // tiles of the experts before it
+};
+
+// Tile `at` of the list of all experts' row tiles of `height` rows.  A wave's
+// work, all lanes active, the same result in every lane: 64 experts at a time
+// are scanned with their tile counts in the lanes.
+__device__ __forceinline__ RowTile row_tile(const Groups& g, int height, int at) {
+  const int lane = lane_id();
+  int before = 0;
+  for (int e0 = 0; e0 < g.N; e0 += MOE_WAVE) {
+    const int e = e0 + lane;
+    const Span s = span_of(g, min(e, g.N - 1));
+    const int tiles = e < g.N ? (s.hi - s.lo + height - 1) / height : 0;
+    const int incl = before + wave_incl_scan(tiles);
+    const uint64_t past = __ballot(incl > at);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      const int first = read_lane(incl - tiles, l);
+      return {e0 + l, read_lane(s.lo, l), read_lane(s.hi, l), at - first, first};
+    }
+    before = read_lane(incl, MOE_WAVE - 1);
+  }
+  return {-1, 0, 0, 0, before};
+}
+
+// Most row tiles that R rows in N groups can make.
+inline long max_row_tiles(int R, int N, int height) {
+  return static_cast<long>(R) / height + (R < N ? R : N);
+}
+
+}  // namespace grp
+}  // namespace moe

@@ -20,16 +20,6 @@ namespace moe {
 namespace lin {
 
 // ------------------------------------------------------------ bf16 product
-// The LDS limit is a per-device function attribute: set once per device.
-inline bool allow_lds(const void* fn, int bytes, std::atomic<bool>* done) {
-  const int dev = current_device();
-  if (dev >= 0 && done[dev].load(std::memory_order_acquire)) return true;
-  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
-    return false;
-  if (dev >= 0) done[dev].store(true, std::memory_order_release);
-  return true;
-}
-
 inline int grid_of(const Mma& a) { return (a.tm * a.tn * a.splits + 7) / 8 * 8; }
 
 template <bool RS, bool CS, int BM, int BN, int WGS, bool GLU, bool PART>
@@ -150,32 +140,6 @@ int launch_skinny(Skinny p, int rf, hipStream_t s) {
 }
 
 // ------------------------------------------------ activation gradient, bias
-// dz of V consecutive columns from dy and z, in fp32.  GLU: g ends as the gate
-// half and up as the up half.
-template <typename E, int V>
-__device__ __forceinline__ void act_grad(const E* dy, const E* z, int O, int act, float* g,
-                                         float* up) {
-  load_v<V>(dy, g);
-  if (act == MOE_ACT_NONE) return;
-  float a[V];
-  load_v<V>(z, a);
-  if (act == MOE_ACT_SWIGLU) {
-    load_v<V>(z + O, up);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float sg = sigmoid(a[i]), d = g[i] * silu(a[i], sg);
-      g[i] *= up[i] * silu_slope(a[i], sg);
-      up[i] = d;
-    }
-  } else if (act == MOE_ACT_RELU) {  // a closed unit passes nothing, whatever dy is
-#pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = a[i] <= 0.f ? 0.f : g[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) g[i] *= act_slope<E>(act, a[i]);
-  }
-}
-
 // dz rounded to the element type, the operand of both products: 16 bytes of
 // dy's columns per thread.  Bound by HBM: dy and z read, dz written once (8192 x
 // 768 swiglu: 13 us, 63 MB, 4.8 TB/s).  bf16 is what the matrix instructions
@@ -252,21 +216,7 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(BiasSum b) {
   bias_sum<E>(b, blockIdx.x, red);
 }
 
-template <typename E>
-__global__ void zero_kernel(E* p, size_t n) {
-  const size_t step = gridDim.x * static_cast<size_t>(256);
-  for (size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; i < n; i += step)
-    store1(p + i, 0.f);
-}
-
 // --------------------------------------------------------------------- host
-// Workgroups of 256 threads for n items; kernels loop over what is left beyond
-// 2^22 of them (a grid holds fewer than 2^32 threads).
-inline dim3 grid_of(size_t n) {
-  return dim3(static_cast<unsigned>(std::min<size_t>((n + 255) / 256, size_t(1) << 22)));
-}
-inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 inline int check(int T, int K, int O, int act, int dtype) {
   if (T < 0 || T > (1 << 20) || K < 1 || K > MOE_LINEAR_MAX_DIM || O < 1 ||
       O > MOE_LINEAR_MAX_DIM || act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU)

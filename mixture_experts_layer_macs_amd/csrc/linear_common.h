@@ -1,5 +1,9 @@
-// Activations and the output epilogue of the dense layer.
+// Activations, their gradients and the output epilogue of the dense layer and the
+// grouped products.
 #pragma once
+
+#include <algorithm>
+#include <atomic>
 
 #include "common.h"
 
@@ -78,6 +82,10 @@ __device__ __forceinline__ void store_v(float* p, const float* f) {
 #pragma unroll
   for (int i = 0; i < V; i += 4) store4(p + i, f + i);
 }
+__device__ __forceinline__ float load1(const uint16_t* p) {
+  return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) {
   *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
@@ -253,6 +261,58 @@ __device__ __forceinline__ void bias_sum(const BiasSum& b, int block, float* red
   if (r == 0 && o < b.W)
     store1(static_cast<E*>(b.dbias) + o, (red[c] + red[64 + c]) + (red[128 + c] + red[192 + c]));
 }
+
+// ----------------------------------------------------- activation gradient
+// dz of V consecutive columns from dy and z, in fp32.  GLU: g ends as the gate
+// half and up as the up half.
+template <typename E, int V>
+__device__ __forceinline__ void act_grad(const E* dy, const E* z, int O, int act, float* g,
+                                         float* up) {
+  load_v<V>(dy, g);
+  if (act == MOE_ACT_NONE) return;
+  float a[V];
+  load_v<V>(z, a);
+  if (act == MOE_ACT_SWIGLU) {
+    load_v<V>(z + O, up);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float sg = sigmoid(a[i]), d = g[i] * silu(a[i], sg);
+      g[i] *= up[i] * silu_slope(a[i], sg);
+      up[i] = d;
+    }
+  } else if (act == MOE_ACT_RELU) {  // a closed unit passes nothing, whatever dy is
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = a[i] <= 0.f ? 0.f : g[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] *= act_slope<E>(act, a[i]);
+  }
+}
+
+// ------------------------------------------------------------ host, memory
+// The LDS limit is a per-device function attribute: set once per device.
+inline bool allow_lds(const void* fn, int bytes, std::atomic<bool>* done) {
+  const int dev = current_device();
+  if (dev >= 0 && done[dev].load(std::memory_order_acquire)) return true;
+  if (hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess)
+    return false;
+  if (dev >= 0) done[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+template <typename E>
+__global__ void zero_kernel(E* p, size_t n) {
+  const size_t step = gridDim.x * static_cast<size_t>(256);
+  for (size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; i < n; i += step)
+    store1(p + i, 0.f);
+}
+
+// Workgroups of 256 threads for n items; kernels loop over what is left beyond
+// 2^22 of them (a grid holds fewer than 2^32 threads).
+inline dim3 grid_of(size_t n) {
+  return dim3(static_cast<unsigned>(std::min<size_t>((n + 255) / 256, size_t(1) << 22)));
+}
+inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace lin
 }  // namespace moe

@@ -1,0 +1,697 @@
+"""Grouped products, norm and gradient clipping on the GPU, through the binding,
+against the 64-bit definitions of experts_ref."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import experts_ref as E
+import training_ref as R
+from gpu_util import load_binding, needs_gpu
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+BF16, F32 = torch.bfloat16, torch.float32
+DTYPES = pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+ACTS = ["none", "relu", "silu", "gelu", "swiglu"]
+
+
+@pytest.fixture(scope="module")
+def B():
+    return load_binding()
+
+
+def _rand(g, shape, scale=1.0, dtype=F32):
+    return (torch.from_numpy(g.normal(size=shape)) * scale).to(dtype).cuda()
+
+
+def _near(got, want, bound, what):
+    got = R.f64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == want.shape
+    bad = ~(np.abs(got - want) <= bound + 1e-30)
+    if bad.any():
+        i = np.unravel_index(np.argmax(np.where(bad, np.abs(got - want) / (bound + 1e-30), 0)), got.shape)
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} over the bound, e.g. at {i}: "
+                             f"{got[i]} for {want[i]}, bound {bound[i]:.3e}")
+
+
+def _guard(shape, dtype, pad=64):
+    """A contiguous tensor of sevens inside a buffer of sevens."""
+    n = int(np.prod(shape))
+    buf = torch.full((n + 2 * pad,), 7.0, dtype=dtype, device="cuda")
+    return buf, buf[pad:pad + n].view(shape)
+
+
+def _outside(buf, n, pad=64):
+    return bool((buf[:pad] == 7).all() and (buf[pad + n:] == 7).all())
+
+
+# -------------------------------------------------------------------- grouped
+# rows of each expert, rows behind the last expert's, K, O: no rows, one row, one
+# expert with everything, empty experts at both ends, groups around every tile
+# edge, reductions that end inside a slice, more columns than a tile
+GROUPS = [
+    ([0, 0, 0], 5, 64, 32), ([1], 0, 8, 8), ([0, 1, 0], 3, 72, 24), ([1, 1, 1, 1, 1, 1, 1, 1], 0, 2048, 768),
+    ([3, 0, 7, 1], 2, 136, 264), ([15, 16, 17], 1, 520, 40), ([0, 0, 64, 0], 0, 64, 128), ([63, 65], 9, 200, 136),
+    ([127, 0, 129, 1], 4, 264, 72), ([300], 20, 328, 520), ([255, 257], 0, 72, 264), ([2] * 70, 3, 128, 64),
+    ([513, 3], 5, 136, 776), ([40, 0, 500, 260, 31], 100, 1032, 200), ([33] * 5 + [0] * 130 + [50], 7, 40, 72),
+    ([700, 20], 0, 64, 1544), ([900], 1, 264, 264),
+]
+
+
+def _grouped_inputs(i, act, dtype, gather, seed):
+    counts, behind, K, O = GROUPS[i]
+    g = np.random.default_rng(seed)
+    M = sum(counts)
+    rows = M + behind
+    T = max(1, rows // 2) if gather else rows
+    W = 2 * O if act == "swiglu" else O
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    token = None
+    if gather:  # what stands behind the experts' rows names no token
+        token = np.concatenate([g.integers(0, T, M), np.full(behind, -(1 << 30))]).astype(np.int32)
+    x, w = _rand(g, (T, K), 1.0, dtype), _rand(g, (len(counts), W, K), K ** -0.5, dtype)
+    if not gather:
+        x[M:] = float("nan")
+    dev = lambda a: None if a is None else torch.from_numpy(a).cuda()  # noqa: E731
+    return g, M, rows, O, W, x, w, dev(token), token, dev(offsets), offsets
+
+
+@pytest.mark.parametrize("i", range(len(GROUPS)))
+@DTYPES
+def test_grouped(B, i, dtype):
+    for j in range(2):  # two of the activations with each size, all of them over the sizes
+        act, gather, keep = ACTS[(i + 3 * j) % 5], (i + j) % 2 == 0, (i + j) % 3 != 0
+        print(f"[gpu-test] grouped {GROUPS[i]} {act} {gather} {dtype}", flush=True)
+        g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(i, act, dtype, gather, 10 * i + j)
+        ws = B.new_workspace(B.moe_grouped_linear_workspace_size(rows, len(w), x.shape[1], O, act, dtype), "cuda")
+        ybuf, y = _guard((rows, O), dtype)
+        zbuf, z = _guard((rows, W), dtype)
+        B.moe_grouped_linear(x, w, off, ws, row_token=token, act=act, z=z if keep else None, y=y)
+        yr, zr, ey, ez = E.grouped(R.f64(x), tok, offsets, R.f64(w), act, dtype)
+        _near(y[:M], yr, ey, "y")
+        if keep:
+            _near(z[:M], zr, ez, "z")
+        assert _outside(ybuf, M * O) and _outside(zbuf, M * W if keep else 0)
+        first = y.clone()
+        ws.fill_(0xFF)  # the workspace needs no initialisation
+        B.moe_grouped_linear(x, w, off, ws, row_token=token, act=act, z=z if keep else None, y=y)
+        assert torch.equal(first, y)
+
+
+@pytest.mark.parametrize("i", range(len(GROUPS)))
+@DTYPES
+def test_grouped_backward(B, i, dtype):
+    for j in range(2):
+        act, gather = ACTS[(i + 2 + 3 * j) % 5], (i + j) % 2 == 1
+        print(f"[gpu-test] grouped backward {GROUPS[i]} {act} {gather} {dtype}", flush=True)
+        g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(i, act, dtype, gather, 10 * i + j)
+        K = x.shape[1]
+        dy, z = _rand(g, (rows, O), 0.5, dtype), _rand(g, (rows, W), 1.0, dtype)
+        dy[M:], z[M:] = float("nan"), float("nan")
+        ws = B.new_workspace(B.moe_grouped_linear_backward_workspace_size(rows, len(w), K, O, act, dtype), "cuda")
+        xbuf, dx = _guard((rows, K), dtype)
+        wbuf, dw = _guard(tuple(w.shape), dtype)
+        zz = None if act == "none" else z
+        B.moe_grouped_linear_backward(dy, x, w, off, ws, row_token=token, z=zz, act=act, dx=dx, dw=dw)
+        r = E.grouped_backward(R.f64(dy), R.f64(x), tok, offsets, R.f64(w), R.f64(z), act, dtype)
+        _near(dx[:M], *r["dx"], "dx")
+        _near(dw, *r["dw"], "dw")
+        assert _outside(xbuf, M * K) and _outside(wbuf, dw.numel())
+        first = dx.clone(), dw.clone()
+        ws.fill_(0xFF)
+        B.moe_grouped_linear_backward(dy, x, None, off, ws, row_token=token, z=zz, act=act, dw=dw)
+        B.moe_grouped_linear_backward(dy, None, w, off, ws, z=zz, act=act, dx=dx)
+        # rows behind the experts' stay, so the whole buffers are equal
+        assert torch.equal(first[0], dx) and torch.equal(first[1], dw)
+
+
+@DTYPES
+def test_grouped_keeps_experts_apart(B, dtype):
+    """A row of NaN, an expert whose weights are infinite and the rows behind the
+    last expert's reach only what is theirs."""
+    g = np.random.default_rng(2)
+    counts, K, O = [20, 0, 70, 33, 5], 136, 72
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    M, N = 128, len(counts)
+    x, w = _rand(g, (M + 6, K), 1.0, dtype), _rand(g, (N, O, K), 0.1, dtype)
+    dy = _rand(g, (M + 6, O), 1.0, dtype)
+    x[M:], dy[M:] = float("nan"), float("nan")
+    ws = B.new_workspace(1 << 16, "cuda")
+    y0 = B.moe_grouped_linear(x, w, off, ws, y=torch.zeros(M + 6, O, dtype=dtype, device="cuda"))
+    dx0, dw0 = torch.zeros_like(x), torch.zeros_like(w)
+    B.moe_grouped_linear_backward(dy, x, w, off, ws, dx=dx0, dw=dw0)
+    x[25], dy[25], w[1], w[3] = float("nan"), float("nan"), float("nan"), float("inf")
+    y1 = B.moe_grouped_linear(x, w, off, ws, y=torch.zeros_like(y0))
+    dx1, dw1 = torch.zeros_like(x), torch.zeros_like(w)
+    B.moe_grouped_linear_backward(dy, x, w, off, ws, dx=dx1, dw=dw1)
+    same = torch.ones(M + 6, dtype=torch.bool, device="cuda")
+    same[25] = False
+    same[90:123] = False  # expert 3
+    assert torch.equal(y0[same], y1[same]) and torch.equal(dx0[same], dx1[same])
+    assert not torch.isfinite(y1[~same].float()).any() and not torch.isfinite(dx1[~same].float()).any()
+    assert torch.equal(dw0[[0, 1, 3, 4]], dw1[[0, 1, 3, 4]]) and torch.isnan(dw1[2].float()).all()
+    assert (dw1[1] == 0).all()
+
+
+@DTYPES
+def test_grouped_without_rows(B, dtype):
+    w = torch.ones(4, 32, 64, dtype=dtype, device="cuda")
+    off = torch.zeros(5, dtype=torch.int32, device="cuda")
+    x, dy = torch.empty(0, 64, dtype=dtype, device="cuda"), torch.empty(0, 32, dtype=dtype, device="cuda")
+    ws = B.new_workspace(B.moe_grouped_linear_backward_workspace_size(0, 4, 64, 32, "silu", dtype), "cuda")
+    assert B.moe_grouped_linear(x, w, off, ws).shape == (0, 32)
+    dw = torch.full_like(w, 7.0)
+    B.moe_grouped_linear_backward(dy, x, w, off, ws, act="silu", dx=torch.empty_like(x), dw=dw)
+    assert (dw == 0).all()
+
+
+@DTYPES
+def test_grouped_offsets_outside_the_rows_touch_nothing_else(B, dtype):
+    """Offsets past the arrays' rows are held inside them."""
+    g = np.random.default_rng(3)
+    x, w = _rand(g, (40, 64), 1.0, dtype), _rand(g, (3, 32, 64), 0.1, dtype)
+    off = torch.tensor([0, 30, 5000, 9000], dtype=torch.int32, device="cuda")
+    ws = B.new_workspace(1 << 16, "cuda")
+    buf, y = _guard((40, 32), dtype)
+    B.moe_grouped_linear(x, w, off, ws, y=y)
+    want = E.grouped(R.f64(x), None, [0, 30, 40, 40], R.f64(w), "none", dtype)
+    _near(y, want[0], want[2], "y")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    B.moe_grouped_linear_backward(y, x, w, off, ws, dx=dx, dw=dw)
+    r = E.grouped_backward(R.f64(y), R.f64(x), None, [0, 30, 40, 40], R.f64(w), R.f64(y), "none", dtype)
+    _near(dx, *r["dx"], "dx")
+    _near(dw, *r["dw"], "dw")
+    assert _outside(buf, 40 * 32)
+
+
+def test_grouped_with_more_than_2_31_elements(B):
+    """Weights of 2.2e9 elements, rows of outputs beyond 2^31 and their gradients,
+    compared in the last expert."""
+    g = np.random.default_rng(4)
+    N, K, O, M = 130, 2056, 8264, 130 * 2
+    w = torch.zeros(N, O, K, dtype=BF16, device="cuda")
+    w[-1] = _rand(g, (O, K), K ** -0.5, BF16)
+    off = torch.arange(0, M + 1, 2, dtype=torch.int32, device="cuda")
+    x, dy = _rand(g, (M, K), 1.0, BF16), _rand(g, (M, O), 1.0, BF16)
+    ws = B.new_workspace(B.moe_grouped_linear_backward_workspace_size(M, N, K, O, "none", BF16), "cuda")
+    y = B.moe_grouped_linear(x, w, off, ws)
+    yr, _, ey, _ = E.grouped(R.f64(x[-2:]), None, [0, 2], R.f64(w[-1:]), "none", BF16)
+    _near(y[-2:], yr, ey, "y")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    B.moe_grouped_linear_backward(dy, x, w, off, ws, dx=dx, dw=dw)
+    r = E.grouped_backward(R.f64(dy[-2:]), R.f64(x[-2:]), None, [0, 2], R.f64(w[-1:]), np.zeros((2, O)), "none", BF16)
+    _near(dx[-2:], *r["dx"], "dx")
+    _near(dw[-1:], *r["dw"], "dw")
+    del w, dw
+    M, K, O = 300000, 64, 7304  # y and dz: 2.19e9 elements
+    off = torch.tensor([0, 3, M - 40, M], dtype=torch.int32, device="cuda")
+    x, w = _rand(g, (M, K), 1.0, BF16), _rand(g, (3, O, K), K ** -0.5, BF16)
+    ws = B.new_workspace(B.moe_grouped_linear_backward_workspace_size(M, 3, K, O, "silu", BF16), "cuda")
+    z = torch.empty(M, O, dtype=BF16, device="cuda")
+    y = B.moe_grouped_linear(x, w, off, ws, act="silu", z=z)
+    yr, zr, ey, ez = E.grouped(R.f64(x[-40:]), None, [0, 40], R.f64(w[-1:]), "silu", BF16)
+    _near(y[-40:], yr, ey, "y")
+    _near(z[-40:], zr, ez, "z")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    B.moe_grouped_linear_backward(y, x, w, off, ws, z=z, act="silu", dx=dx, dw=dw)
+    r = E.grouped_backward(R.f64(y[-40:]), R.f64(x[-40:]), None, [0, 40], R.f64(w[-1:]), R.f64(z[-40:]), "silu", BF16)
+    _near(dx[-40:], *r["dx"], "dx")
+    _near(dw[-1:], *r["dw"], "dw")
+
+
+def test_grouped_equals_the_expert_ffn(B):
+    """The two halves against moe_expert_ffn on the same dispatch: the same
+    formula, so the rows differ by roundings of h and of themselves."""
+    from mixture_experts_layer_macs_amd import configs, synth
+    from mixture_experts_layer_macs_amd.staging import to_device
+    wl = configs.QWEN3_DECODE.with_(T=96, H=512, I=256)
+    d = to_device(synth.make_inputs(wl, 1), "cuda", weights=True)
+    lay = B.Layer(wl.T, wl.H, wl.N, wl.k, wl.I, wl.R, BF16)
+    lay.forward(d["logits"], d["x"], d["w13"], d["w2"], d["is_visual"], d["entropy_w"], d["modality"], d["sim"],
+                d["prot"], wl.kprime, wl.rho, wl.gamma, wl.lam, wl.group)
+    M = int(lay.disp["expert_offsets"][-1])
+    off, ws = lay.disp["expert_offsets"], B.new_workspace(1 << 16, "cuda")
+    h = B.moe_grouped_linear(d["x"], d["w13"], off, ws, row_token=lay.disp["row_token"], act="swiglu")
+    rows = B.moe_grouped_linear(h, d["w2"], off, ws)
+    a, b = rows[:M].double(), lay.out_rows[:M].double()
+    assert float((a - b).norm() / b.norm()) <= 2 * 2.0 ** -8
+
+
+# ----------------------------------------------------------------------- norm
+# T, H: single rows, every width class of the kernels and its edges
+NORMS = [(1, 8), (1, 2048), (3, 64), (5, 128), (17, 136), (40, 256), (33, 512), (9, 520), (130, 1024), (65, 1032),
+         (2, 2056), (1030, 96), (700, 2048), (6, 4096), (5, 4104), (3, 8192), (4, 8200), (2, 65536), (2500, 24)]
+
+
+def _norm_inputs(T, H, dtype, seed):
+    g = np.random.default_rng(seed)
+    x, res = _rand(g, (T, H), 1.0, dtype), _rand(g, (T, H), 2.0, dtype) + 0.5
+    return g, x, res.to(dtype), (1 + _rand(g, (H,), 0.3)).to(dtype), _rand(g, (H,), 0.3, dtype)
+
+
+@pytest.mark.parametrize("i", range(len(NORMS)))
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@DTYPES
+def test_norm(B, i, kind, dtype):
+    T, H = NORMS[i]
+    print(f"[gpu-test] norm {T} {H} {kind} {dtype}", flush=True)
+    g, x, res, w, b = _norm_inputs(T, H, dtype, i)
+    residual, bias = i % 3 != 0, i % 2 == 0
+    bufs = [_guard((T, H), dtype) for _ in range(3)]
+    (_, total), (_, y), (_, dx) = bufs
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    B.moe_norm(x, w, bias=b if bias else None, residual=res if residual else None, kind=kind, eps=1e-5,
+               total=total if residual else None, y=y, mean=mean, rstd=rstd)
+    s = x
+    if residual:
+        assert torch.equal(total, (x.float() + res.float()).to(dtype))
+        s = total
+    want = E.norm(R.f64(s), R.f64(w), R.f64(b) if bias else None, kind, 1e-5, dtype)
+    for name, got in (("y", y), ("mean", mean), ("rstd", rstd)):
+        _near(got, *want[name], name)
+    # the backward pass of these statistics
+    dy, ds = _rand(g, (T, H), 0.5, dtype), _rand(g, (T, H), 0.5, dtype) if residual else None
+    wbuf, dw = _guard((H,), dtype)
+    bbuf, db = _guard((H,), dtype)
+    ws = B.new_workspace(B.moe_norm_backward_workspace_size(T, H, dtype), "cuda")
+    ws.fill_(0xFF)
+    st = dict(mean=mean if kind == "layer" else None, kind=kind)
+    B.moe_norm_backward(dy, s, w, rstd, ws, dtotal=ds, dx=dx, dweight=dw, dbias=db, **st)
+    r = E.norm_backward(R.f64(dy), R.f64(s), R.f64(w), R.f64(mean), R.f64(rstd), R.f64(ds), kind, dtype)
+    for name, got in (("dx", dx), ("dw", dw), ("db", db)):
+        _near(got, *r[name], name)
+    assert all(_outside(q, T * H) for q, _ in bufs[1:]) and _outside(wbuf, H) and _outside(bbuf, H)
+    # each output alone, and dx in the place of dy or dsum, give the same bits
+    one = torch.full_like(dw, 7.0)
+    B.moe_norm_backward(dy, s, None, rstd, ws, dweight=one, **st)
+    assert torch.equal(one, dw)
+    B.moe_norm_backward(dy, s, None, rstd, ws, dbias=one, **st)
+    assert torch.equal(one, db)
+    for place in ([dy] if ds is None else [ds, dy]):
+        keep = place.clone()
+        B.moe_norm_backward(dy, s, w, rstd, ws, dtotal=ds, dx=place, dweight=one, **st)
+        assert torch.equal(place, dx) and torch.equal(one, dw)
+        place.copy_(keep)
+
+
+@pytest.mark.parametrize("H", [24, 256, 2048, 4104, 65536])
+@DTYPES
+def test_norm_in_place(B, H, dtype):
+    _, x, res, w, b = _norm_inputs(5, H, dtype, 1)
+    total = torch.empty_like(x)
+    y = B.moe_norm(x, w, bias=b, residual=res, total=total)
+    p, q = x.clone(), res.clone()
+    B.moe_norm(p, w, bias=b, residual=q, total=q, y=p)  # the stream in the residual's place, y in x's
+    assert torch.equal(p, y) and torch.equal(q, total)
+    p, q = x.clone(), res.clone()
+    B.moe_norm(p, w, bias=b, residual=q, total=p, y=q)
+    assert torch.equal(q, y) and torch.equal(p, total)
+
+
+@pytest.mark.parametrize("H", [64, 2048, 65536])
+@DTYPES
+def test_norm_of_rows_far_from_zero(B, H, dtype):
+    """A mean far above the deviation: the variance is that of the centred values."""
+    g = np.random.default_rng(5)
+    x = (_rand(g, (7, H), 1.0) + 64).to(dtype)
+    w = torch.ones(H, dtype=dtype, device="cuda")
+    y = B.moe_norm(x, w)
+    want = E.norm(R.f64(x), R.f64(w), None, "layer", 1e-5, dtype)["y"]
+    _near(y, *want, "y")
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_norm_of_constant_large_and_broken_rows(B, kind):
+    """Constant rows give the bias; a row of NaN or infinity stays its own."""
+    H = 256
+    x = torch.ones(6, H, device="cuda")
+    x[0] = 0
+    x[1] = 3
+    x[2, 5] = float("nan")
+    x[3, 7] = float("inf")
+    x[4] = torch.linspace(-1e15, 1e15, H)
+    x[5] = torch.linspace(-1e-15, 1e-15, H)
+    w, b = torch.full((H,), 2.0, device="cuda"), torch.full((H,), 0.5, device="cuda")
+    y = B.moe_norm(x, w, bias=b, kind=kind, eps=1e-30)
+    assert (y[0] == 0.5).all()
+    if kind == "layer":
+        assert (y[1] == 0.5).all()
+    assert torch.isnan(y[2]).all() and torch.isnan(y[3]).any()
+    for r in (4, 5):
+        want = E.norm(R.f64(x[r:r + 1]), R.f64(w), R.f64(b), kind, 1e-30, F32)["y"]
+        _near(y[r:r + 1], *want, f"row {r}")
+
+
+@DTYPES
+def test_norm_without_tokens(B, dtype):
+    e, w = torch.empty(0, 64, dtype=dtype, device="cuda"), torch.ones(64, dtype=dtype, device="cuda")
+    assert B.moe_norm(e, w).shape == (0, 64)
+    dw, db = torch.full_like(w, 7.0), torch.full_like(w, 7.0)
+    st = torch.empty(0, device="cuda")
+    B.moe_norm_backward(e, e, w, st, B.new_workspace(256, "cuda"), mean=st, dx=e, dweight=dw, dbias=db)
+    assert (dw == 0).all() and (db == 0).all()
+
+
+def test_norm_with_more_than_2_31_elements(B):
+    T, H = 300000, 7304
+    x = torch.empty(T, H, dtype=BF16, device="cuda").normal_()
+    w = torch.full((H,), 1.5, dtype=BF16, device="cuda")
+    rstd = torch.empty(T, device="cuda")
+    y = B.moe_norm(x, w, kind="rms", rstd=rstd)
+    at = [0, T // 2, T - 1]
+    want = E.norm(R.f64(x[at]), R.f64(w), None, "rms", 1e-5, BF16)
+    _near(y[at], *want["y"], "y")
+    dx = torch.empty_like(x)
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    ws = B.new_workspace(B.moe_norm_backward_workspace_size(T, H, BF16), "cuda")
+    B.moe_norm_backward(y, x, w, rstd, ws, kind="rms", dx=dx, dweight=dw, dbias=db)
+    r = E.norm_backward(R.f64(y[at]), R.f64(x[at]), R.f64(w), None, R.f64(rstd[at]), None, "rms", BF16)
+    _near(dx[at], *r["dx"], "dx")
+    cols = [0, 1, 4095, H - 1]  # whole columns
+    r = E.norm_backward(R.f64(y[:, cols]), R.f64(x[:, cols]), R.f64(w[cols]), None, R.f64(rstd), None, "rms", BF16)
+    _near(dw[cols], *r["dw"], "dw")
+    _near(db[cols], *r["db"], "db")
+
+
+def test_norm_sums_of_many_rows(B):
+    """2^20 rows: ones and a large value that cancels at the end; fp64 between the
+    workgroups, so the columns' sums keep the units."""
+    T = 1 << 20
+    dy = torch.ones(T, 8, device="cuda")
+    dy[0, 1], dy[T - 1, 1] = 3e7, -3e7
+    s, rstd = torch.ones(T, 8, device="cuda"), torch.ones(T, device="cuda")
+    dw, db = torch.empty(8, device="cuda"), torch.empty(8, device="cuda")
+    ws = B.new_workspace(B.moe_norm_backward_workspace_size(T, 8, F32), "cuda")
+    B.moe_norm_backward(dy, s, None, rstd, ws, kind="rms", dweight=dw, dbias=db)
+    r = E.norm_backward(R.f64(dy), R.f64(s), np.ones(8), None, np.ones(T), None, "rms", F32)
+    _near(dw, *r["dw"], "dw")
+    _near(db, *r["db"], "db")
+    assert float(db[0]) == T
+
+
+# ------------------------------------------------------------------- clipping
+def _check_clip(grads, before, outs, norm, max_norm):
+    """norm: sums in fp64, one rounding to fp32 and a few units of the sums; a
+    scaled value: the factor's and the product's rounding in fp32, then the type's."""
+    want, c = E.clip([R.f64(t) for t in before], max_norm)
+    assert abs(float(norm) - want) <= want * 1.01 * R.U
+    for i, (o, t) in enumerate(zip(outs, before)):
+        v = R.f64(t) * c
+        h = R.half(o.dtype)
+        e = 0 if c == 1 else 3 * R.U * np.abs(v)
+        # the smallest step of the type where the value leaves its normal range
+        _near(o, v, (e + h * np.abs(v) if c != 1 else 0 * v) + (2.0 ** -133 if c != 1 else 0), f"gradient {i}")
+
+
+SHAPES = [(1,), (7,), (0,), (8,), (129, 65), (32768,), (32769,), (3, 5, 7), (300, 1000), (16384,), (0, 4), (65536 * 3 + 1,)]
+
+
+@pytest.mark.parametrize("mix", ["bf16", "f32", "both"])
+@pytest.mark.parametrize("place", ["in", "out"])
+def test_clip(B, mix, place):
+    g = np.random.default_rng(6)
+    types = [BF16 if mix == "bf16" or mix == "both" and i % 2 else F32 for i in range(len(SHAPES))]
+    bufs = [_guard(s, t) for s, t in zip(SHAPES, types)]
+    for (_, v), s, t in zip(bufs, SHAPES, types):
+        v.copy_(_rand(g, s, 10.0 ** -g.integers(0, 4), t))
+    grads = [v for _, v in bufs]
+    before = [v.clone() for v in grads]
+    outs = grads if place == "in" else [torch.full_like(v, 7.0) for v in grads]
+    lst = B.GradList(grads, outs)
+    ws = B.new_workspace(B.moe_grad_clip_workspace_size(lst.blocks), "cuda")
+    ws.fill_(0xFF)
+    for max_norm in (1.0, 1e6, math.inf):
+        for v, o in zip(grads, before):
+            v.copy_(o)
+        norm = B.moe_grad_clip(lst, max_norm, ws)
+        if max_norm < math.inf:
+            _check_clip(grads, before, outs, norm, max_norm)
+        else:
+            assert all(torch.equal(a, b) for a, b in zip(grads, before))
+        first = [o.clone() for o in outs]
+        for v, o in zip(grads, before):
+            v.copy_(o)
+        again = B.moe_grad_clip(lst, max_norm, ws)
+        assert torch.equal(norm, again) and all(torch.equal(a, b) for a, b in zip(first, outs))
+    assert all(_outside(buf, v.numel()) for buf, v in bufs)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_clip_of_unaligned_views(B, dtype):
+    """Tensors that start and end anywhere inside a 16-byte piece, side by side."""
+    g = np.random.default_rng(7)
+    sizes = [1, 2, 3, 5, 9, 17, 4093, 32765, 33001]
+    buf = _rand(g, (sum(sizes) + 11,), 1.0, dtype)
+    at, grads = 3, []
+    for n in sizes:
+        grads.append(buf[at:at + n])
+        at += n
+    keep = buf.clone()
+    before = [v.clone() for v in grads]
+    lst = B.GradList(grads)
+    ws = B.new_workspace(B.moe_grad_clip_workspace_size(lst.blocks), "cuda")
+    norm = B.moe_grad_clip(lst, 0.5, ws)
+    _check_clip(grads, before, grads, norm, 0.5)
+    assert torch.equal(buf[:3], keep[:3]) and torch.equal(buf[at:], keep[at:])
+
+
+def test_clip_of_extreme_gradients(B):
+    """Squares beyond fp32's range at both ends; a gradient that is not finite
+    shows in the norm and changes nothing."""
+    for value in (1e30, 3e38, 1e-30, 1e-42):
+        t = torch.full((1000,), value, device="cuda")
+        before = t.clone()
+        lst = B.GradList([t])
+        ws = B.new_workspace(B.moe_grad_clip_workspace_size(lst.blocks), "cuda")
+        norm = B.moe_grad_clip(lst, math.inf, ws)
+        want = math.sqrt(1000) * float(before[0])
+        if want < 3.4e38:
+            tiny = 2.0 ** -149
+            assert abs(float(norm) - want) <= want * 1.01 * R.U + tiny
+        else:
+            assert math.isinf(float(norm))
+        B.moe_grad_clip(lst, 1.0, ws)
+        if value > 1:  # scaled by 1 / norm, whether or not the norm itself fits fp32
+            assert torch.allclose(t, torch.full_like(t, 1 / math.sqrt(1000)), rtol=4 * R.U, atol=0)
+        else:
+            assert torch.equal(t, before)
+    for bad in (float("nan"), float("inf")):
+        a, b = torch.ones(5000, device="cuda"), torch.ones(70000, dtype=BF16, device="cuda")
+        b[69999] = bad
+        lst = B.GradList([a, b])
+        norm = B.moe_grad_clip(lst, 1.0, B.new_workspace(B.moe_grad_clip_workspace_size(lst.blocks), "cuda"))
+        assert not math.isfinite(float(norm))
+        assert (a == 1).all() and (b[:69999] == 1).all()
+
+
+def test_clip_of_many_tensors_and_one_large(B):
+    g = np.random.default_rng(8)
+    small = [_rand(g, (int(n),), 1.0, BF16 if n % 2 else F32) for n in g.integers(1, 5000, 1500)]
+    big = torch.zeros((1 << 31) + 64, dtype=BF16, device="cuda")  # beyond 2^31 elements
+    big[-3:] = 5.0
+    grads = small + [big]
+    before = [v.clone() for v in small]
+    lst = B.GradList(grads)
+    ws = B.new_workspace(B.moe_grad_clip_workspace_size(lst.blocks), "cuda")
+    norm = B.moe_grad_clip(lst, 1.0, ws)
+    want, c = E.clip([R.f64(t) for t in before] + [np.full(3, 5.0)], 1.0)
+    assert abs(float(norm) - want) <= want * 1.01 * R.U
+    for o, t in zip(small, before):
+        v = R.f64(t) * c
+        _near(o, v, (3 * R.U + R.half(o.dtype)) * np.abs(v), "gradient")
+    assert abs(float(big[-1]) - 5 * c) <= (3 * R.U + 2.0 ** -8) * 5 * c and float(big[0]) == 0
+
+
+def test_clip_refusals(B):
+    a = torch.ones(100, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        B.GradList([a, a])
+    with pytest.raises(ValueError, match="overlaps"):
+        B.GradList([a[:60], a[50:]])
+    with pytest.raises(ValueError, match="overlaps"):
+        B.GradList([a[1:]], [torch.ones(99, device="cuda")])
+    with pytest.raises(ValueError, match="contiguous"):
+        B.GradList([torch.ones(4, 4, device="cuda").t()])
+    with pytest.raises(ValueError, match="dtype"):
+        B.GradList([a.half()])
+    with pytest.raises(ValueError, match="shape"):
+        B.GradList([a], [torch.ones(50, device="cuda")])
+    lst = B.GradList([a])
+    with pytest.raises(RuntimeError, match="EINVAL"):
+        B.moe_grad_clip(lst, 0.0, B.new_workspace(1 << 16, "cuda"))
+    with pytest.raises(RuntimeError, match="EINVAL"):
+        B.moe_grad_clip(lst, 1.0, B.new_workspace(4, "cuda")[:2])
+
+
+def test_grouped_refusals(B):
+    x, w, off = (torch.zeros(*s, device="cuda") for s in ((4, 64), (2, 32, 64), (3,)))
+    off = off.int()
+    ws = B.new_workspace(1 << 16, "cuda")
+    with pytest.raises(ValueError, match="expert_offsets"):
+        B.moe_grouped_linear(x, w, off[:2].clone(), ws)
+    with pytest.raises(ValueError, match="dtype"):
+        B.moe_grouped_linear(x, w, off.long(), ws)
+    with pytest.raises(ValueError, match="shape"):
+        B.moe_grouped_linear(x, w, off, ws, row_token=torch.zeros(6, dtype=torch.int32, device="cuda"),
+                             y=torch.zeros(4, 32, device="cuda"))
+    with pytest.raises(RuntimeError, match="EUNSUP"):
+        B.moe_grouped_linear(torch.zeros(4, 62, device="cuda"), torch.zeros(2, 32, 62, device="cuda"), off, ws)
+    with pytest.raises(RuntimeError, match="EINVAL"):
+        B.moe_grouped_linear_backward(torch.zeros(4, 32, device="cuda"), x, w, off, ws[:100],
+                                      z=torch.zeros(4, 32, device="cuda"), act="silu", dx=torch.zeros_like(x))
+    with pytest.raises(ValueError, match="contiguous"):
+        B.moe_norm(x.t().contiguous().t(), w[0, 0])
+
+
+# -------------------------------------------------------------- a whole step
+class _Step:
+    """One training step of a whole layer (norm, router, routed experts) with its
+    residual stream, as a user's program runs it: forward, loss, every gradient,
+    clipping."""
+
+    def __init__(self, B, T=96, H=256, N=16, k=4, I=128, dtype=BF16, seed=0):
+        self.B, self.k, self.N, self.T = B, k, N, T
+        g = np.random.default_rng(seed)
+        c = lambda *s: _rand(g, s, s[-1] ** -0.5, dtype)  # noqa: E731
+        e = lambda *s: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+        f = lambda *s: torch.empty(s, device="cuda")  # noqa: E731
+        self.x, self.res, self.target = (_rand(g, (T, H), 1.0, dtype) for _ in range(3))
+        self.nw, self.wg, self.w13, self.w2 = (1 + c(H)).to(dtype), c(N, H), c(N, 2 * I, H), c(N, H, I)
+        self.lay = B.Layer(T, H, N, k, I, 0, dtype)
+        n = lambda size: B.new_workspace(size, "cuda")  # noqa: E731
+        self.ws_router = n(B.moe_router_workspace_size(T, N, H, dtype))
+        self.ws = n(max(B.moe_grouped_linear_workspace_size(T * k, N, H, I, "swiglu", dtype),
+                        B.moe_grouped_linear_workspace_size(T * k, N, I, H, "none", dtype),
+                        B.moe_grouped_linear_backward_workspace_size(T * k, N, H, I, "swiglu", dtype),
+                        B.moe_grouped_linear_backward_workspace_size(T * k, N, I, H, "none", dtype),
+                        B.moe_linear_backward_workspace_size(T, H, N, "none", dtype),
+                        B.moe_balance_workspace_size(T, N), B.moe_norm_backward_workspace_size(T, H, dtype),
+                        1 << 16))
+        self.total, self.h, self.y, self.dy = e(T, H), e(T, H), e(T, H), e(T, H)
+        self.rstd, self.logits = f(T), f(T, N)
+        # rows behind the last expert's are not written: zeros from the start
+        zeros = lambda *s: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+        R_ = T * k
+        self.z, self.a, self.rows = zeros(R_, 2 * I), zeros(R_, I), zeros(R_, H)
+        self.d_rows, self.da, self.dxr = zeros(R_, H), zeros(R_, I), zeros(R_, H)
+        self.dg, self.dl, self.dh, self.dhr = f(T, k), e(T, N), e(T, H), e(T, H)
+        self.ones = torch.ones(T, k, device="cuda")
+        self.loss = dict(losses=f(2), counts=torch.empty(N + 1, dtype=torch.int32, device="cuda"), mean_prob=f(N), lse=f(T))
+        self.d_losses = torch.tensor([0.02, 0.001], device="cuda")
+        self.grads = dict(wg=e(N, H), w13=e(N, 2 * I, H), w2=e(N, H, I), nw=e(H))
+        self.dx, self.norm = e(T, H), f(1)
+        self.clipped = {name: torch.empty_like(t) for name, t in self.grads.items()}
+        self.list = B.GradList(self.grads.values(), self.clipped.values())
+
+    def run(self):
+        B, lay, k, G, d = self.B, self.lay, self.k, self.grads, self.lay.disp
+        token, off, slot_row = d["row_token"], d["expert_offsets"], d["slot_row"]
+        B.moe_norm(self.x, self.nw, residual=self.res, kind="rms", total=self.total, y=self.h, rstd=self.rstd)
+        B.moe_router_topk(self.h, self.wg, k, 0, self.ws_router, self.logits, lay.topk_ids, lay.topk_gates,
+                          lay.fallback_ids)
+        B.moe_dispatch(lay.topk_ids, self.N, lay.ws_disp, d)
+        B.moe_grouped_linear(self.h, self.w13, off, self.ws, row_token=token, act="swiglu", z=self.z, y=self.a)
+        B.moe_grouped_linear(self.a, self.w2, off, self.ws, y=self.rows)
+        B.moe_combine_dropout(self.rows, slot_row, lay.topk_gates, residual=self.total, y=self.y)
+        B.moe_balance_loss(self.logits, lay.topk_ids, self.ws, None, self.loss)
+        torch.sub(self.y, self.target, out=self.dy)
+        B.moe_combine_backward(self.dy, self.rows, slot_row, lay.topk_gates, d_out_rows=self.d_rows, d_gates=self.dg)
+        B.moe_grouped_linear_backward(self.d_rows, self.a, self.w2, off, self.ws, dx=self.da, dw=G["w2"])
+        B.moe_grouped_linear_backward(self.da, self.h, self.w13, off, self.ws, row_token=token, z=self.z,
+                                      act="swiglu", dx=self.dxr, dw=G["w13"])
+        B.moe_router_backward(self.logits, lay.topk_ids, self.loss["lse"], self.loss["counts"], self.d_losses,
+                              None, self.dg, self.dl)
+        B.moe_linear_backward(self.dl, self.h, self.wg, self.ws, dx=self.dhr, dw=G["wg"])
+        # the tokens' gradient: the sum of their rows, and the router's
+        B.moe_combine_dropout(self.dxr, slot_row, self.ones, residual=self.dhr, y=self.dh)
+        B.moe_norm_backward(self.dh, self.total, self.nw, self.rstd, self.ws, dtotal=self.dy, kind="rms",
+                            dx=self.dx, dweight=G["nw"])
+        B.moe_grad_clip(self.list, 0.5, self.ws, self.norm)
+
+    def outputs(self):
+        return {"y": self.y, "dx": self.dx, "norm": self.norm, **self.grads,
+                **{"clipped_" + n: t for n, t in self.clipped.items()}}
+
+
+def test_training_step_against_autograd(B):
+    """The step's gradients against a 64-bit autograd of the same step (same
+    routing).  Every intermediate that the kernels hand on in bf16 is off by half
+    a step, 2^-8; a dozen such roundings along a chain keep the relative error of
+    a whole gradient tensor (2-norm) under 12 2^-8."""
+    st = _Step(B)
+    st.run()
+    T, k, N = st.T, st.k, st.N
+    D = lambda t: t.detach().double().cpu()  # noqa: E731
+    total, nw, wg, w13, w2 = (D(t).requires_grad_() for t in (st.total, st.nw, st.wg, st.w13, st.w2))
+    ids = st.lay.topk_ids.cpu().long()
+    h = total / torch.sqrt((total ** 2).mean(1, keepdim=True) + 1e-5) * nw
+    logits = h @ wg.t()
+    prob = torch.softmax(logits, 1)
+    gates = prob.gather(1, ids)
+    I = w2.shape[2]
+    y = total
+    for s in range(k):
+        z = torch.bmm(w13[ids[:, s]], h[:, :, None])[:, :, 0]
+        a = torch.nn.functional.silu(z[:, :I]) * z[:, I:]
+        y = y + gates[:, s:s + 1] * torch.bmm(w2[ids[:, s]], a[:, :, None])[:, :, 0]
+    counts = torch.bincount(ids.reshape(-1), minlength=N).double()
+    loss = 0.5 * ((y - D(st.target)) ** 2).sum() + 0.02 * N / (k * T) * (counts * prob.mean(0)).sum() \
+        + 0.001 * (torch.logsumexp(logits, 1) ** 2).mean()
+    loss.backward()
+    want = dict(y=y.detach(), dx=total.grad, wg=wg.grad, w13=w13.grad, w2=w2.grad, nw=nw.grad)
+    norm = math.sqrt(sum(float((want[n] ** 2).sum()) for n in ("wg", "w13", "w2", "nw")))
+    assert norm > 0.5
+    want.update({"clipped_" + n: want[n] * (0.5 / norm) for n in ("wg", "w13", "w2", "nw")}, norm=torch.tensor([norm]))
+    for name, v in want.items():
+        got = D(st.outputs()[name])
+        rel = float((got - v).norm() / v.norm())
+        print(f"[gpu-test] step {name}: {rel:.2e}", flush=True)
+        assert rel <= 12 * 2.0 ** -8, (name, rel)
+
+
+def test_training_step_on_a_side_stream(B):
+    st = _Step(B, seed=1)
+    st.run()
+    torch.cuda.synchronize()
+    want = {n: t.clone() for n, t in st.outputs().items()}
+    for t in st.outputs().values():
+        t.zero_()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        st.run()
+    side.synchronize()
+    for n, t in st.outputs().items():
+        assert torch.equal(t, want[n]), n
+
+
+def test_training_steps_captured_with_one_workspace(B):
+    """Two captured steps that share a workspace, replayed in turn with eager work
+    between; the inputs, and so the routing, change between replays, and every
+    replay equals the eager step."""
+    a, b = _Step(B, seed=2), _Step(B, T=80, seed=3)
+    if b.ws.numel() > a.ws.numel():
+        a.ws = b.ws
+    b.ws = a.ws
+    graphs = []
+    for st in (a, b):
+        st.run()
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            st.run()
+        graphs.append(gr)
+    for rep in range(4):
+        for st, gr in zip((a, b), graphs):
+            st.x.mul_(-1 if rep % 2 else 1.5)
+            st.run()
+            torch.cuda.synchronize()
+            want = {n: t.clone() for n, t in st.outputs().items()}
+            for t in st.outputs().values():
+                t.zero_()
+            gr.replay()
+            torch.cuda.synchronize()
+            for n, t in st.outputs().items():
+                assert torch.equal(t, want[n]), (rep, n)

@@ -45,7 +45,7 @@ def _flags(src: str) -> list:
 
 # Kernels whose loops wait for counted vector-memory instructions: a register
 # spilled to scratch memory would add instructions to the count.
-COUNTED = {"linear.hip": "mma_"}
+COUNTED = {"linear.hip": "mma_", "grouped.hip": "mma_"}
 
 
 def _check_scratch(src: str, remarks: str) -> None:

@@ -7,23 +7,11 @@
 
 #include "common.h"
 #include "grouped_common.h"
+#include "grouped_mma.h"
 #include "linear_common.h"
 
 namespace moe {
 namespace grp {
-
-using namespace lin;
-
-enum { FWD, DX, DW };
-
-// FWD: r = x rows, c = w; DX: r = dz, c = w; DW: r = dz, c = x.
-struct Prod {
-  const void *r, *c;
-  const int32_t* token;  // of the gathered operand (FWD: r, DW: c); may be null
-  Groups g;
-  int W, K;              // rows (GLU: gate and up) and columns of an expert's weights
-  Epilogue e;            // y: dx, dw
-};
 
 constexpr int TILE = 64, BK = 16, PITCH = TILE + 4;
 
@@ -159,13 +147,47 @@ void launch(const Prod& p, hipStream_t s) {
                      s, p, cols, tiles);
 }
 
+template <int MODE, int BM, int BN, int WGS, bool GLU, bool GATHER>
+int launch_mma(const Prod& p, hipStream_t s) {
+  constexpr int lds = (SA * BM + SB * BN) * SLICE * 2, NC = GLU ? BN / 2 : BN;
+  const auto fn = grouped_mma_kernel<MODE, BM, BN, WGS, GLU, GATHER>;
+  static std::atomic<bool> done[64];
+  if (!allow_lds(reinterpret_cast<const void*>(fn), lds, done)) return MOE_EHIP;
+  const int N = MODE == FWD ? (GLU ? p.W / 2 : p.W) : p.K;
+  const long rows = MODE == DW ? static_cast<long>(p.g.N) * ((p.W + BM - 1) / BM)
+                               : max_row_tiles(p.g.R, p.g.N, BM);
+  const long tiles = (rows * ((N + NC - 1) / NC) + 7) / 8 * 8;
+  if (tiles > (1 << 23)) return MOE_EUNSUP;
+  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(tiles)), dim3(lin::W * MOE_WAVE), lds, s, p);
+  return MOE_OK;
+}
+
+template <int MODE, bool GLU>
+int launch_bf16(const Prod& p, hipStream_t s) {
+  // rows of an expert: a 256-row tile is half empty for 128
+  const bool large = p.g.R / p.g.N >= 192;
+  if (MODE != DX && p.token)
+    return large ? launch_mma<MODE, 256, 256, 1, GLU, MODE != DX>(p, s)
+                 : launch_mma<MODE, 128, 128, 2, GLU, MODE != DX>(p, s);
+  return large ? launch_mma<MODE, 256, 256, 1, GLU, false>(p, s)
+               : launch_mma<MODE, 128, 128, 2, GLU, false>(p, s);
+}
+
+// Product of any type
+template <typename E, int MODE, bool GLU>
+int product(const Prod& p, hipStream_t s) {
+  if constexpr (sizeof(E) == 2) return launch_bf16<MODE, GLU>(p, s);
+  launch<E, MODE, GLU>(p, s);
+  return MOE_OK;
+}
+
 inline size_t dz_bytes(int R, int O, int act, int dtype) {
   return act == MOE_ACT_NONE ? 0 : static_cast<size_t>(R) * width(O, act) * elem_size(dtype);
 }
 
 template <typename D>
 int backward(const void* dy, const void* x, const int32_t* row_token, const Groups& g,
-             const void* w, const void* z, int K, int O, int act, void* dx, void* dw, void* ws,
+             const void* w, const void* z, int T, int K, int O, int act, void* dx, void* dw, void* ws,
              hipStream_t s) {
   typedef typename D::elem E;
   const int W = width(O, act);
@@ -183,14 +205,15 @@ int backward(const void* dy, const void* x, const int32_t* row_token, const Grou
                        static_cast<const E*>(dy), static_cast<const E*>(z), g, O, act,
                        static_cast<E*>(ws));
   }
-  Prod p{dz, w, nullptr, g, W, K, Epilogue{}};
+  Prod p{dz, w, nullptr, 0, g, W, K, Epilogue{}};
   p.e.y = dx;
-  if (dx) launch<E, DX, false>(p, s);
+  int rc = dx ? product<E, DX, false>(p, s) : MOE_OK;
   p.c = x;
   p.token = row_token;
+  p.x_rows = T;
   p.e.y = dw;
-  if (dw) launch<E, DW, false>(p, s);
-  return launch_status();
+  if (dw && rc == MOE_OK) rc = product<E, DW, false>(p, s);
+  return rc == MOE_OK ? launch_status() : rc;
 }
 
 }  // namespace grp
@@ -217,16 +240,13 @@ extern "C" int moe_grouped_linear(const void* x, const int32_t* row_token,
                         static_cast<const void*>(workspace)})
     if (!aligned16(q)) return MOE_EINVAL;
   hipStream_t s = as_stream(stream);
-  const Prod p{x, w, row_token, Groups{expert_offsets, N, R}, width(O, act), K,
+  const Prod p{x, w, row_token, static_cast<size_t>(T), Groups{expert_offsets, N, R}, width(O, act), K,
                Epilogue{nullptr, nullptr, z, y, act}};
-  if (dtype == MOE_BF16) {
-    if (act == MOE_ACT_SWIGLU) launch<uint16_t, FWD, true>(p, s);
-    else launch<uint16_t, FWD, false>(p, s);
-  } else {
-    if (act == MOE_ACT_SWIGLU) launch<float, FWD, true>(p, s);
-    else launch<float, FWD, false>(p, s);
-  }
-  return launch_status();
+  const bool glu = act == MOE_ACT_SWIGLU;
+  rc = dtype == MOE_BF16
+           ? (glu ? product<uint16_t, FWD, true>(p, s) : product<uint16_t, FWD, false>(p, s))
+           : (glu ? product<float, FWD, true>(p, s) : product<float, FWD, false>(p, s));
+  return rc == MOE_OK ? launch_status() : rc;
 }
 
 extern "C" size_t moe_grouped_linear_backward_workspace_size(int R, int N, int K, int O, int act,
@@ -253,6 +273,6 @@ extern "C" int moe_grouped_linear_backward(const void* dy, const void* x, const 
   const Groups g{expert_offsets, N, R};
   hipStream_t s = as_stream(stream);
   return dtype == MOE_BF16
-             ? backward<Bf16>(dy, x, row_token, g, w, z, K, O, act, dx, dw, workspace, s)
-             : backward<F32>(dy, x, row_token, g, w, z, K, O, act, dx, dw, workspace, s);
+             ? backward<Bf16>(dy, x, row_token, g, w, z, T, K, O, act, dx, dw, workspace, s)
+             : backward<F32>(dy, x, row_token, g, w, z, T, K, O, act, dx, dw, workspace, s);
 }

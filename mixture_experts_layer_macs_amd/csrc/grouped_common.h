@@ -51,6 +51,56 @@ __device__ __forceinline__ RowTile row_tile(const Groups& g, int height, int at)
   return {-1, 0, 0, 0, before};
 }
 
+// All experts' row tiles of `height` rows; a wave's work as above.
+__device__ __forceinline__ int row_tiles(const Groups& g, int height) {
+  int n = 0;
+  for (int e = lane_id(); e < g.N; e += MOE_WAVE) {
+    const Span s = span_of(g, e);
+    n += (s.hi - s.lo + height - 1) / height;
+  }
+  return wave_sum(n);
+}
+
+// Workgroups go round-robin over the 8 XCDs: place `block` of a list of `total`
+// tiles of which each XCD gets one contiguous range; -1: none.
+__device__ __forceinline__ int place_of(int block, int total) {
+  const int q = (total + 7) / 8, at = block % 8 * q + block / 8;
+  return block / 8 < q && at < total ? at : -1;
+}
+
+// Tile `in` of rows x cols tiles, in bands of at most 6 rows, so that tiles that
+// run side by side share the operands' slices in the XCD's L2.
+__device__ __forceinline__ void banded(int in, int rows, int cols, int& mt, int& nt) {
+  const int bands = (rows + 5) / 6, height = (rows + bands - 1) / bands;
+  const int band = in / (height * cols), at = in - band * height * cols;
+  const int h = min(height, rows - band * height);
+  mt = band * height + at % h;
+  nt = at / h;
+}
+
+// Tile of a product of data rows: expert by expert.
+__device__ __forceinline__ bool data_tile(const Groups& g, int height, int cols, int block, int& e,
+                                          int& lo, int& hi, int& mt, int& nt) {
+  const int at = place_of(block, row_tiles(g, height) * cols);
+  if (at < 0) return false;
+  const RowTile t = row_tile(g, height, at / cols);
+  e = t.e;
+  lo = t.lo;
+  hi = t.hi;
+  banded(at - t.before * cols, (hi - lo + height - 1) / height, cols, mt, nt);
+  return true;
+}
+
+// Tile of a weight gradient.
+__device__ __forceinline__ bool weight_tile(int N, int rows, int cols, int block, int& e, int& mt,
+                                            int& nt) {
+  const int at = place_of(block, N * rows * cols);
+  if (at < 0) return false;
+  e = at / (rows * cols);
+  banded(at - e * rows * cols, rows, cols, mt, nt);
+  return true;
+}
+
 // Most row tiles that R rows in N groups can make.
 inline long max_row_tiles(int R, int N, int height) {
   return static_cast<long>(R) / height + (R < N ? R : N);

@@ -109,6 +109,9 @@ struct Operand {
   static __device__ __forceinline__ int swizzle(int k) {
     return EXT % 128 == 0 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
   }
+  // what a slice's loads need to know beforehand: nothing here
+  __device__ __forceinline__ void fetch(int, int) {}
+  __device__ __forceinline__ void prepare(int, int) {}
   // load q of the slice from k0 (k up to kend) into the stage at lds
   __device__ __forceinline__ void load(int q, int k0, int kend, uint32_t lds, int wave) const {
     if constexpr (!STRIDED) {
@@ -187,15 +190,16 @@ struct Staging {
   static_assert(WM * XC * 32 * PITCH * 4 <= RING, "fits the ring");
 };
 
-// Workgroup `block` of a product; smem: the ring.
-template <bool RS, bool CS, int BM, int BN, bool GLU, bool PART>
-__device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char* smem) {
-  static_assert(!GLU || (!CS && !PART), "pairs of gate and up rows: y = x w^T only");
+// One tile: the sum over k_lo <= k < k_hi (not empty) of the operands' slices,
+// whose chunks of V output columns go to out(row, column, sums, up sums), places
+// within the tile, also those past the matrix's end.  Row and Col: Operand, or
+// another with its functions; smem: the ring.
+template <bool RS, bool CS, int BM, int BN, bool GLU, int V, class Row, class Col, class Out>
+__device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
+                                         unsigned char* smem, Out out_chunk) {
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
   static_assert(TM % 32 == 0 && TN % 32 == 0, "whole fragments");
   static_assert(SA == 2 && SB == 3, "the order of requests, below");
-  typedef Operand<RS, false, BM, W> Row;
-  typedef Operand<CS, GLU, BN, W> Col;
   typedef Reader<RS, BM> RowR;
   typedef Reader<CS, BN> ColR;
   constexpr int B_BASE = SA * Row::BYTES;
@@ -203,21 +207,11 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
   static_assert(KK % 2 == 0, "fragment sets alternate");
   constexpr int NMF = FM * FN;
 
-  int mt, nt, split;
-  if (!tile_of(a, block, mt, nt, split)) return;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
   const int wm = wave / WN, wn = wave % WN;
   constexpr int NC = GLU ? BN / 2 : BN;  // output columns of the tile
-  const int m0 = mt * BM, n0 = nt * NC;
-  const int k_lo = split * a.per_split, k_hi = min(a.K, k_lo + a.per_split);
   const int nk = (k_hi - k_lo + SLICE - 1) / SLICE;
-
-  Row row;
-  Col col;
-  row.init(a.r + (RS ? m0 : m0 * a.ldr), a.ldr, min(BM, a.M - m0), wave, lane);
-  col.init(a.c + (CS ? n0 : n0 * a.ldc), a.ldc, min(NC, a.N - n0), wave, lane,
-           GLU ? a.N * a.ldc : 0);
   const uint32_t lds_base = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(smem))));
   lds_cbyte* lds0 = (lds_cbyte*)(smem);
@@ -231,6 +225,8 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
     col.load(q, k_lo + min(t, nk - 1) * SLICE, k_hi, lds_base + B_BASE + (t % SB) * Col::BYTES,
              wave);
   };
+  auto fetch_col = [&](int t) { col.fetch(k_lo + min(t, nk - 1) * SLICE, wave); };
+  auto prepare_col = [&](int t) { col.prepare(k_lo + min(t, nk - 1) * SLICE, k_hi); };
   auto load_rows = [&](int t) {
 #pragma unroll
     for (int q = 0; q < Row::Q; ++q) load_row(t, q);
@@ -289,11 +285,16 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
   // latency shows at the slice boundary.  Row slice t + 1 and column slice t + 1 come before row
   // slices t + 2 .. t + SA - 1 and column slices t + 2 .. t + SB - 1 in the
   // order of requests; only those may still be outstanding at the wait.
+  fetch_col(0);
 #pragma unroll
   for (int t = 0; t < SB - 1; ++t) {
+    prepare_col(t);
+    fetch_col(t + 1);
     if (t < SA - 1) load_rows(t);
     load_cols(t);
   }
+  prepare_col(SB - 1);
+  fetch_col(SB);
   load_rows(SA - 1);
   wait_vmcnt<(SA - 1) * Row::Q + (SB - 2) * Col::Q>();
   wg_barrier();
@@ -307,6 +308,8 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
            [&](int q) { load_col(t + SB - 1, kk * CQ + q); });
     wait_vmcnt<(SA - 2) * Row::Q + (SB - 2) * Col::Q>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    prepare_col(t + SB);
+    fetch_col(t + SB + 1);
     step(KK - 1, t + 1, Row::Q, [&](int q) { load_row(t + SA, q); });
   }
   wait_vmcnt<0>();  // no load may land after the workgroup ends
@@ -317,7 +320,7 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
   // 12 to 22 us of a 52 to 64 us product, for 4 to 8 us of traffic.)
   typedef Staging<BM, BN, SA * Row::BYTES + SB * Col::BYTES> St;
   constexpr int XC = St::XC, ROWS = WM * XC * 32, PITCH = St::PITCH;  // PITCH in floats
-  constexpr int V = PART ? 4 : 8, CC = NC / V;
+  constexpr int CC = NC / V;
   constexpr int ITER = ROWS * CC / (W * MOE_WAVE);
   static_assert(ROWS * CC % (W * MOE_WAVE) == 0, "whole rounds");
   constexpr int U = ITER % 4 == 0 ? 4 : ITER % 3 == 0 ? 3 : ITER % 2 == 0 ? 2 : 1;
@@ -365,16 +368,38 @@ __device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char*
       }
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int i = i0 + k * W * MOE_WAVE, r = i / CC, n = n0 + i % CC * V;
-        const int m = m0 + r / (XC * 32) * TM + xc * 32 + r % (XC * 32);
-        if (m >= a.M || n >= a.N) continue;
-        if constexpr (PART)
-          store4(a.part + (static_cast<size_t>(split) * a.M + m) * a.N + n, g[k]);
-        else
-          finish<uint16_t, GLU, V>(a.e, m, n, a.N, g[k], u[k]);
+        const int i = i0 + k * W * MOE_WAVE, r = i / CC;
+        out_chunk(r / (XC * 32) * TM + xc * 32 + r % (XC * 32), i % CC * V, g[k], u[k]);
       }
     }
   }
+}
+
+// Workgroup `block` of a product; smem: the ring.
+template <bool RS, bool CS, int BM, int BN, bool GLU, bool PART>
+__device__ __forceinline__ void mma_tile(const Mma& a, int block, unsigned char* smem) {
+  static_assert(!GLU || (!CS && !PART), "pairs of gate and up rows: y = x w^T only");
+  int mt, nt, split;
+  if (!tile_of(a, block, mt, nt, split)) return;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
+  constexpr int NC = GLU ? BN / 2 : BN;  // output columns of the tile
+  const int m0 = mt * BM, n0 = nt * NC;
+  const int k_lo = split * a.per_split, k_hi = min(a.K, k_lo + a.per_split);
+  Operand<RS, false, BM, W> row;
+  Operand<CS, GLU, BN, W> col;
+  row.init(a.r + (RS ? m0 : m0 * a.ldr), a.ldr, min(BM, a.M - m0), wave, lane);
+  col.init(a.c + (CS ? n0 : n0 * a.ldc), a.ldc, min(NC, a.N - n0), wave, lane,
+           GLU ? a.N * a.ldc : 0);
+  mma_core<RS, CS, BM, BN, GLU, PART ? 4 : 8>(
+      row, col, k_lo, k_hi, smem, [&](int r, int c, float* g, float* u) {
+        const int m = m0 + r, n = n0 + c;
+        if (m >= a.M || n >= a.N) return;
+        if constexpr (PART)
+          store4(a.part + (static_cast<size_t>(split) * a.M + m) * a.N + n, g);
+        else
+          finish<uint16_t, GLU, 8>(a.e, m, n, a.N, g, u);
+      });
 }
 
 template <bool RS, bool CS, int BM, int BN, int WGS, bool GLU, bool PART>

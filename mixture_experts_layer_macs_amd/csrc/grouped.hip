@@ -156,9 +156,12 @@ int launch_mma(const Prod& p, hipStream_t s) {
   const int N = MODE == FWD ? (GLU ? p.W / 2 : p.W) : p.K;
   const long rows = MODE == DW ? static_cast<long>(p.g.N) * ((p.W + BM - 1) / BM)
                                : max_row_tiles(p.g.R, p.g.N, BM);
-  const long tiles = (rows * ((N + NC - 1) / NC) + 7) / 8 * 8;
-  if (tiles > (1 << 23)) return MOE_EUNSUP;
-  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(tiles)), dim3(lin::W * MOE_WAVE), lds, s, p);
+  const long tiles = rows * ((N + NC - 1) / NC);
+  if (tiles > (1 << 23)) return MOE_EUNSUP;  // the outputs alone would not fit the card
+  // DW: workgroups that stay; a short list may fall unevenly on the XCDs
+  const long wgs = MODE == DW ? std::min<long>(WGS * cu_count(), 2 * tiles) : tiles;
+  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>((wgs + 7) / 8 * 8)), dim3(lin::W * MOE_WAVE), lds,
+                     s, p);
   return MOE_OK;
 }
 

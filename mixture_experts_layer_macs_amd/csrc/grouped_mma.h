@@ -8,6 +8,8 @@
 //                                reduction-strided, x gathered along it
 #pragma once
 
+#include <type_traits>
+
 #include "grouped_common.h"
 #include "linear_mma.h"
 
@@ -17,6 +19,8 @@ namespace grp {
 using namespace lin;
 
 enum { FWD, DX, DW };
+
+constexpr int UNIT = 64;  // rows
 
 struct Prod {
   const void *r, *c;     // FWD: x, w; DX: dz, w; DW: dz, x
@@ -48,128 +52,149 @@ struct GatherRows : Operand<false, false, EXT, lin::W> {
 };
 
 // The reduction-strided operand whose k are the rows of a token list.  A wave's
-// loads of a slice are 16 consecutive k, whose tokens it holds in scalar
-// registers: fetch requests them a slice ahead, prepare, behind a wait that the
-// loop makes anyway, turns them into the lanes' offsets.
+// loads of a slice are 16 consecutive k.  The list lies in vector registers, 64
+// tokens each, CHUNKS slices at a time; a load reads its rows' tokens from the
+// lanes that hold them, between the MFMAs.  (Tokens loaded by the scalar unit a
+// slice ahead cost 6 to 13 % of the product: a wait for the LDS fragments is
+// then a wait for them too.)
 template <int EXT>
 struct GatherStrided {
   typedef Operand<true, false, EXT, lin::W> Base;
   static constexpr int BYTES = Base::BYTES, Q = Base::Q, CPR = EXT / 8, PER = 64 / CPR;
+  static constexpr int CHUNKS = 16;
   static_assert(64 % CPR == 0 && PER * Q == 16 && lin::W * 16 == SLICE, "16 rows per wave and slice");
-  typedef __attribute__((address_space(4))) const int32_t scalar_i32;
   i32x4 rsrc;
-  uint32_t voff[Q], step, ch;
+  uint32_t step, first;  // bytes of a row of x, of the tile's first column
+  uint32_t voff[4];      // the lane's chunk in loads q, q + 4, ..: the swizzle repeats every 4 rows
   const int32_t* token;
-  int left, sub;  // entries of the token list, the lane's row of a load's PER
-  bool live;
-  int32_t t[16];
-  int at;         // k of t[0]
+  int last, lane;        // last entry of the list
+  typedef uint32_t u32x16 __attribute__((ext_vector_type(CHUNKS)));
+  u32x16 list;
+  uint32_t now;          // the slice's
+  int run;               // which CHUNKS slices the list is of
 
   __device__ __forceinline__ void init(const uint16_t* x, int n0, size_t ld, size_t x_rows,
-                                       const int32_t* tok, int tokens, int valid, int wave, int lane) {
+                                       const int32_t* tok, int tokens, int valid, int lane_) {
+    lane = lane_;
     step = static_cast<uint32_t>(ld) * 2;
+    first = static_cast<uint32_t>(n0) * 2;
     rsrc = buffer_rsrc(x, static_cast<uint32_t>(x_rows * step));
     token = tok;
-    left = tokens;
-    sub = lane / CPR;
-    // row of a load: PER (16 wave + ..) + sub; PER is a multiple of 2, so the swizzle depends on q and sub
-    ch = static_cast<uint32_t>(lane % CPR);
-    n_bytes = static_cast<uint32_t>(n0) * 2;
-    valid_ch = valid / 8;
-  }
-  uint32_t n_bytes;
-  int valid_ch;
-  __device__ __forceinline__ void fetch(int k0, int wave) {
-    at = k0 + wave * 16;
-    scalar_i32* p = (scalar_i32*)(token);
-    if (at + 16 <= left) {
+    last = tokens - 1;
+    run = -1;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = p[at + i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = p[min(at + i, left - 1)];
+    for (int q = 0; q < 4; ++q) {
+      const int ch = lane % CPR ^ Base::swizzle(q * PER + lane / CPR);
+      voff[q] = ch * 8 < valid ? first + ch * 16 : OOB_OFF;
     }
   }
-  __device__ __forceinline__ void prepare(int, int kend) {
-    uint32_t off[16];
+  __device__ __forceinline__ void fetch(int k0) {
+    const int at = k0 / SLICE;
+    if (at / CHUNKS != run) {
+      run = at / CHUNKS;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      off[i] = at + i < kend ? static_cast<uint32_t>(t[i]) * step + n_bytes : OOB_OFF;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      uint32_t v = off[q * PER];
-#pragma unroll
-      for (int s = 1; s < PER; ++s) v = sub == s ? off[q * PER + s] : v;
-      const uint32_t c = ch ^ static_cast<uint32_t>(Base::swizzle(q * PER + sub));
-      voff[q] = static_cast<int>(c) < valid_ch ? v + c * 16 : OOB_OFF;
+      for (int i = 0; i < CHUNKS; ++i)
+        list[i] = static_cast<uint32_t>(token[min((run * CHUNKS + i) * SLICE + lane, last)]);
     }
+    now = list[at % CHUNKS];
   }
-  __device__ __forceinline__ void load(int q, int, int, uint32_t lds, int wave) const {
-    lds_dma16(rsrc, voff[q], 0, lds + (wave * Q + q) * 1024);
+  __device__ __forceinline__ void load(int q, int k0, int kend, uint32_t lds, int wave) const {
+    uint32_t row = OOB_OFF;
+#pragma unroll
+    for (int s = 0; s < PER; ++s) {
+      const int k = wave * 16 + q * PER + s;
+      const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(now), k));
+      const uint32_t off = k0 + k < kend ? t * step : OOB_OFF;
+      row = s == 0 || lane / CPR == s ? off : row;
+    }
+    const uint32_t v = voff[q % 4];
+    // either may be OOB_OFF; both would add up to a valid offset
+    lds_dma16(rsrc, row == OOB_OFF ? OOB_OFF : row + v, 0, lds + (wave * Q + q) * 1024);
   }
 };
 
+// FWD, DX: one tile of at most BM rows.  An expert's rows are cut into units of
+// 64 and these shared out evenly over its tiles, so that half a unit per expert
+// is multiplied in vain, not half a tile.
 template <int MODE, int BM, int BN, bool GLU, bool GATHER>
-__device__ __forceinline__ void grouped_tile(const Prod& p, int block, unsigned char* smem) {
-  const uint16_t *R = static_cast<const uint16_t*>(p.r), *C = static_cast<const uint16_t*>(p.c);
-  const int lane = lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
+__device__ __forceinline__ void data_product(const Prod& p, int block, unsigned char* smem) {
   constexpr int NC = GLU ? BN / 2 : BN;
-  const int O = GLU ? p.W / 2 : p.W, N = MODE == FWD ? O : p.K;
+  constexpr bool STRIDED = MODE == DX;
+  const int O = GLU ? p.W / 2 : p.W, N = MODE == FWD ? O : p.K, len = MODE == FWD ? p.K : p.W;
   const int cols = (N + NC - 1) / NC;
   int e, lo, hi, mt, nt;
-  if constexpr (MODE == DW) {
-    const int rows = (p.W + BM - 1) / BM;
-    if (!weight_tile(p.g.N, rows, cols, block, e, mt, nt)) return;
+  if (!data_tile(p.g, BM, cols, block, e, lo, hi, mt, nt)) return;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
+  const int tiles = (hi - lo + BM - 1) / BM, units = (hi - lo + UNIT - 1) / UNIT;
+  const int height = units / tiles + (mt < units % tiles);
+  const int m0 = lo + (units / tiles * mt + min(mt, units % tiles)) * UNIT, n0 = nt * NC;
+  const int rows = min(height * UNIT, hi - m0);
+  const uint16_t* w = static_cast<const uint16_t*>(p.c) + static_cast<size_t>(e) * p.W * p.K;
+  Operand<STRIDED, GLU, BN, lin::W> col;
+  col.init(w + (STRIDED ? n0 : n0 * static_cast<size_t>(p.K)), p.K, min(NC, N - n0), wave, lane,
+           GLU ? O * static_cast<size_t>(p.K) : 0);
+  auto run = [&](auto h) {
+    constexpr int H = decltype(h)::value * UNIT;
+    if constexpr (H <= BM) {
+      GatherRows<H> row;
+      const uint16_t* r = static_cast<const uint16_t*>(p.r);
+      if constexpr (GATHER)
+        row.init_gather(r, len, p.x_rows, p.token + m0, rows, wave, lane);
+      else
+        row.init(r + static_cast<size_t>(m0) * len, len, rows, wave, lane);
+      mma_core<false, STRIDED, H, BN, GLU, 8>(
+          row, col, 0, len, smem, [&](int r, int c, float* g, float* u) {
+            if (r < rows && n0 + c < N) finish<uint16_t, GLU, 8>(p.e, m0 + r, n0 + c, N, g, u);
+          });
+    }
+  };
+  if (height == 1) run(std::integral_constant<int, 1>());
+  else if (height == 2) run(std::integral_constant<int, 2>());
+  else if (height == 3) run(std::integral_constant<int, 3>());
+  else run(std::integral_constant<int, 4>());
+}
+
+// DW: the tiles of this workgroup, every (workgroups of the XCD)-th of its range.
+template <int BM, int BN, bool GATHER>
+__device__ __forceinline__ void weight_product(const Prod& p, unsigned char* smem) {
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
+  const int tm = (p.W + BM - 1) / BM, tn = (p.K + BN - 1) / BN;
+  const Range range = weight_tiles(p.g, tm * tn, blockIdx.x % 8);
+  for (int at = range.first + blockIdx.x / 8; at < range.end; at += gridDim.x / 8) {
+    const int e = at / (tm * tn);
+    int mt, nt;
+    banded(at - e * tm * tn, tm, tn, mt, nt);
     const Span s = span_of(p.g, e);
-    lo = s.lo;
-    hi = s.hi;
-  } else {
-    if (!data_tile(p.g, BM, cols, block, e, lo, hi, mt, nt)) return;
-  }
-  const int n0 = nt * NC, m0 = mt * BM;
-  if constexpr (MODE == DW) {
+    const int n0 = nt * BN, m0 = mt * BM, lo = s.lo, count = s.hi - s.lo;
+    const int rows = min(BM, p.W - m0), width = min(BN, p.K - n0);
     uint16_t* out = static_cast<uint16_t*>(p.e.y) + static_cast<size_t>(e) * p.W * p.K;
-    const int rows = min(BM, p.W - m0), width = min(BN, N - n0);
-    if (lo == hi) {  // no rows: zeros
+    if (count == 0) {  // no rows: zeros
       for (int i = threadIdx.x; i < rows * (BN / 8); i += lin::W * MOE_WAVE) {
         const int r = i / (BN / 8), c = i % (BN / 8) * 8;
         if (c < width)
           *reinterpret_cast<u32x4*>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c) = u32x4{0, 0, 0, 0};
       }
-      return;
+      continue;
     }
     Operand<true, false, BM, lin::W> row;
-    row.init(R + static_cast<size_t>(lo) * p.W + m0, p.W, rows, wave, lane);
+    row.init(static_cast<const uint16_t*>(p.r) + static_cast<size_t>(lo) * p.W + m0, p.W, rows, wave,
+             lane);
     auto chunk = [&](int r, int c, float* g, float*) {
       if (r < rows && c < width) store_v<8>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c, g);
     };
+    const uint16_t* x = static_cast<const uint16_t*>(p.c);
     if constexpr (GATHER) {
       GatherStrided<BN> col;
-      col.init(C, n0, p.K, p.x_rows, p.token + lo, p.g.R - lo, width, wave, lane);
-      mma_core<true, true, BM, BN, false, 8>(row, col, 0, hi - lo, smem, chunk);
+      col.init(x, n0, p.K, p.x_rows, p.token + lo, p.g.R - lo, width, lane);
+      mma_core<true, true, BM, BN, false, 8>(row, col, 0, count, smem, chunk);
     } else {
       Operand<true, false, BN, lin::W> col;
-      col.init(C + static_cast<size_t>(lo) * p.K + n0, p.K, width, wave, lane);
-      mma_core<true, true, BM, BN, false, 8>(row, col, 0, hi - lo, smem, chunk);
+      col.init(x + static_cast<size_t>(lo) * p.K + n0, p.K, width, wave, lane);
+      mma_core<true, true, BM, BN, false, 8>(row, col, 0, count, smem, chunk);
     }
-  } else {
-    const int m1 = lo + m0, rows = min(BM, hi - m1);
-    const int len = MODE == FWD ? p.K : p.W;
-    GatherRows<BM> row;
-    if constexpr (GATHER)
-      row.init_gather(R, len, p.x_rows, p.token + m1, rows, wave, lane);
-    else
-      row.init(R + static_cast<size_t>(m1) * len, len, rows, wave, lane);
-    const uint16_t* w = C + static_cast<size_t>(e) * p.W * p.K;
-    constexpr bool STRIDED = MODE == DX;
-    Operand<STRIDED, GLU, BN, lin::W> col;
-    col.init(w + (STRIDED ? n0 : n0 * static_cast<size_t>(p.K)), p.K, min(NC, N - n0), wave, lane,
-             GLU ? O * static_cast<size_t>(p.K) : 0);
-    mma_core<false, STRIDED, BM, BN, GLU, 8>(
-        row, col, 0, len, smem, [&](int r, int c, float* g, float* u) {
-          if (r < rows && n0 + c < N) finish<uint16_t, GLU, 8>(p.e, m1 + r, n0 + c, N, g, u);
-        });
+    __syncthreads();  // the next tile's ring takes the place of this one's output
   }
 }
 
@@ -177,7 +202,8 @@ template <int MODE, int BM, int BN, int WGS, bool GLU, bool GATHER>
 __global__ __launch_bounds__(lin::W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(WGS, WGS)))
 void grouped_mma_kernel(Prod p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  grouped_tile<MODE, BM, BN, GLU, GATHER>(p, blockIdx.x, smem);
+  if constexpr (MODE == DW) weight_product<BM, BN, GATHER>(p, smem);
+  else data_product<MODE, BM, BN, GLU, GATHER>(p, blockIdx.x, smem);
 }
 
 }  // namespace grp

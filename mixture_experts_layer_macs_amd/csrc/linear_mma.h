@@ -109,9 +109,8 @@ struct Operand {
   static __device__ __forceinline__ int swizzle(int k) {
     return EXT % 128 == 0 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
   }
-  // what a slice's loads need to know beforehand: nothing here
-  __device__ __forceinline__ void fetch(int, int) {}
-  __device__ __forceinline__ void prepare(int, int) {}
+  // what the loads of the slice from k0 need to know beforehand: nothing here
+  __device__ __forceinline__ void fetch(int) {}
   // load q of the slice from k0 (k up to kend) into the stage at lds
   __device__ __forceinline__ void load(int q, int k0, int kend, uint32_t lds, int wave) const {
     if constexpr (!STRIDED) {
@@ -186,7 +185,8 @@ __device__ __forceinline__ bool tile_of(const Mma& a, int p, int& mt, int& nt, i
 // 16 bytes, within the ring's LDS.
 template <int BM, int BN, int RING>
 struct Staging {
-  static constexpr int FM = BM / WM / 32, XC = FM % 2 == 0 ? 2 : 1, PITCH = BN + 4;
+  static constexpr int FM = BM / WM / 32, PITCH = BN + 4;
+  static constexpr int XC = FM % 2 == 0 && WM * 2 * 32 * PITCH * 4 <= RING ? 2 : 1;
   static_assert(WM * XC * 32 * PITCH * 4 <= RING, "fits the ring");
 };
 
@@ -225,8 +225,7 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
     col.load(q, k_lo + min(t, nk - 1) * SLICE, k_hi, lds_base + B_BASE + (t % SB) * Col::BYTES,
              wave);
   };
-  auto fetch_col = [&](int t) { col.fetch(k_lo + min(t, nk - 1) * SLICE, wave); };
-  auto prepare_col = [&](int t) { col.prepare(k_lo + min(t, nk - 1) * SLICE, k_hi); };
+  auto fetch_col = [&](int t) { col.fetch(k_lo + min(t, nk - 1) * SLICE); };
   auto load_rows = [&](int t) {
 #pragma unroll
     for (int q = 0; q < Row::Q; ++q) load_row(t, q);
@@ -285,16 +284,13 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
   // latency shows at the slice boundary.  Row slice t + 1 and column slice t + 1 come before row
   // slices t + 2 .. t + SA - 1 and column slices t + 2 .. t + SB - 1 in the
   // order of requests; only those may still be outstanding at the wait.
-  fetch_col(0);
 #pragma unroll
   for (int t = 0; t < SB - 1; ++t) {
-    prepare_col(t);
-    fetch_col(t + 1);
+    fetch_col(t);
     if (t < SA - 1) load_rows(t);
     load_cols(t);
   }
-  prepare_col(SB - 1);
-  fetch_col(SB);
+  fetch_col(SB - 1);
   load_rows(SA - 1);
   wait_vmcnt<(SA - 1) * Row::Q + (SB - 2) * Col::Q>();
   wg_barrier();
@@ -308,8 +304,7 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
            [&](int q) { load_col(t + SB - 1, kk * CQ + q); });
     wait_vmcnt<(SA - 2) * Row::Q + (SB - 2) * Col::Q>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    prepare_col(t + SB);
-    fetch_col(t + SB + 1);
+    fetch_col(t + SB);
     step(KK - 1, t + 1, Row::Q, [&](int q) { load_row(t + SA, q); });
   }
   wait_vmcnt<0>();  // no load may land after the workgroup ends

@@ -3,7 +3,7 @@
 //
 //   norm = sqrt(sum g^2);   out = g min(1, max_norm / norm)
 //
-// Tensors are cut into blocks of 64 KB, counted from their address rounded down
+// Tensors are cut into blocks of 16 KB, counted from their address rounded down
 // to 16 bytes, and a workgroup takes a contiguous run of blocks, whatever
 // tensors they belong to: one launch for the squares and one for the scaling,
 // for any number and mixture of tensors.  Bound by HBM (gradients read twice,
@@ -19,7 +19,7 @@ namespace moe {
 namespace clip {
 
 constexpr int NTHR = 256;
-constexpr int BLOCK = 65536;          // bytes of a block
+constexpr int BLOCK = 16384;  // bytes of a block
 constexpr int WORDS = MOE_GRAD_TABLE_WORDS;
 // row of the table: address, output address, first block << 1 | bf16, elements;
 // behind the last tensor a row whose first block is their number
@@ -74,25 +74,24 @@ __device__ __forceinline__ float element(uint64_t p, bool bf16) {
 
 constexpr int PIECES = BLOCK / 16 / NTHR;  // 16-byte pieces of a thread in a block
 
-__device__ __forceinline__ double squares_of(u32x4 v, bool bf16) {
-  double s = 0.0;
+// s: two running sums
+__device__ __forceinline__ void add_squares(u32x4 v, bool bf16, double* s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (bf16) {
-      s += square(__uint_as_float(v[i] << 16));
-      s += square(__uint_as_float(v[i] & 0xffff0000u));
+      s[0] += square(__uint_as_float(v[i] << 16));
+      s[1] += square(__uint_as_float(v[i] & 0xffff0000u));
     } else {
-      s += square(__uint_as_float(v[i]));
+      s[i % 2] += square(__uint_as_float(v[i]));
     }
   }
-  return s;
 }
 
 __global__ __launch_bounds__(NTHR) void squares_kernel(const int64_t* __restrict__ table, int n,
                                                        int64_t blocks, double* __restrict__ part) {
   __shared__ double red[NTHR / MOE_WAVE];
   const Run run = run_of(blocks);
-  double sum = 0.0;
+  double s[2] = {};
   int i = run.lo < run.hi ? find(table, n, run.lo) : 0;
   for (int64_t b = run.lo; b < run.hi; ++b) {
     while (first_of(table, i + 1) <= b) ++i;
@@ -100,16 +99,26 @@ __global__ __launch_bounds__(NTHR) void squares_kernel(const int64_t* __restrict
     const int size = t.bf16 ? 2 : 4;
     const uint64_t end = t.in + static_cast<uint64_t>(t.elements) * size;
     const uint64_t base = (t.in & ~uint64_t(15)) + static_cast<uint64_t>(b - t.first) * BLOCK;
+    const uint64_t mine = base + threadIdx.x * 16;
+    if (base >= t.in && base + BLOCK <= end) {  // all loads of a whole block at once
+      u32x4 v[PIECES];
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) v[j] = *reinterpret_cast<const u32x4*>(mine + j * NTHR * 16);
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) add_squares(v[j], t.bf16, s);
+      continue;
+    }
     for (int j = 0; j < PIECES; ++j) {
-      const uint64_t p = base + static_cast<uint64_t>(j * NTHR + threadIdx.x) * 16;
+      const uint64_t p = mine + j * NTHR * 16;
       if (p >= t.in && p + 16 <= end) {
-        sum += squares_of(*reinterpret_cast<const u32x4*>(p), t.bf16);
+        add_squares(*reinterpret_cast<const u32x4*>(p), t.bf16, s);
       } else {
         for (uint64_t q = p; q < p + 16; q += size)
-          if (q >= t.in && q < end) sum += square(element(q, t.bf16));
+          if (q >= t.in && q < end) s[0] += square(element(q, t.bf16));
       }
     }
   }
+  double sum = s[0] + s[1];
   sum = wave_sum_f64(sum);
   if (lane_id() == 0) red[threadIdx.x / MOE_WAVE] = sum;
   __syncthreads();
@@ -157,26 +166,38 @@ __global__ __launch_bounds__(NTHR) void scale_kernel(const int64_t* __restrict__
   const bool keep = !(v > max_norm && v < INFINITY);
   Factor c{1.f, 0};
   if (!keep) c.m = static_cast<float>(frexp(max_norm / v, &c.e));
+  // Last block first: what the squares read last is still in the last-level cache.
   const Run run = run_of(blocks);
-  int i = run.lo < run.hi ? find(table, n, run.lo) : 0;
-  for (int64_t b = run.lo; b < run.hi; ++b) {
-    while (first_of(table, i + 1) <= b) ++i;
+  int i = run.lo < run.hi ? find(table, n, run.hi - 1) : 0;
+  for (int64_t b = run.hi - 1; b >= run.lo; --b) {
+    while (first_of(table, i) > b) --i;
     const Tensor t = read(table, i);
     if (keep && t.in == t.out) continue;
     const int size = t.bf16 ? 2 : 4;
     const uint64_t end = t.in + static_cast<uint64_t>(t.elements) * size;
     const uint64_t base = (t.in & ~uint64_t(15)) + static_cast<uint64_t>(b - t.first) * BLOCK;
-    const uint64_t move = t.out - t.in;
-    for (int j = 0; j < PIECES; ++j) {
-      const uint64_t p = base + static_cast<uint64_t>(j * NTHR + threadIdx.x) * 16;
-      if (p >= t.in && p + 16 <= end) {
-        u32x4 w = *reinterpret_cast<const u32x4*>(p);
+    const uint64_t mine = base + threadIdx.x * 16, move = t.out - t.in;
+    auto scaled = [&](u32x4 w) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[k] = t.bf16 ? lin::pack2(c(__uint_as_float(w[k] << 16)),
-                                     c(__uint_as_float(w[k] & 0xffff0000u)))
-                        : __float_as_uint(c(__uint_as_float(w[k])));
-        *reinterpret_cast<u32x4*>(p + move) = w;
+      for (int k = 0; k < 4; ++k)
+        w[k] = t.bf16 ? lin::pack2(c(__uint_as_float(w[k] << 16)),
+                                   c(__uint_as_float(w[k] & 0xffff0000u)))
+                      : __float_as_uint(c(__uint_as_float(w[k])));
+      return w;
+    };
+    if (base >= t.in && base + BLOCK <= end) {
+      u32x4 v[PIECES];
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j) v[j] = *reinterpret_cast<const u32x4*>(mine + j * NTHR * 16);
+#pragma unroll
+      for (int j = 0; j < PIECES; ++j)
+        *reinterpret_cast<u32x4*>(mine + move + j * NTHR * 16) = scaled(v[j]);
+      continue;
+    }
+    for (int j = 0; j < PIECES; ++j) {
+      const uint64_t p = mine + j * NTHR * 16;
+      if (p >= t.in && p + 16 <= end) {
+        *reinterpret_cast<u32x4*>(p + move) = scaled(*reinterpret_cast<const u32x4*>(p));
       } else {
         for (uint64_t q = p; q < p + 16; q += size)
           if (q >= t.in && q < end) {

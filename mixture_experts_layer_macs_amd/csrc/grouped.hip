@@ -7,92 +7,13 @@
 
 #include "common.h"
 #include "grouped_common.h"
+#include "grouped_f32.h"
 #include "grouped_mma.h"
+#include "grouped_plan.h"
 #include "linear_common.h"
 
 namespace moe {
 namespace grp {
-
-constexpr int TILE = 64, BK = 16, PITCH = TILE + 4;
-
-// 64 x 64 outputs per workgroup, 4 x 4 per thread, operands through LDS as
-// fp32, the reduction's elements outside the matrix as zeros.
-template <typename E, int MODE, bool GLU>
-__global__ __launch_bounds__(256) void simple_kernel(Prod p, int col_tiles, long tiles) {
-  __shared__ float sr[BK][PITCH], sc[GLU ? 2 : 1][BK][PITCH];
-  const E *R = static_cast<const E*>(p.r), *C = static_cast<const E*>(p.c);
-  const int O = GLU ? p.W / 2 : p.W;
-  const int M_dw = (p.W + TILE - 1) / TILE;
-  for (long at = blockIdx.x; at < tiles; at += gridDim.x) {
-    int e, lo, hi, m0;
-    const int n0 = static_cast<int>(at % col_tiles) * TILE;
-    if (MODE == DW) {
-      const int rest = static_cast<int>(at / col_tiles);
-      e = rest / M_dw;
-      m0 = rest % M_dw * TILE;
-      const Span s = span_of(p.g, e);
-      lo = s.lo;
-      hi = s.hi;
-    } else {
-      const RowTile t = row_tile(p.g, TILE, static_cast<int>(at / col_tiles));
-      if (t.e < 0) return;
-      e = t.e;
-      lo = t.lo + t.tile * TILE;
-      hi = min(t.hi, lo + TILE);
-      m0 = 0;
-    }
-    const int N = MODE == FWD ? O : p.K;                        // output columns
-    const int len = MODE == DW ? hi - lo : MODE == FWD ? p.K : p.W;  // reduction
-    const E* we = C + static_cast<size_t>(e) * p.W * p.K;
-    float acc[GLU ? 2 : 1][4][4] = {};
-    const int tm = threadIdx.x / 16 * 4, tn = threadIdx.x % 16 * 4;
-    for (int k0 = 0; k0 < len; k0 += BK) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < TILE * BK; i += 256) {
-        // along memory: k for reduction-contiguous operands, m or n otherwise
-        const int kc = i % BK, mc = i / BK, ks = i / TILE, ms = i % TILE;
-        if (MODE == DW) {
-          const int r = lo + k0 + ks;
-          const bool in = k0 + ks < len;
-          sr[ks][ms] = in && m0 + ms < p.W ? load1(R + static_cast<size_t>(r) * p.W + m0 + ms) : 0.f;
-          const int xr = in && p.token ? p.token[r] : r;
-          sc[0][ks][ms] = in && n0 + ms < N ? load1(C + static_cast<size_t>(xr) * p.K + n0 + ms) : 0.f;
-        } else {
-          const int r = lo + mc;
-          const bool in = r < hi && k0 + kc < len;
-          const int xr = in && MODE == FWD && p.token ? p.token[r] : r;
-          sr[kc][mc] = in ? load1(R + static_cast<size_t>(xr) * len + k0 + kc) : 0.f;
-          if (MODE == FWD) {
-            const bool on = n0 + mc < N && k0 + kc < len;
-            const size_t w = static_cast<size_t>(n0 + mc) * p.K + k0 + kc;
-            sc[0][kc][mc] = on ? load1(we + w) : 0.f;
-            if constexpr (GLU) sc[1][kc][mc] = on ? load1(we + w + static_cast<size_t>(O) * p.K) : 0.f;
-          } else {
-            sc[0][ks][ms] = n0 + ms < N && k0 + ks < len
-                                ? load1(we + static_cast<size_t>(k0 + ks) * p.K + n0 + ms) : 0.f;
-          }
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < BK; ++k)
-#pragma unroll
-        for (int h = 0; h < (GLU ? 2 : 1); ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[h][i][j] += sr[k][tm + i] * sc[h][k][tn + j];
-    }
-    if (n0 + tn >= N) continue;
-    Epilogue out = p.e;
-    if (MODE == DW) out.y = static_cast<E*>(p.e.y) + static_cast<size_t>(e) * p.W * p.K;
-    for (int i = 0; i < 4; ++i) {
-      const int m = MODE == DW ? m0 + tm + i : lo + tm + i;
-      if (m >= (MODE == DW ? p.W : hi)) continue;
-      finish<E, GLU, 4>(out, m, n0 + tn, N, acc[0][i], acc[GLU ? 1 : 0][i]);
-    }
-  }
-}
 
 // dz of the rows that the experts have, rounded to the element type: 16 bytes of
 // dy's columns per thread.
@@ -138,19 +59,10 @@ inline int check_tokens(const int32_t* row_token, int T, int R, int K, int dtype
   return static_cast<size_t>(T) * K * elem_size(dtype) > (size_t(1) << 31) ? MOE_EUNSUP : MOE_OK;
 }
 
-template <typename E, int MODE, bool GLU>
-void launch(const Prod& p, hipStream_t s) {
-  const int N = MODE == FWD ? (GLU ? p.W / 2 : p.W) : p.K, cols = (N + TILE - 1) / TILE;
-  const long tiles = cols * (MODE == DW ? static_cast<long>(p.g.N) * ((p.W + TILE - 1) / TILE)
-                                        : max_row_tiles(p.g.R, p.g.N, TILE));
-  hipLaunchKernelGGL((simple_kernel<E, MODE, GLU>), dim3(std::min<long>(tiles, 1 << 20)), dim3(256), 0,
-                     s, p, cols, tiles);
-}
-
-template <int MODE, int BM, int BN, int WGS, bool GLU, bool GATHER>
+template <int MODE, int BM, int BN, int SL, int RA, int WGS, bool GLU, bool GATHER>
 int launch_mma(const Prod& p, hipStream_t s) {
-  constexpr int lds = (SA * BM + SB * BN) * SLICE * 2, NC = GLU ? BN / 2 : BN;
-  const auto fn = grouped_mma_kernel<MODE, BM, BN, WGS, GLU, GATHER>;
+  constexpr int lds = (RA * BM + SB * BN) * SL * 2, NC = GLU ? BN / 2 : BN;
+  const auto fn = grouped_mma_kernel<MODE, BM, BN, SL, RA, WGS, GLU, GATHER>;
   static std::atomic<bool> done[64];
   if (!allow_lds(reinterpret_cast<const void*>(fn), lds, done)) return MOE_EHIP;
   const int N = MODE == FWD ? (GLU ? p.W / 2 : p.W) : p.K;
@@ -165,23 +77,82 @@ int launch_mma(const Prod& p, hipStream_t s) {
   return MOE_OK;
 }
 
+template <int MODE, bool GLU, bool GATHER>
+int launch_tile(const Prod& p, hipStream_t s) {
+  switch (tile_choice(MODE, p.g.R, p.g.N, p.W, p.K, cu_count())) {
+    case TILE_256: return launch_mma<MODE, 256, 256, 64, 2, 1, GLU, GATHER>(p, s);
+    case TILE_128x256:
+      if constexpr (MODE == DX) return launch_mma<MODE, 128, 256, 32, 3, 2, GLU, GATHER>(p, s);
+    default: return launch_mma<MODE, 128, 128, 64, 2, 2, GLU, GATHER>(p, s);
+  }
+}
+
 template <int MODE, bool GLU>
 int launch_bf16(const Prod& p, hipStream_t s) {
-  // rows of an expert: a 256-row tile is half empty for 128
-  const bool large = p.g.R / p.g.N >= 192;
-  if (MODE != DX && p.token)
-    return large ? launch_mma<MODE, 256, 256, 1, GLU, MODE != DX>(p, s)
-                 : launch_mma<MODE, 128, 128, 2, GLU, MODE != DX>(p, s);
-  return large ? launch_mma<MODE, 256, 256, 1, GLU, false>(p, s)
-               : launch_mma<MODE, 128, 128, 2, GLU, false>(p, s);
+  if constexpr (MODE != DX)
+    if (p.token) return launch_tile<MODE, GLU, true>(p, s);
+  return launch_tile<MODE, GLU, false>(p, s);
+}
+
+template <int MODE>
+long f32_tiles(const Prod& p, bool glu, int edge) {
+  const int nc = glu && edge > 32 ? edge / 2 : edge, N = MODE == FWD ? (glu ? p.W / 2 : p.W) : p.K;
+  const long rows = MODE == DW ? static_cast<long>(p.g.N) * ((p.W + edge - 1) / edge)
+                               : max_row_tiles(p.g.R, p.g.N, edge);
+  return (rows * ((N + nc - 1) / nc) + 7) / 8 * 8;
+}
+
+template <int MODE, bool GLU, bool GATHER, int EDGE>
+int launch_f32_tile(const Prod& p, hipStream_t s) {
+  const long tiles = f32_tiles<MODE>(p, GLU, EDGE);
+  if (tiles > INT32_MAX) return MOE_EUNSUP;  // the outputs alone would not fit the card
+  hipLaunchKernelGGL((grouped_f32_kernel<MODE, GLU, GATHER, EDGE>),
+                     dim3(static_cast<unsigned>(std::min<long>(tiles, 1 << 20))), dim3(256), 0, s, p,
+                     static_cast<int>(tiles));
+  return MOE_OK;
+}
+
+template <int MODE, bool GLU, bool GATHER>
+int launch_f32_edge(const Prod& p, hipStream_t s) {
+  const int edge = tile_choice_f32(MODE, p.g.R, p.g.N, p.W, p.K, cu_count());
+  return edge == 32   ? launch_f32_tile<MODE, GLU, GATHER, 32>(p, s)
+         : edge == 64 ? launch_f32_tile<MODE, GLU, GATHER, 64>(p, s)
+                      : launch_f32_tile<MODE, GLU, GATHER, 128>(p, s);
+}
+
+template <int MODE, bool GLU>
+int launch_f32(const Prod& p, hipStream_t s) {
+  if constexpr (MODE != DX)
+    if (p.token) return launch_f32_edge<MODE, GLU, true>(p, s);
+  return launch_f32_edge<MODE, GLU, false>(p, s);
 }
 
 // Product of any type
 template <typename E, int MODE, bool GLU>
 int product(const Prod& p, hipStream_t s) {
   if constexpr (sizeof(E) == 2) return launch_bf16<MODE, GLU>(p, s);
-  launch<E, MODE, GLU>(p, s);
-  return MOE_OK;
+  else return launch_f32<MODE, GLU>(p, s);
+}
+
+// dx and dw (either may be absent: null y)
+template <typename E>
+int products(const Prod& x, const Prod& w, hipStream_t s) {
+  if (sizeof(E) == 4 && x.e.y && w.e.y) {
+    const int cus = cu_count();
+    const long dw0 = f32_tiles<DX>(x, false, 32), all = dw0 + f32_tiles<DW>(w, false, 32);
+    if (tile_choice_f32(DX, x.g.R, x.g.N, x.W, x.K, cus) == 32 &&
+        tile_choice_f32(DW, x.g.R, x.g.N, x.W, x.K, cus) == 32 && all <= (1 << 20)) {
+      const dim3 grid(static_cast<unsigned>(all)), block(256);
+      if (w.token)
+        hipLaunchKernelGGL((grouped_f32_pair_kernel<true>), grid, block, 0, s, x, w, static_cast<int>(dw0));
+      else
+        hipLaunchKernelGGL((grouped_f32_pair_kernel<false>), grid, block, 0, s, x, w, static_cast<int>(dw0));
+      return MOE_OK;
+    }
+  }
+  int rc = x.e.y ? product<E, DX, false>(x, s) : MOE_OK;
+  if (w.e.y && rc == MOE_OK) rc = product<E, DW, false>(w, s);
+  return rc;
 }
 
 inline size_t dz_bytes(int R, int O, int act, int dtype) {
@@ -208,14 +179,11 @@ int backward(const void* dy, const void* x, const int32_t* row_token, const Grou
                        static_cast<const E*>(dy), static_cast<const E*>(z), g, O, act,
                        static_cast<E*>(ws));
   }
-  Prod p{dz, w, nullptr, 0, g, W, K, Epilogue{}};
-  p.e.y = dx;
-  int rc = dx ? product<E, DX, false>(p, s) : MOE_OK;
-  p.c = x;
-  p.token = row_token;
-  p.x_rows = T;
-  p.e.y = dw;
-  if (dw && rc == MOE_OK) rc = product<E, DW, false>(p, s);
+  Prod px{dz, w, nullptr, 0, g, W, K, Epilogue{}};
+  Prod pw{dz, x, row_token, static_cast<size_t>(T), g, W, K, Epilogue{}};
+  px.e.y = dx;
+  pw.e.y = dw;
+  const int rc = products<E>(px, pw, s);
   return rc == MOE_OK ? launch_status() : rc;
 }
 

@@ -11,14 +11,13 @@
 #include <type_traits>
 
 #include "grouped_common.h"
+#include "grouped_plan.h"
 #include "linear_mma.h"
 
 namespace moe {
 namespace grp {
 
 using namespace lin;
-
-enum { FWD, DX, DW };
 
 constexpr int UNIT = 64;  // rows
 
@@ -33,17 +32,17 @@ struct Prod {
 
 // The dense layer's row operand with the rows of a token list: the tile's rows
 // are fixed, so the gather is in the lanes' offsets (x is at most 2^31 bytes).
-template <int EXT>
-struct GatherRows : Operand<false, false, EXT, lin::W> {
-  typedef Operand<false, false, EXT, lin::W> Base;
+template <int EXT, int SL>
+struct GatherRows : Operand<false, false, EXT, lin::W, SL> {
+  typedef Operand<false, false, EXT, lin::W, SL> Base;
   __device__ __forceinline__ void init_gather(const uint16_t* x, size_t ld, size_t x_rows,
                                               const int32_t* token, int valid, int wave, int lane) {
     const uint32_t row_bytes = static_cast<uint32_t>(ld) * 2;
     this->rsrc = buffer_rsrc(x, static_cast<uint32_t>(x_rows * row_bytes));
-    const int lrow = lane / 8, slot = lane % 8;
+    const int lrow = lane / Base::CPR, slot = lane % Base::CPR;
 #pragma unroll
     for (int q = 0; q < Base::Q; ++q) {
-      const int row = (wave * Base::Q + q) * 8 + lrow;
+      const int row = (wave * Base::Q + q) * Base::RPL + lrow;
       const int ch = slot ^ Base::row_swizzle(row);
       if (q < 2) this->first[q] = ch * 8;
       this->voff[q] = row < valid ? static_cast<uint32_t>(token[row]) * row_bytes + ch * 16 : OOB_OFF;
@@ -52,17 +51,17 @@ struct GatherRows : Operand<false, false, EXT, lin::W> {
 };
 
 // The reduction-strided operand whose k are the rows of a token list.  A wave's
-// loads of a slice are 16 consecutive k.  The list lies in vector registers, 64
-// tokens each, CHUNKS slices at a time; a load reads its rows' tokens from the
+// loads of a slice are consecutive k.  The list lies in vector registers, 64
+// tokens each, 64 CHUNKS tokens at a time; a load reads its rows' tokens from the
 // lanes that hold them, between the MFMAs.  (Tokens loaded by the scalar unit a
 // slice ahead cost 6 to 13 % of the product: a wait for the LDS fragments is
 // then a wait for them too.)
-template <int EXT>
+template <int EXT, int SL>
 struct GatherStrided {
-  typedef Operand<true, false, EXT, lin::W> Base;
+  typedef Operand<true, false, EXT, lin::W, SL> Base;
   static constexpr int BYTES = Base::BYTES, Q = Base::Q, CPR = EXT / 8, PER = 64 / CPR;
   static constexpr int CHUNKS = 16;
-  static_assert(64 % CPR == 0 && PER * Q == 16 && lin::W * 16 == SLICE, "16 rows per wave and slice");
+  static_assert(64 % CPR == 0 && PER * Q * lin::W == SL, "whole rows of every load");
   i32x4 rsrc;
   uint32_t step, first;  // bytes of a row of x, of the tile's first column
   uint32_t voff[4];      // the lane's chunk in loads q, q + 4, ..: the swizzle repeats every 4 rows
@@ -71,7 +70,7 @@ struct GatherStrided {
   typedef uint32_t u32x16 __attribute__((ext_vector_type(CHUNKS)));
   u32x16 list;
   uint32_t now;          // the slice's
-  int run;               // which CHUNKS slices the list is of
+  int run;               // which 64 CHUNKS tokens the list is of
 
   __device__ __forceinline__ void init(const uint16_t* x, int n0, size_t ld, size_t x_rows,
                                        const int32_t* tok, int tokens, int valid, int lane_) {
@@ -89,12 +88,12 @@ struct GatherStrided {
     }
   }
   __device__ __forceinline__ void fetch(int k0) {
-    const int at = k0 / SLICE;
+    const int at = k0 / 64;
     if (at / CHUNKS != run) {
       run = at / CHUNKS;
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i)
-        list[i] = static_cast<uint32_t>(token[min((run * CHUNKS + i) * SLICE + lane, last)]);
+        list[i] = static_cast<uint32_t>(token[min((run * CHUNKS + i) * 64 + lane, last)]);
     }
     now = list[at % CHUNKS];
   }
@@ -102,8 +101,9 @@ struct GatherStrided {
     uint32_t row = OOB_OFF;
 #pragma unroll
     for (int s = 0; s < PER; ++s) {
-      const int k = wave * 16 + q * PER + s;
-      const uint32_t t = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(now), k));
+      const int k = wave * (PER * Q) + q * PER + s;
+      const uint32_t t =
+          static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(now), k0 % 64 + k));
       const uint32_t off = k0 + k < kend ? t * step : OOB_OFF;
       row = s == 0 || lane / CPR == s ? off : row;
     }
@@ -116,7 +116,7 @@ struct GatherStrided {
 // FWD, DX: one tile of at most BM rows.  An expert's rows are cut into units of
 // 64 and these shared out evenly over its tiles, so that half a unit per expert
 // is multiplied in vain, not half a tile.
-template <int MODE, int BM, int BN, bool GLU, bool GATHER>
+template <int MODE, int BM, int BN, int SL, int RA, bool GLU, bool GATHER>
 __device__ __forceinline__ void data_product(const Prod& p, int block, unsigned char* smem) {
   constexpr int NC = GLU ? BN / 2 : BN;
   constexpr bool STRIDED = MODE == DX;
@@ -131,19 +131,19 @@ __device__ __forceinline__ void data_product(const Prod& p, int block, unsigned 
   const int m0 = lo + (units / tiles * mt + min(mt, units % tiles)) * UNIT, n0 = nt * NC;
   const int rows = min(height * UNIT, hi - m0);
   const uint16_t* w = static_cast<const uint16_t*>(p.c) + static_cast<size_t>(e) * p.W * p.K;
-  Operand<STRIDED, GLU, BN, lin::W> col;
+  Operand<STRIDED, GLU, BN, lin::W, SL> col;
   col.init(w + (STRIDED ? n0 : n0 * static_cast<size_t>(p.K)), p.K, min(NC, N - n0), wave, lane,
            GLU ? O * static_cast<size_t>(p.K) : 0);
   auto run = [&](auto h) {
     constexpr int H = decltype(h)::value * UNIT;
     if constexpr (H <= BM) {
-      GatherRows<H> row;
+      GatherRows<H, SL> row;
       const uint16_t* r = static_cast<const uint16_t*>(p.r);
       if constexpr (GATHER)
         row.init_gather(r, len, p.x_rows, p.token + m0, rows, wave, lane);
       else
         row.init(r + static_cast<size_t>(m0) * len, len, rows, wave, lane);
-      mma_core<false, STRIDED, H, BN, GLU, 8>(
+      mma_core<false, STRIDED, H, BN, GLU, 8, SL, RA, SB, (RA * BM + SB * BN) * SL * 2>(
           row, col, 0, len, smem, [&](int r, int c, float* g, float* u) {
             if (r < rows && n0 + c < N) finish<uint16_t, GLU, 8>(p.e, m0 + r, n0 + c, N, g, u);
           });
@@ -156,7 +156,7 @@ __device__ __forceinline__ void data_product(const Prod& p, int block, unsigned 
 }
 
 // DW: the tiles of this workgroup, every (workgroups of the XCD)-th of its range.
-template <int BM, int BN, bool GATHER>
+template <int BM, int BN, int SL, int RA, bool GATHER>
 __device__ __forceinline__ void weight_product(const Prod& p, unsigned char* smem) {
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
@@ -178,7 +178,7 @@ __device__ __forceinline__ void weight_product(const Prod& p, unsigned char* sme
       }
       continue;
     }
-    Operand<true, false, BM, lin::W> row;
+    Operand<true, false, BM, lin::W, SL> row;
     row.init(static_cast<const uint16_t*>(p.r) + static_cast<size_t>(lo) * p.W + m0, p.W, rows, wave,
              lane);
     auto chunk = [&](int r, int c, float* g, float*) {
@@ -186,24 +186,25 @@ __device__ __forceinline__ void weight_product(const Prod& p, unsigned char* sme
     };
     const uint16_t* x = static_cast<const uint16_t*>(p.c);
     if constexpr (GATHER) {
-      GatherStrided<BN> col;
+      GatherStrided<BN, SL> col;
       col.init(x, n0, p.K, p.x_rows, p.token + lo, p.g.R - lo, width, lane);
-      mma_core<true, true, BM, BN, false, 8>(row, col, 0, count, smem, chunk);
+      mma_core<true, true, BM, BN, false, 8, SL, RA>(row, col, 0, count, smem, chunk);
     } else {
-      Operand<true, false, BN, lin::W> col;
+      Operand<true, false, BN, lin::W, SL> col;
       col.init(x + static_cast<size_t>(lo) * p.K + n0, p.K, width, wave, lane);
-      mma_core<true, true, BM, BN, false, 8>(row, col, 0, count, smem, chunk);
+      mma_core<true, true, BM, BN, false, 8, SL, RA>(row, col, 0, count, smem, chunk);
     }
     __syncthreads();  // the next tile's ring takes the place of this one's output
   }
 }
 
-template <int MODE, int BM, int BN, int WGS, bool GLU, bool GATHER>
+// RA: ring stages of the row operand.
+template <int MODE, int BM, int BN, int SL, int RA, int WGS, bool GLU, bool GATHER>
 __global__ __launch_bounds__(lin::W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(WGS, WGS)))
 void grouped_mma_kernel(Prod p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  if constexpr (MODE == DW) weight_product<BM, BN, GATHER>(p, smem);
-  else data_product<MODE, BM, BN, GLU, GATHER>(p, blockIdx.x, smem);
+  if constexpr (MODE == DW) weight_product<BM, BN, SL, RA, GATHER>(p, smem);
+  else data_product<MODE, BM, BN, SL, RA, GLU, GATHER>(p, blockIdx.x, smem);
 }
 
 }  // namespace grp

@@ -1,0 +1,72 @@
+// Which kernel a grouped product runs: functions of the sizes and the number of
+// compute units, without device code (the tests compile this file for the host).
+// The rows of each expert are known on the device only, so the choice goes by
+// their mean.
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+
+namespace moe {
+namespace grp {
+
+enum { FWD, DX, DW };
+
+// Tiles of the bf16 products
+enum { TILE_256, TILE_128, TILE_128x256 };
+
+inline double rounds(double tiles, int cus) { return std::ceil(tiles / cus); }
+
+// rows, W, K: of a product as in Prod; cols: output columns (FWD with a gated
+// activation: of W).  Times in us, from sweeps of 64 .. 1024 rows per expert, 128
+// experts, weights of 512^2 .. 4096^2: a slice of 64 k takes a 256 x 256 tile 1.55
+// (the matrix pipe at its power limit), a 128 x 128 tile 0.43, on top of 14 (8 for
+// a weight gradient, whose workgroups stay) and 4.
+//   64 rows, 1536 x 2048:  dw 257 with 256 x 256 tiles, 274 with 128 x 128;
+//     dx 165, 170, and 150 with 128 x 256 tiles and slices of 32: it is the weights
+//     that are read, 5.4 TB/s, by two workgroups a CU
+//   512 rows:  dw 518 and 642, dx 432 and 523 (481), forward 374 and 429
+inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
+  const int used = std::min(N, R);  // experts that can have rows
+  const double rows = static_cast<double>(R) / used;
+  auto tiles = [&](int m, int n) {
+    const double a = mode == DW ? std::ceil(static_cast<double>(W) / m) : std::ceil(rows / m);
+    const double b = std::ceil(static_cast<double>(mode == FWD ? W : K) / n);
+    return (mode == DW ? N : used) * a * b;
+  };
+  const double slices = (mode == DW ? rows : mode == FWD ? K : W) / 64.0;
+  const double height = mode == DW ? 1.0 : std::min(1.0, std::ceil(rows / 64) / 4);
+  const double large = rounds(tiles(256, 256), cus) *
+                       (slices * std::max(0.4, 1.55 * height) + (mode == DW ? 8 : 14));
+  const double small = rounds(tiles(128, 128), cus) * (slices * 0.43 + 2) + 4;
+  if (mode == DX && rows <= 128 && tiles(128, 256) >= cus) return TILE_128x256;
+  return large <= small ? TILE_256 : TILE_128;
+}
+
+// The same for fp32: the edge of the tile, by the dense layer's measures (us per
+// k of a tile alone on its compute unit, and with others).
+//   512^3 in one expert: see plan_f32, whose model this is without splits
+inline int tile_choice_f32(int mode, int R, int N, int W, int K, int cus) {
+  const int used = std::min(N, R);
+  const double rows = static_cast<double>(R) / used;
+  int best = 32;
+  double least = 1e30;
+  for (int edge = 32; edge <= 128; edge *= 2) {
+    const double a = std::ceil((mode == DW ? W : rows) / edge);
+    const double b = std::ceil(static_cast<double>(mode == FWD ? W : K) / edge);
+    const double len = mode == DW ? rows : mode == FWD ? K : W;
+    double load = (mode == DW ? N : used) * a * b / cus;
+    if (load <= 4) load = std::ceil(load);
+    const double alone = edge == 32 ? (mode == FWD ? 0.009 : 0.011) : edge == 64 ? 0.028 : 0.084;
+    const double shared = edge == 32 ? alone : edge == 64 ? 0.025 : 0.068;
+    const double us = len * std::max(alone, load * shared);
+    if (us < least) {
+      least = us;
+      best = edge;
+    }
+  }
+  return best;
+}
+
+}  // namespace grp
+}  // namespace moe

@@ -97,6 +97,23 @@ int product(Mma a, const Plan& p, float* part, hipStream_t s) {
 }
 
 // ------------------------------------------------------------ fp32 product
+// Both products of a small backward pass and the bias gradient's last sum in
+// one launch: workgroups from dw0 on are dw's, from bias0 on the bias's; nx:
+// tiles along the columns, K for both.
+__global__ __launch_bounds__(256) void f32_pair_kernel(F32Prod dx, F32Prod dw, BiasSum b, int nx,
+                                                       int dw0, int bias0) {
+  __shared__ float lds[SMALL_LDS];
+  int block = blockIdx.x;
+  if (block < dw0) {
+    f32_small_tile<false, true, false>(dx, block % nx, block / nx, lds);
+  } else if (block < bias0) {
+    block -= dw0;
+    f32_small_tile<true, true, false>(dw, block % nx, block / nx, lds);
+  } else {
+    bias_sum<float>(b, block - bias0, lds);
+  }
+}
+
 template <bool RS, bool CS, bool GLU>
 int product_f32(F32Prod a, const Plan& p, float* part, hipStream_t s) {
   if (p.tile == 32) {

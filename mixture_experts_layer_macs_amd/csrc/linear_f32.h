@@ -20,17 +20,32 @@ struct F32Prod {
   int per_split;    // reduction length of a split (large tiles)
   float* part;      // splits > 1: [splits][M][N] partial sums
   Epilogue e;
+  const int32_t* token;  // grouped products: stored rows of the gathered operand
 };
 
+// Which stored rows of an operand a product reads: as they lie, or those of a
+// token list.
+enum Gather { PLAIN, ROWS, COLUMNS };  // COLUMNS: of the column operand
+
+template <bool LISTED>
+__device__ __forceinline__ size_t stored(const int32_t* token, int i) {
+  if constexpr (LISTED) return static_cast<size_t>(token[i]);
+  else return static_cast<size_t>(i);
+}
+
 // Four values k, k + 1, .. of row m, zeros outside the matrix.
-template <bool STRIDED>
-__device__ __forceinline__ f32x4 quad(const float* p, size_t ld, int m, int mend, int k, int kend) {
+template <bool STRIDED, bool LISTED = false>
+__device__ __forceinline__ f32x4 quad(const float* p, size_t ld, int m, int mend, int k, int kend,
+                                      const int32_t* token = nullptr) {
   if constexpr (!STRIDED) {
-    return m < mend && k < kend ? *reinterpret_cast<const f32x4*>(p + m * ld + k) : f32x4{0, 0, 0, 0};
+    return m < mend && k < kend
+               ? *reinterpret_cast<const f32x4*>(p + stored<LISTED>(token, m) * ld + k)
+               : f32x4{0, 0, 0, 0};
   } else {
     f32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = m < mend && k + i < kend ? p[(k + i) * ld + m] : 0.f;
+    for (int i = 0; i < 4; ++i)
+      v[i] = m < mend && k + i < kend ? p[stored<LISTED>(token, k + i) * ld + m] : 0.f;
     return v;
   }
 }
@@ -42,7 +57,7 @@ __device__ __forceinline__ f32x4 quad(const float* p, size_t ld, int m, int mend
 // larger tile would leave the card empty.  256 x 128 -> 256: 4.2 us.
 constexpr int SMALL_LDS = 4 * 32 * 33;  // floats per output matrix
 
-template <bool RS, bool CS, bool GLU>
+template <bool RS, bool CS, bool GLU, Gather G = PLAIN>
 __device__ __forceinline__ void f32_small_tile(const F32Prod& p, int bx, int by, float* lds) {
   constexpr int H = GLU ? 2 : 1, TURNS = 4;
   float(*red)[4][32][33] = reinterpret_cast<float(*)[4][32][33]>(lds);
@@ -61,10 +76,11 @@ __device__ __forceinline__ void f32_small_tile(const F32Prod& p, int bx, int by,
 #pragma unroll
     for (int u = 0; u < TURNS; ++u) {
       const int k = k0 + 32 * u + k_lane;
-      a[u] = quad<RS>(p.r, p.ldr, m, p.M, k, p.K);
+      a[u] = quad<RS, G == ROWS>(p.r, p.ldr, m, p.M, k, p.K, p.token);
 #pragma unroll
       for (int h = 0; h < H; ++h)
-        b[h][u] = quad<CS>(p.c + h * static_cast<size_t>(p.N) * p.ldc, p.ldc, n, p.N, k, p.K);
+        b[h][u] = quad<CS, G == COLUMNS>(p.c + h * static_cast<size_t>(p.N) * p.ldc, p.ldc, n, p.N, k,
+                                         p.K, p.token);
     }
 #pragma unroll
     for (int u = 0; u < TURNS; ++u)
@@ -100,29 +116,12 @@ __global__ __launch_bounds__(256) void f32_small_kernel(F32Prod p) {
   f32_small_tile<RS, CS, GLU>(p, blockIdx.x, blockIdx.y, lds);
 }
 
-// Both products of a small backward pass and the bias gradient's last sum in
-// one launch: workgroups from dw0 on are dw's, from bias0 on the bias's; nx:
-// tiles along the columns, K for both.
-__global__ __launch_bounds__(256) void f32_pair_kernel(F32Prod dx, F32Prod dw, BiasSum b, int nx,
-                                                       int dw0, int bias0) {
-  __shared__ float lds[SMALL_LDS];
-  int block = blockIdx.x;
-  if (block < dw0) {
-    f32_small_tile<false, true, false>(dx, block % nx, block / nx, lds);
-  } else if (block < bias0) {
-    block -= dw0;
-    f32_small_tile<true, true, false>(dw, block % nx, block / nx, lds);
-  } else {
-    bias_sum<float>(b, block - bias0, lds);
-  }
-}
-
 // Large outputs: tiles of 64 F x 64 F (F = 1 or 2), 4 waves of 32 F x 32 F,
 // slices of 32 / F k through two LDS buffers laid out [k][m], the next two
 // slices' loads in flight in registers while one is multiplied.  A slice is 16 F MFMAs
 // of 64 cycles per wave, so the LDS traffic stays below the matrix pipe's time.
 // 4096^3: 1.12 ms (123 TFLOP/s; the library 0.92 to 1.0).
-template <bool STRIDED, bool MIX, int F>
+template <bool STRIDED, bool MIX, int F, bool LISTED = false>
 struct F32Stage {
   static constexpr int EXT = 64 * F, BK = 32 / F;
   static constexpr int PITCH = EXT + 4;  // floats: rows 4 banks apart, 16-byte aligned
@@ -132,18 +131,20 @@ struct F32Stage {
   // strided: k t / MQ and 256 / MQ on, m quad t % MQ.  MIX (gated weights):
   // every 32 rows are 16 gate rows and the 16 up rows of the same columns.
   __device__ __forceinline__ void fetch(const float* p, size_t ld, int valid, int k0, int kend,
-                                        size_t up) {
+                                        size_t up, const int32_t* token) {
     const int t = threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if constexpr (!STRIDED) {
         const int row = t / KQ + 256 / KQ * i;
         const int at = MIX ? row / 32 * 16 + row % 16 : row;
-        v[i] = quad<false>(p + (MIX && row % 32 >= 16 ? up : 0), ld, at, valid, k0 + t % KQ * 4, kend);
+        v[i] = quad<false, LISTED>(p + (MIX && row % 32 >= 16 ? up : 0), ld, at, valid,
+                                   k0 + t % KQ * 4, kend, token);
       } else {
         const int k = k0 + t / MQ + 256 / MQ * i, m = t % MQ * 4;
-        v[i] = k < kend && m < valid ? *reinterpret_cast<const f32x4*>(p + k * ld + m)
-                                     : f32x4{0, 0, 0, 0};
+        v[i] = k < kend && m < valid
+                   ? *reinterpret_cast<const f32x4*>(p + stored<LISTED>(token, k) * ld + m)
+                   : f32x4{0, 0, 0, 0};
       }
     }
   }
@@ -161,27 +162,32 @@ struct F32Stage {
   }
 };
 
-template <bool RS, bool CS, int F, bool GLU, bool PART>
-__global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
+constexpr int LARGE_LDS = 2 * 32 * 68;  // floats of an operand's buffers: F = 2: 2 * 16 * 132
+
+template <bool RS, bool CS, int F, bool GLU, bool PART, Gather G = PLAIN>
+__device__ __forceinline__ void f32_large_tile(const F32Prod& p, int bx, int by, int bz, float* lds) {
   static_assert(!GLU || (!CS && !PART), "pairs of gate and up rows: y = x w^T only");
-  typedef F32Stage<RS, false, F> Row;
-  typedef F32Stage<CS, GLU, F> Col;
+  typedef F32Stage<RS, false, F, G == ROWS> Row;
+  typedef F32Stage<CS, GLU, F, G == COLUMNS> Col;
   constexpr int PITCH = Row::PITCH, BK = Row::BK, EXT = Row::EXT;
-  __shared__ __align__(16) float sr[2][BK * PITCH], sc[2][BK * PITCH];
+  static_assert(2 * BK * PITCH <= LARGE_LDS, "two buffers");
+  float(*sr)[BK * PITCH] = reinterpret_cast<float(*)[BK * PITCH]>(lds);
+  float(*sc)[BK * PITCH] = reinterpret_cast<float(*)[BK * PITCH]>(lds + LARGE_LDS);
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
   const int wm = wave / 2, wn = wave % 2;
   constexpr int NC = GLU ? EXT / 2 : EXT;
-  const int m0 = blockIdx.y * EXT, n0 = blockIdx.x * NC;
-  const int k_lo = blockIdx.z * p.per_split, k_hi = min(p.K, k_lo + p.per_split);
-  const float* r = p.r + (RS ? m0 : m0 * p.ldr);
+  const int m0 = by * EXT, n0 = bx * NC;
+  const int k_lo = bz * p.per_split, k_hi = min(p.K, k_lo + p.per_split);
+  const float* r = p.r + (RS ? m0 : G == ROWS ? 0 : m0 * p.ldr);
+  const int32_t* token = p.token + (G == ROWS ? m0 : 0);
   const float* c = p.c + (CS ? n0 : n0 * p.ldc);
   const int mv = p.M - m0, nv = p.N - n0;
   Row row[2];
   Col col[2];
   auto fetch = [&](int set, int k0) {
-    row[set].fetch(r, p.ldr, mv, k0, k_hi, 0);
-    col[set].fetch(c, p.ldc, nv, k0, k_hi, GLU ? p.N * p.ldc : 0);
+    row[set].fetch(r, p.ldr, mv, k0, k_hi, 0, token);
+    col[set].fetch(c, p.ldc, nv, k0, k_hi, GLU ? p.N * p.ldc : 0, token);
   };
   f32x16 acc[F][F];
 #pragma unroll
@@ -236,11 +242,17 @@ __global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
           if constexpr (GLU) u[i] = acc[x][y][4 * q + 8 + i];
         }
         if constexpr (PART)
-          store4(p.part + (static_cast<size_t>(blockIdx.z) * p.M + m) * p.N + n, g);
+          store4(p.part + (static_cast<size_t>(bz) * p.M + m) * p.N + n, g);
         else
           finish<float, GLU, 4>(p.e, m, n, p.N, g, u);
       }
   }
+}
+
+template <bool RS, bool CS, int F, bool GLU, bool PART>
+__global__ __launch_bounds__(256) void f32_large_kernel(F32Prod p) {
+  __shared__ __align__(16) float lds[2 * LARGE_LDS];
+  f32_large_tile<RS, CS, F, GLU, PART>(p, blockIdx.x, blockIdx.y, blockIdx.z, lds);
 }
 
 }  // namespace lin

@@ -53,11 +53,14 @@ struct Mma {
 // of a gated activation): every 32 tile rows are 16 gate rows and the 16 up
 // rows of the same columns, so that a lane's accumulators r and r + 8 are a
 // pair; a load of 8 rows lies in one half.
-template <bool STRIDED, bool MIX, int EXT, int NW>
+// SL: k of a slice, 64 or 32.
+template <bool STRIDED, bool MIX, int EXT, int NW, int SL = SLICE>
 struct Operand {
-  static constexpr int BYTES = EXT * SLICE * 2;
+  static constexpr int BYTES = EXT * SL * 2;
+  static constexpr int RPL = 512 / SL, CPR = STRIDED ? EXT / 8 : SL / 8;  // contiguous: rows of a load; chunks of an LDS row
   static constexpr int Q = BYTES / 1024 / NW;
-  static_assert(Q >= 2 && Q % 2 == 0 && BYTES % (1024 * NW) == 0, "whole pairs of loads per wave");
+  static_assert(Q >= 1 && BYTES % (1024 * NW) == 0, "whole loads per wave");
+  static_assert(STRIDED || SL == 32 || Q % 2 == 0, "rows of a load: the swizzle goes by its parity");
   static_assert(!(STRIDED && MIX), "gated weights are reduction-contiguous");
   uint32_t voff[Q];
   int first[2];  // contiguous: k of the lane's chunk in the slice, by load parity
@@ -75,17 +78,16 @@ struct Operand {
       const uint32_t bytes = static_cast<uint32_t>(valid) * row_bytes;
       rsrc = buffer_rsrc(p, bytes);
       if constexpr (MIX) rsrc_up = buffer_rsrc(p + up, bytes);
-      const int lrow = lane / 8, slot = lane % 8;
+      const int lrow = lane / CPR, slot = lane % CPR;
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const int row = (wave * Q + q) * 8 + lrow;
+        const int row = (wave * Q + q) * RPL + lrow;
         const int ch = slot ^ row_swizzle(row);
         const int at = MIX ? row / 32 * 16 + row % 16 : row;
         if (q < 2) first[q] = ch * 8;
         voff[q] = at < valid ? static_cast<uint32_t>(at) * row_bytes + ch * 16 : OOB_OFF;
       }
     } else {
-      constexpr int CPR = EXT / 8;  // 16-byte chunks of an LDS row
       base = reinterpret_cast<const char*>(p);
       step = ld * 2;
       tail = static_cast<uint32_t>(valid) * 2;
@@ -101,7 +103,7 @@ struct Operand {
   // Contiguous: 16-byte chunks of a row, so that 16 rows of a fragment read
   // cover all banks.
   static __device__ __forceinline__ int row_swizzle(int row) {
-    return (row >> 1) & 7;
+    return SL == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
   }
   // Strided: the four k rows of a read, 64-byte group g of each: on different groups
   // of 16 banks.  LDS rows of 512 or 256 bytes start at bank 0, those of 384
@@ -114,11 +116,11 @@ struct Operand {
   // load q of the slice from k0 (k up to kend) into the stage at lds
   __device__ __forceinline__ void load(int q, int k0, int kend, uint32_t lds, int wave) const {
     if constexpr (!STRIDED) {
-      lds_dma16(MIX && ((wave * Q + q) >> 1 & 1) ? rsrc_up : rsrc,
+      lds_dma16(MIX && ((wave * Q + q) / (16 / RPL) & 1) ? rsrc_up : rsrc,
                 first[q & 1] < kend - k0 ? voff[q] : OOB_OFF, static_cast<uint32_t>(k0) * 2,
                 lds + (wave * Q + q) * 1024);
     } else {
-      const uint32_t rows = static_cast<uint32_t>(min(SLICE, kend - k0));
+      const uint32_t rows = static_cast<uint32_t>(min(SL, kend - k0));
       const i32x4 rs = buffer_rsrc(base + static_cast<size_t>(k0) * step,
                                    (rows - 1) * static_cast<uint32_t>(step) + tail);
       lds_dma16(rs, voff[q], 0, lds + (wave * Q + q) * 1024);
@@ -128,12 +130,12 @@ struct Operand {
 
 // Fragment reader: 32 rows (m or n) x 16 k from row m0 of the operand's tile.
 typedef __attribute__((address_space(3))) const unsigned char lds_cbyte;
-template <bool STRIDED, int EXT>
+template <bool STRIDED, int EXT, int SL = SLICE>
 struct Reader {
-  typedef Operand<STRIDED, false, EXT, 1> Op;
+  typedef Operand<STRIDED, false, EXT, 1, SL> Op;
   static __device__ __forceinline__ uint32_t lane_off(int m0, int lane) {
     if constexpr (!STRIDED) {
-      return (m0 + (lane & 31)) * (SLICE * 2);
+      return (m0 + (lane & 31)) * (SL * 2);
     } else {
       const int g = lane >> 4, i = lane & 15;
       const int k = 8 * (g >> 1) + (i >> 2);
@@ -193,17 +195,18 @@ struct Staging {
 // One tile: the sum over k_lo <= k < k_hi (not empty) of the operands' slices,
 // whose chunks of V output columns go to out(row, column, sums, up sums), places
 // within the tile, also those past the matrix's end.  Row and Col: Operand, or
-// another with its functions; smem: the ring.
-template <bool RS, bool CS, int BM, int BN, bool GLU, int V, class Row, class Col, class Out>
+// another with its functions; smem: LDS bytes, the ring.
+template <bool RS, bool CS, int BM, int BN, bool GLU, int V, int SL = SLICE, int SA = lin::SA,
+          int SB = lin::SB, int LDS = (SA * BM + SB * BN) * SL * 2, class Row, class Col, class Out>
 __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
                                          unsigned char* smem, Out out_chunk) {
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
   static_assert(TM % 32 == 0 && TN % 32 == 0, "whole fragments");
-  static_assert(SA == 2 && SB == 3, "the order of requests, below");
-  typedef Reader<RS, BM> RowR;
-  typedef Reader<CS, BN> ColR;
+  static_assert(SA >= 2 && SA <= 3 && SB == 3, "the order of requests, below");
+  typedef Reader<RS, BM, SL> RowR;
+  typedef Reader<CS, BN, SL> ColR;
   constexpr int B_BASE = SA * Row::BYTES;
-  constexpr int KK = SLICE / 16;
+  constexpr int KK = SL / 16;
   static_assert(KK % 2 == 0, "fragment sets alternate");
   constexpr int NMF = FM * FN;
 
@@ -211,7 +214,7 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
   const int wm = wave / WN, wn = wave % WN;
   constexpr int NC = GLU ? BN / 2 : BN;  // output columns of the tile
-  const int nk = (k_hi - k_lo + SLICE - 1) / SLICE;
+  const int nk = (k_hi - k_lo + SL - 1) / SL;
   const uint32_t lds_base = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(smem))));
   lds_cbyte* lds0 = (lds_cbyte*)(smem);
@@ -219,13 +222,13 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
   // Requests past the last slice fetch it again into a stage that is not read
   // any more, so that every iteration issues the same number of loads.
   auto load_row = [&](int t, int q) {
-    row.load(q, k_lo + min(t, nk - 1) * SLICE, k_hi, lds_base + (t % SA) * Row::BYTES, wave);
+    row.load(q, k_lo + min(t, nk - 1) * SL, k_hi, lds_base + (t % SA) * Row::BYTES, wave);
   };
   auto load_col = [&](int t, int q) {
-    col.load(q, k_lo + min(t, nk - 1) * SLICE, k_hi, lds_base + B_BASE + (t % SB) * Col::BYTES,
+    col.load(q, k_lo + min(t, nk - 1) * SL, k_hi, lds_base + B_BASE + (t % SB) * Col::BYTES,
              wave);
   };
-  auto fetch_col = [&](int t) { col.fetch(k_lo + min(t, nk - 1) * SLICE); };
+  auto fetch_col = [&](int t) { col.fetch(k_lo + min(t, nk - 1) * SL); };
   auto load_rows = [&](int t) {
 #pragma unroll
     for (int q = 0; q < Row::Q; ++q) load_row(t, q);
@@ -313,7 +316,7 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
   // wave at a time, so that rows are stored whole, 16 bytes per lane.  (Stored
   // from the MFMA layout, 8 bytes per lane in 32 rows at once, the output took
   // 12 to 22 us of a 52 to 64 us product, for 4 to 8 us of traffic.)
-  typedef Staging<BM, BN, SA * Row::BYTES + SB * Col::BYTES> St;
+  typedef Staging<BM, BN, LDS> St;
   constexpr int XC = St::XC, ROWS = WM * XC * 32, PITCH = St::PITCH;  // PITCH in floats
   constexpr int CC = NC / V;
   constexpr int ITER = ROWS * CC / (W * MOE_WAVE);

@@ -73,6 +73,8 @@ struct RowSum {
 };
 
 constexpr int threads_of(int tpr) { return tpr > 256 ? tpr : 256; }
+// Backward: 8 waves, so that few workgroups leave few column sums to join.
+constexpr int back_threads_of(int tpr) { return tpr > 64 ? tpr : 512; }
 
 // 16 bytes of an array, or zeros
 template <typename E, int V>
@@ -201,15 +203,18 @@ __global__ __launch_bounds__(WIDE) void norm_wide_kernel(Forward a) {
 }
 
 // ------------------------------------------------------------------ backward
-template <typename E, int V>
-__device__ __forceinline__ void dx_out(const Backward& a, size_t row, int col, const float* dy,
-                                       const float* h, float mu, float muh, float rstd) {
-  float w[V], d[V], g[V];
-  load_v<V>(static_cast<const E*>(a.weight) + col, w);
-  load_if<E, V>(static_cast<const E*>(a.dsum) + row + col, a.dsum != nullptr, g);
+// 16 bytes as they lie in memory, and their values
+template <int V>
+__device__ __forceinline__ void values(lin::u32x4 w, float* f) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) d[i] = rstd * (dy[i] * w[i] - mu - h[i] * muh) + g[i];
-  store_v<V>(static_cast<E*>(a.dx) + row + col, d);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (V == 8) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      f[i] = __uint_as_float(w[i]);
+    }
+  }
 }
 
 // The workgroup's sums of V columns
@@ -225,53 +230,87 @@ __device__ __forceinline__ void sums_out(const Backward& a, int col, const float
   if (a.dbias) store_v<V>(static_cast<E*>(a.dbias) + col, b);
 }
 
-// A group of TPR threads takes every (workgroups x ROWS)-th row and keeps the
-// column sums of its rows in registers; the workgroup's groups add theirs in
-// order through LDS.
-template <typename D, int TPR, int NV>
-__global__ __launch_bounds__(threads_of(TPR)) void norm_backward_kernel(Backward a) {
+// A group of TPR threads takes every (workgroups x ROWS)-th row, the next one's
+// arrays in flight while one is worked on, and keeps the column sums of its rows
+// in registers; the workgroup's groups add theirs in order through LDS.
+// BIAS: the bias's column sums are wanted (their registers otherwise are not).
+template <typename D, int TPR, int NV, bool BIAS>
+__global__ __launch_bounds__(back_threads_of(TPR)) void norm_backward_kernel(Backward a) {
   typedef typename D::elem E;
-  constexpr int V = D::V, ROWS = threads_of(TPR) / TPR;
+  constexpr int V = D::V, ROWS = back_threads_of(TPR) / TPR;
   __shared__ float red[2][TPR / MOE_WAVE > 0 ? TPR / MOE_WAVE : 1];
   __shared__ float cols[2][ROWS > 1 ? TPR * NV * V : 1];
   RowSum<TPR> sum{red};
   const int l = threadIdx.x % TPR, group = threadIdx.x / TPR;
-  float aw[NV][V] = {}, ab[NV][V] = {};
-  for (int t = blockIdx.x * ROWS + group; t < a.T; t += gridDim.x * ROWS) {
-    const size_t row = static_cast<size_t>(t) * a.H;
-    const float mean = a.mean ? a.mean[t] : 0.f, rstd = a.rstd[t];
-    float dy[NV][V], h[NV][V], u = 0.f, uh = 0.f;
+  lin::u32x4 dyn[NV], sn[NV], gn[NV];
+  float mean_n = 0.f, rstd_n;
+  auto piece = [&](const void* p, size_t row, int j) {
+    const int col = (l + TPR * j) * V;
+    const size_t at = row + (col < a.H ? col : 0);  // past the end: a piece that is not used
+    return *reinterpret_cast<const lin::u32x4*>(static_cast<const E*>(p) + at);
+  };
+  auto row_of = [&](int t) { return static_cast<size_t>(min(t, a.T - 1)) * a.H; };
+  auto request = [&](int t) {
+    const size_t row = row_of(t);
+    t = min(t, a.T - 1);
+    if (a.mean) mean_n = a.mean[t];
+    rstd_n = a.rstd[t];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int col = (l + TPR * j) * V;
-      const bool in = col < a.H;
-      load_if<E, V>(static_cast<const E*>(a.dy) + row + col, in, dy[j]);
-      load_if<E, V>(static_cast<const E*>(a.s) + row + col, in, h[j]);
+      dyn[j] = piece(a.dy, row, j);
+      sn[j] = piece(a.s, row, j);
+    }
+  };
+  auto request_sum = [&](int t) {
+    const size_t row = row_of(t);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) gn[j] = a.dsum ? piece(a.dsum, row, j) : lin::u32x4{0, 0, 0, 0};
+  };
+  float aw[NV][V] = {}, ab[NV][V] = {};
+  int t = blockIdx.x * ROWS + group;
+  request(t);
+  request_sum(t);
+  for (; t < a.T; t += gridDim.x * ROWS) {
+    const size_t row = static_cast<size_t>(t) * a.H;
+    const float mean = mean_n, rstd = rstd_n;
+    float h[NV][V], u = 0.f, uh = 0.f;
+    lin::u32x4 dyr[NV];  // as it lies: half the registers of its values in bf16
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const bool in = (l + TPR * j) * V < a.H;
+      dyr[j] = in ? dyn[j] : lin::u32x4{0, 0, 0, 0};
+      values<V>(sn[j], h[j]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[j][i] = in ? (h[j][i] - mean) * rstd : 0.f;
+    }
+    request(t + gridDim.x * ROWS);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float dy[V], w[V] = {};
+      values<V>(dyr[j], dy);
+      if (a.dx) values<V>(piece(a.weight, 0, j), w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        h[j][i] = in ? (h[j][i] - mean) * rstd : 0.f;
-        aw[j][i] += dy[j][i] * h[j][i];
-        ab[j][i] += dy[j][i];
+        aw[j][i] += dy[i] * h[j][i];
+        if constexpr (BIAS) ab[j][i] += dy[i];
+        u += dy[i] * w[i];
+        uh += dy[i] * w[i] * h[j][i];
       }
     }
     if (!a.dx) continue;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int col = (l + TPR * j) * V;
-      float w[V];
-      load_if<E, V>(static_cast<const E*>(a.weight) + col, col < a.H, w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        u += dy[j][i] * w[i];
-        uh += dy[j][i] * w[i] * h[j][i];
-      }
-    }
     const float mu = a.mean ? sum(u) / a.H : 0.f, muh = sum(uh) / a.H;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = (l + TPR * j) * V;
-      if (col < a.H) dx_out<E, V>(a, row, col, dy[j], h[j], mu, muh, rstd);
+      float dy[V], w[V], g[V];
+      values<V>(dyr[j], dy);
+      values<V>(piece(a.weight, 0, j), w);
+      values<V>(gn[j], g);
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] += rstd * (dy[i] * w[i] - mu - h[j][i] * muh);
+      if (col < a.H) store_v<V>(static_cast<E*>(a.dx) + row + col, g);
     }
+    request_sum(t + gridDim.x * ROWS);
   }
   if (!a.dweight && !a.dbias) return;
   if constexpr (ROWS == 1) {
@@ -293,7 +332,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_backward_kernel(Backward
           }
       __syncthreads();
     }
-    for (int c = threadIdx.x * V; c < a.H; c += threads_of(TPR) * V)
+    for (int c = threadIdx.x * V; c < a.H; c += back_threads_of(TPR) * V)
       sums_out<E, V>(a, c, cols[0] + c, cols[1] + c);
   }
 }
@@ -309,7 +348,7 @@ __global__ __launch_bounds__(WIDE) void norm_backward_wide_kernel(Backward a) {
   const size_t row = static_cast<size_t>(t) * a.H;
   const float mean = a.mean ? a.mean[t] : 0.f, rstd = a.rstd[t];
   const E *pdy = static_cast<const E*>(a.dy) + row, *ps = static_cast<const E*>(a.s) + row;
-  float dy[V], h[V], w[V], u = 0.f, uh = 0.f;
+  float dy[V], h[V], w[V], g[V], u = 0.f, uh = 0.f;
   for (int col = l * V; col < a.H; col += WIDE * V) {
     load_v<V>(pdy + col, dy);
     load_v<V>(ps + col, h);
@@ -326,7 +365,11 @@ __global__ __launch_bounds__(WIDE) void norm_backward_wide_kernel(Backward a) {
     load_v<V>(ps + col, h);
 #pragma unroll
     for (int i = 0; i < V; ++i) h[i] = (h[i] - mean) * rstd;
-    dx_out<E, V>(a, row, col, dy, h, mu, muh, rstd);
+    load_v<V>(static_cast<const E*>(a.weight) + col, w);
+    load_if<E, V>(static_cast<const E*>(a.dsum) + row + col, a.dsum != nullptr, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dy[i] = rstd * (dy[i] * w[i] - mu - h[i] * muh) + g[i];
+    store_v<V>(static_cast<E*>(a.dx) + row + col, dy);
   }
 }
 
@@ -384,24 +427,23 @@ struct Shape {
   int tpr, nv;  // tpr 0: wide rows
 };
 
-// Threads of a row and 16-byte pieces of each: the fewest threads whose pieces,
-// at most 4, hold the row (the backward pass keeps five values per column).
+// Threads of a row and 16-byte pieces of each: a wave while its lanes hold at
+// most 32 columns (the backward pass keeps six values per column), else four
+// waves.  (fp32 rows of 1028 in four waves, the second piece all but empty: 57 us
+// backward for 16381 rows.)
 inline Shape shape_of(int H, int dtype) {
-  const int pieces = H / (dtype == MOE_BF16 ? 8 : 4);
+  const int most = dtype == MOE_BF16 ? 4 : 6, pieces = H / (dtype == MOE_BF16 ? 8 : 4);
   if (pieces <= 16) return {16, 1};
-  if (pieces <= 64) return {64, 1};
-  if (pieces <= 128) return {64, 2};
-  if (pieces <= 256) return {64, 4};
-  if (pieces <= 512) return {256, 2};
-  if (pieces <= 1024) return {256, 4};
-  return {0, 0};
+  const int tpr = pieces <= 64 * most ? 64 : 256, nv = (pieces + tpr - 1) / tpr;
+  if (nv > most) return {0, 0};
+  return {tpr, nv};
 }
 
-// Workgroups that keep column sums: two to a CU.
+// Workgroups that keep column sums: 8 waves to a CU.
 inline int sum_blocks(int T, int H, int dtype) {
   const Shape s = shape_of(H, dtype);
-  const int rows = s.tpr ? threads_of(s.tpr) / s.tpr : 1;
-  return std::max(1, std::min((T + rows - 1) / rows, 2 * cu_count()));
+  const int rows = s.tpr ? back_threads_of(s.tpr) / s.tpr : 1;
+  return std::max(1, std::min((T + rows - 1) / rows, s.tpr && s.tpr < 256 ? cu_count() : 2 * cu_count()));
 }
 
 inline int check(int T, int H, int kind, int dtype) {
@@ -420,18 +462,32 @@ void launch(const Forward& a, hipStream_t s) {
 }
 template <typename D, int TPR, int NV>
 void launch(const Backward& a, hipStream_t s, int blocks) {
-  hipLaunchKernelGGL((norm_backward_kernel<D, TPR, NV>), dim3(blocks), dim3(threads_of(TPR)), 0, s,
-                     a);
+  const dim3 block(back_threads_of(TPR));
+  if (a.dbias)
+    hipLaunchKernelGGL((norm_backward_kernel<D, TPR, NV, true>), dim3(blocks), block, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_backward_kernel<D, TPR, NV, false>), dim3(blocks), block, 0, s, a);
+}
+
+template <typename D, int TPR, typename A, typename... Rest>
+void launch_pieces(int nv, const A& a, Rest... rest) {
+  switch (nv) {
+    case 1: return launch<D, TPR, 1>(a, rest...);
+    case 2: return launch<D, TPR, 2>(a, rest...);
+    case 3: return launch<D, TPR, 3>(a, rest...);
+    case 4: return launch<D, TPR, 4>(a, rest...);
+  }
+  if constexpr (D::V == 4) {
+    if (nv == 5) launch<D, TPR, 5>(a, rest...);
+    else launch<D, TPR, 6>(a, rest...);
+  }
 }
 
 template <typename D, typename A, typename... Rest>
 void launch_shape(Shape p, const A& a, Rest... rest) {
   if (p.tpr == 16) launch<D, 16, 1>(a, rest...);
-  else if (p.tpr == 64 && p.nv == 1) launch<D, 64, 1>(a, rest...);
-  else if (p.tpr == 64 && p.nv == 2) launch<D, 64, 2>(a, rest...);
-  else if (p.tpr == 64) launch<D, 64, 4>(a, rest...);
-  else if (p.nv == 2) launch<D, 256, 2>(a, rest...);
-  else launch<D, 256, 4>(a, rest...);
+  else if (p.tpr == 64) launch_pieces<D, 64>(p.nv, a, rest...);
+  else launch_pieces<D, 256>(p.nv, a, rest...);
 }
 
 template <typename D>

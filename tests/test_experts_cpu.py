@@ -126,11 +126,11 @@ def _table(lib, grads, outs, counts, types):
 
 
 def test_clip_table(lib):
-    """Blocks of 64 KB from the address rounded down to 16 bytes; empty tensors have none."""
+    """Blocks of 16 KB from the address rounded down to 16 bytes; empty tensors have none."""
     a, b, c = 0x100000, 0x900002, 0xF00000
-    rc, t, blocks = _table(lib, [a, b, None, c], [a, b + 0x100000, None, c], [32769, 32768, 0, 1], [F32, BF16, F32, BF16])
+    rc, t, blocks = _table(lib, [a, b, None, c], [a, b + 0x100000, None, c], [8193, 8192, 0, 1], [F32, BF16, F32, BF16])
     assert rc == OK
-    assert t[0:4] == [a, a, 0 * 2 + 0, 32769] and t[4:8] == [b, b + 0x100000, 3 * 2 + 1, 32768]
+    assert t[0:4] == [a, a, 0 * 2 + 0, 8193] and t[4:8] == [b, b + 0x100000, 3 * 2 + 1, 8192]
     assert t[8:12] == [0, 0, 5 * 2, 0] and t[12:16] == [c, c, 5 * 2 + 1, 1]
     assert t[16:20] == [0, 0, 6 * 2, 0] and blocks == 6
 

@@ -61,19 +61,66 @@ def _check_scratch(src: str, remarks: str) -> None:
                                "counted waits need every value in registers")
 
 
+def _scalars(operand: str) -> set:
+    m = re.fullmatch(r"s(?:(\d+)|\[(\d+):(\d+)\])", operand)
+    if not m:
+        return set()
+    return {int(m[1])} if m[1] else set(range(int(m[2]), int(m[3]) + 1))
+
+
+def _check_hazards(src: str, assembly: str) -> None:
+    """The direct-to-LDS loads are inline assembly, for which the compiler does
+    not keep the five wait states between a vector instruction that writes a
+    scalar register and a load that reads it: a load closer than that may use a
+    stale address."""
+    kernel, loads, recent = "", 0, []
+    for line in assembly.splitlines():
+        if re.match(r"_Z\w+:", line):
+            kernel, recent = line.split(":")[0], []
+        text = line.split(";")[0].strip()
+        if not text or text.startswith(".") or text.endswith(":"):
+            continue
+        op, _, rest = text.partition(" ")
+        args = [a.strip() for a in rest.split(",")]
+        if op.startswith("buffer_load") and text.endswith(" lds"):
+            loads += 1
+            used = set().union(*(_scalars(w) for a in args for w in a.split()))
+            away = 0
+            for wrote, states, what in reversed(recent):
+                if away < 5 and wrote & used:
+                    raise RuntimeError(f"{src}: {kernel}: {text!r} reads what {what!r} writes {away} wait "
+                                       "states before it")
+                away += states
+        wrote = set()
+        if op.startswith(("v_readfirstlane", "v_readlane")):
+            wrote = _scalars(args[0])
+        elif op.startswith(("v_cmp", "v_div_scale", "v_mad_u64", "v_mad_i64")) or "_co_" in op:
+            wrote = set().union(*(_scalars(a) for a in args[:2]))
+        recent = recent[-5:] + [(wrote, int(args[0], 0) + 1 if op == "s_nop" else 1, text)]
+    if not loads:
+        raise RuntimeError(f"{src}: no direct-to-LDS load in its assembly, so their hazards are not known")
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
-        report = ["-Rpass-analysis=kernel-resource-usage"] if src in COUNTED else []
+        report = ["-Rpass-analysis=kernel-resource-usage", "-save-temps=obj"] if src in COUNTED else []
         cmd = [cc, *_flags(src), *report, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")
         if report:
+            stem = src.replace(".hip", "-hip-")
+            with open(os.path.join(BUILD, f"{stem}amdgcn-amd-amdhsa-{ARCH}.s")) as f:
+                assembly = f.read()
+            for name in os.listdir(BUILD):  # the other intermediate files with it
+                if name.startswith((stem, src.replace(".hip", "-host-"), src + "-")):
+                    os.remove(os.path.join(BUILD, name))
             _check_scratch(src, r.stderr)
+            _check_hazards(src, assembly)
         if verbose and r.stderr.strip():
             print(r.stderr, file=sys.stderr)
         return obj

@@ -10,30 +10,69 @@
 #include "grouped_f32.h"
 #include "grouped_mma.h"
 #include "grouped_plan.h"
+#include "grouped_stream.h"
 #include "linear_common.h"
 
 namespace moe {
 namespace grp {
 
 // dz of the rows that the experts have, rounded to the element type: 16 bytes of
-// dy's columns per thread.
+// dy's columns per thread; bound by HBM (65536 x 768 swiglu: 89 us, 5.6 TB/s).
 template <typename D>
-__global__ __launch_bounds__(256) void act_grad_kernel(const typename D::elem* __restrict__ dy,
-                                                       const typename D::elem* __restrict__ z,
-                                                       Groups g, int O, int act,
-                                                       typename D::elem* __restrict__ dz) {
+__device__ __forceinline__ void act_grad_rows(const typename D::elem* dy, const typename D::elem* z,
+                                              const Groups& g, int O, int act, typename D::elem* dz,
+                                              unsigned block, unsigned blocks) {
   constexpr int V = D::V;
   const unsigned cols = O / V;
   const size_t M = max(0, min(g.offsets[g.N], g.R));
-  const size_t n = M * cols, step = gridDim.x * static_cast<size_t>(256);
+  const size_t n = M * cols, step = blocks * static_cast<size_t>(256);
   const bool glu = act == MOE_ACT_SWIGLU;
-  for (size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; i < n; i += step) {
+  for (size_t i = block * static_cast<size_t>(256) + threadIdx.x; i < n; i += step) {
     const size_t t = i / cols, o = (i - t * cols) * V;
     const size_t zr = t * (glu ? 2 * static_cast<size_t>(O) : O) + o;
     float d[V], up[V];
     act_grad<typename D::elem, V>(dy + i * V, z + zr, O, act, d, up);
     store_v<V>(dz + zr, d);
     if (glu) store_v<V>(dz + zr + O, up);
+  }
+}
+
+// The rows of x in the experts' order, for the reduction over them: a gather
+// inside the product, along the axis that it reduces, cost it 20 to 37 % (8192
+// tokens, 128 experts, 1536 x 2048: 743 us for 543), this copy 50 us beside the
+// activation gradient.
+struct Gathered {
+  const uint16_t* x;
+  const int32_t* token;
+  uint16_t* rows;
+  int K;
+};
+__device__ __forceinline__ void gather_rows(const Gathered& a, const Groups& g, unsigned block,
+                                            unsigned blocks) {
+  const unsigned cols = a.K / 8;
+  const size_t M = max(0, min(g.offsets[g.N], g.R));
+  const size_t n = M * cols, step = blocks * static_cast<size_t>(256);
+  for (size_t i = block * static_cast<size_t>(256) + threadIdx.x; i < n; i += step) {
+    const size_t r = i / cols, c = i - r * cols;
+    reinterpret_cast<u32x4*>(a.rows)[i] =
+        *reinterpret_cast<const u32x4*>(a.x + static_cast<size_t>(a.token[r]) * a.K + c * 8);
+  }
+}
+
+// What the products read: the plan of the streaming ones, by the first workgroup,
+// dz, by the next `own`, and the gathered rows, by the others.
+template <typename D>
+__global__ __launch_bounds__(256) void prepare_kernel(const typename D::elem* dy,
+                                                      const typename D::elem* z, Groups g, int O,
+                                                      int act, typename D::elem* dz, unsigned own,
+                                                      Gathered a, Plan* plan) {
+  const unsigned block = blockIdx.x - 1;
+  if (blockIdx.x == 0) {
+    if (plan) make_plan(g, plan);
+  } else if (block < own) {
+    act_grad_rows<D>(dy, z, g, O, act, dz, block, own);
+  } else {
+    gather_rows(a, g, block - own, gridDim.x - 1 - own);
   }
 }
 
@@ -70,16 +109,28 @@ int launch_mma(const Prod& p, hipStream_t s) {
                                : max_row_tiles(p.g.R, p.g.N, BM);
   const long tiles = rows * ((N + NC - 1) / NC);
   if (tiles > (1 << 23)) return MOE_EUNSUP;  // the outputs alone would not fit the card
-  // DW: workgroups that stay; a short list may fall unevenly on the XCDs
-  const long wgs = MODE == DW ? std::min<long>(WGS * cu_count(), 2 * tiles) : tiles;
-  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>((wgs + 7) / 8 * 8)), dim3(lin::W * MOE_WAVE), lds,
+  hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(lin::W * MOE_WAVE), lds,
                      s, p);
   return MOE_OK;
 }
 
+inline int launch_stream(const Prod& p, Plan* plan, hipStream_t s) {
+  static std::atomic<bool> done[64];
+  if (!allow_lds(reinterpret_cast<const void*>(grouped_stream_mma_kernel), ST_LDS, done)) return MOE_EHIP;
+  hipLaunchKernelGGL(grouped_stream_mma_kernel, dim3((cu_count() + 7) / 8 * 8), dim3(lin::W * MOE_WAVE),
+                     ST_LDS, s, p, plan);
+  return MOE_OK;
+}
+
+inline bool streams(const Prod& p) {
+  return tile_choice(DW, p.g.R, p.g.N, p.W, p.K, cu_count()) == STREAM;
+}
+
+// plan: of the streaming product
 template <int MODE, bool GLU, bool GATHER>
-int launch_tile(const Prod& p, hipStream_t s) {
+int launch_tile(const Prod& p, Plan* plan, hipStream_t s) {
   switch (tile_choice(MODE, p.g.R, p.g.N, p.W, p.K, cu_count())) {
+    case STREAM: return launch_stream(p, plan, s);
     case TILE_256: return launch_mma<MODE, 256, 256, 64, 2, 1, GLU, GATHER>(p, s);
     case TILE_128x256:
       if constexpr (MODE == DX) return launch_mma<MODE, 128, 256, 32, 3, 2, GLU, GATHER>(p, s);
@@ -88,10 +139,10 @@ int launch_tile(const Prod& p, hipStream_t s) {
 }
 
 template <int MODE, bool GLU>
-int launch_bf16(const Prod& p, hipStream_t s) {
-  if constexpr (MODE != DX)
-    if (p.token) return launch_tile<MODE, GLU, true>(p, s);
-  return launch_tile<MODE, GLU, false>(p, s);
+int launch_bf16(const Prod& p, Plan* plan, hipStream_t s) {
+  if constexpr (MODE == FWD)
+    if (p.token) return launch_tile<MODE, GLU, true>(p, plan, s);
+  return launch_tile<MODE, GLU, false>(p, plan, s);
 }
 
 template <int MODE>
@@ -129,14 +180,14 @@ int launch_f32(const Prod& p, hipStream_t s) {
 
 // Product of any type
 template <typename E, int MODE, bool GLU>
-int product(const Prod& p, hipStream_t s) {
-  if constexpr (sizeof(E) == 2) return launch_bf16<MODE, GLU>(p, s);
+int product(const Prod& p, Plan* plan, hipStream_t s) {
+  if constexpr (sizeof(E) == 2) return launch_bf16<MODE, GLU>(p, plan, s);
   else return launch_f32<MODE, GLU>(p, s);
 }
 
 // dx and dw (either may be absent: null y)
 template <typename E>
-int products(const Prod& x, const Prod& w, hipStream_t s) {
+int products(const Prod& x, const Prod& w, Plan* plan, hipStream_t s) {
   if (sizeof(E) == 4 && x.e.y && w.e.y) {
     const int cus = cu_count();
     const long dw0 = f32_tiles<DX>(x, false, 32), all = dw0 + f32_tiles<DW>(w, false, 32);
@@ -150,13 +201,20 @@ int products(const Prod& x, const Prod& w, hipStream_t s) {
       return MOE_OK;
     }
   }
-  int rc = x.e.y ? product<E, DX, false>(x, s) : MOE_OK;
-  if (w.e.y && rc == MOE_OK) rc = product<E, DW, false>(w, s);
+  int rc = x.e.y ? product<E, DX, false>(x, plan, s) : MOE_OK;
+  if (w.e.y && rc == MOE_OK) rc = product<E, DW, false>(w, plan, s);
   return rc;
 }
 
-inline size_t dz_bytes(int R, int O, int act, int dtype) {
-  return act == MOE_ACT_NONE ? 0 : static_cast<size_t>(R) * width(O, act) * elem_size(dtype);
+// The backward pass's workspace: dz, then (bf16) the rows of x, then the plan.
+struct BackSpace {
+  size_t rows, plan, bytes;
+};
+inline BackSpace back_space(int R, int K, int O, int act, int dtype) {
+  const size_t el = elem_size(dtype);
+  const size_t dz = act == MOE_ACT_NONE ? 0 : (R * (width(O, act) * el) + 255) / 256 * 256;
+  const size_t rows = dtype == MOE_BF16 ? (static_cast<size_t>(R) * K * el + 255) / 256 * 256 : 0;
+  return {dz, dz + rows, dz + rows + sizeof(Plan)};
 }
 
 template <typename D>
@@ -171,19 +229,29 @@ int backward(const void* dy, const void* x, const int32_t* row_token, const Grou
     hipLaunchKernelGGL(zero_kernel<E>, grid_of(n), dim3(256), 0, s, static_cast<E*>(dw), n);
     return launch_status();
   }
-  const void* dz = dy;
-  if (act != MOE_ACT_NONE) {
-    dz = ws;
-    const size_t chunks = static_cast<size_t>(g.R) * (O / D::V);
-    hipLaunchKernelGGL(act_grad_kernel<D>, grid_of(chunks), dim3(256), 0, s,
-                       static_cast<const E*>(dy), static_cast<const E*>(z), g, O, act,
-                       static_cast<E*>(ws));
+  char* space = static_cast<char*>(ws);
+  const void* dz = act == MOE_ACT_NONE ? dy : ws;
+  const BackSpace b = back_space(g.R, K, O, act, sizeof(E) == 2 ? MOE_BF16 : MOE_F32);
+  Gathered a{};
+  if (sizeof(E) == 2 && row_token && dw) {
+    a = Gathered{static_cast<const uint16_t*>(x), row_token, reinterpret_cast<uint16_t*>(space + b.rows), K};
+    x = a.rows;
+    row_token = nullptr;
   }
   Prod px{dz, w, nullptr, 0, g, W, K, Epilogue{}};
   Prod pw{dz, x, row_token, static_cast<size_t>(T), g, W, K, Epilogue{}};
   px.e.y = dx;
   pw.e.y = dw;
-  const int rc = products<E>(px, pw, s);
+  Plan* plan = nullptr;
+  if (sizeof(E) == 2 && dw && streams(pw))
+    plan = reinterpret_cast<Plan*>(space + b.plan);
+  const unsigned own = act == MOE_ACT_NONE ? 0 : grid_of(static_cast<size_t>(g.R) * (O / D::V)).x;
+  const unsigned copy = a.rows ? grid_of(static_cast<size_t>(g.R) * (K / 8)).x : 0;
+  if (own + copy || plan)
+    hipLaunchKernelGGL(prepare_kernel<D>, dim3(1 + own + copy), dim3(256), 0, s,
+                       static_cast<const E*>(dy), static_cast<const E*>(z), g, O, act,
+                       static_cast<E*>(ws), own, a, plan);
+  const int rc = products<E>(px, pw, plan, s);
   return rc == MOE_OK ? launch_status() : rc;
 }
 
@@ -215,15 +283,15 @@ extern "C" int moe_grouped_linear(const void* x, const int32_t* row_token,
                Epilogue{nullptr, nullptr, z, y, act}};
   const bool glu = act == MOE_ACT_SWIGLU;
   rc = dtype == MOE_BF16
-           ? (glu ? product<uint16_t, FWD, true>(p, s) : product<uint16_t, FWD, false>(p, s))
-           : (glu ? product<float, FWD, true>(p, s) : product<float, FWD, false>(p, s));
+           ? (glu ? product<uint16_t, FWD, true>(p, nullptr, s) : product<uint16_t, FWD, false>(p, nullptr, s))
+           : (glu ? product<float, FWD, true>(p, nullptr, s) : product<float, FWD, false>(p, nullptr, s));
   return rc == MOE_OK ? launch_status() : rc;
 }
 
 extern "C" size_t moe_grouped_linear_backward_workspace_size(int R, int N, int K, int O, int act,
                                                              int dtype) {
   if (check(R, N, K, O, act, dtype) != MOE_OK) return 0;
-  return dz_bytes(R, O, act, dtype) + 256;
+  return back_space(R, K, O, act, dtype).bytes;
 }
 
 extern "C" int moe_grouped_linear_backward(const void* dy, const void* x, const int32_t* row_token,

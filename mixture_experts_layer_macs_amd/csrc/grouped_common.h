@@ -91,50 +91,14 @@ __device__ __forceinline__ bool data_tile(const Groups& g, int height, int cols,
   return true;
 }
 
-// The tiles of all experts' weight gradients, `tiles` for each expert, that one of
-// the 8 XCDs works on: contiguous ranges of equal cost, where a tile costs its
-// expert's rows and TILE_ROWS more for its start and output (256 x 256 tiles:
-// 9.4 us beside 1.42 us for 64 rows).  Equal numbers of tiles instead leave the
-// XCD with the popular experts 13 to 20 % longer at work than the mean.
-constexpr int TILE_ROWS = 448;
-
-struct Range {
-  int first, end;
-};
-
-__device__ __forceinline__ Range weight_tiles(const Groups& g, int tiles, int xcd) {
-  const int lane = lane_id();
-  int total = 0;
-  for (int e = lane; e < g.N; e += MOE_WAVE) {
-    const Span s = span_of(g, e);
-    total += s.hi - s.lo + TILE_ROWS;
-  }
-  total = wave_sum(total);
-  int r[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    // the first tile that starts at or behind share xcd + k of the cost
-    const int64_t share = static_cast<int64_t>(total) * (xcd + k) / 8;
-    const int64_t bound = static_cast<int64_t>(total) * tiles * (xcd + k) / 8;
-    r[k] = g.N * tiles;
-    int before = 0;
-    for (int e0 = 0; e0 < g.N && xcd + k < 8; e0 += MOE_WAVE) {
-      const int e = e0 + lane;
-      const Span s = span_of(g, min(e, g.N - 1));
-      const int cost = e < g.N ? s.hi - s.lo + TILE_ROWS : 0;
-      const int incl = before + wave_incl_scan(cost);
-      const uint64_t past = __ballot(e < g.N && incl > share);
-      if (past) {
-        const int l = __builtin_ctzll(past);
-        const int c = read_lane(cost, l), start = read_lane(incl, l) - c;
-        const int64_t left = bound - static_cast<int64_t>(start) * tiles;
-        r[k] = (e0 + l) * tiles + static_cast<int>((left + c - 1) / c);
-        break;
-      }
-      before = read_lane(incl, MOE_WAVE - 1);
-    }
-  }
-  return {r[0], r[1]};
+// Tile of a weight gradient.
+__device__ __forceinline__ bool weight_tile(int N, int rows, int cols, int block, int& e, int& mt,
+                                            int& nt) {
+  const int at = place_of(block, N * rows * cols);
+  if (at < 0) return false;
+  e = at / (rows * cols);
+  banded(at - e * rows * cols, rows, cols, mt, nt);
+  return true;
 }
 
 // Most row tiles that R rows in N groups can make.

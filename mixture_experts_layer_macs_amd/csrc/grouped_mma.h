@@ -5,7 +5,7 @@
 //   FWD  y_r = act(W_e x_t)      rows of x, gathered, by W_e's rows
 //   DX   dx_r = dz_r W_e         rows of dz by W_e's columns
 //   DW   dW_e = sum dz_r x_t^T   reduction over the expert's rows, both operands
-//                                reduction-strided, x gathered along it
+//                                reduction-strided, x laid out by rows beforehand
 #pragma once
 
 #include <type_traits>
@@ -23,7 +23,7 @@ constexpr int UNIT = 64;  // rows
 
 struct Prod {
   const void *r, *c;     // FWD: x, w; DX: dz, w; DW: dz, x
-  const int32_t* token;  // of the gathered operand (x); null: x holds the rows
+  const int32_t* token;  // of the gathered operand (x); null: x holds the rows (DW in bf16: always)
   size_t x_rows;         // rows of x
   Groups g;
   int W, K;              // rows (GLU: gate and up) and columns of an expert's weights
@@ -47,69 +47,6 @@ struct GatherRows : Operand<false, false, EXT, lin::W, SL> {
       if (q < 2) this->first[q] = ch * 8;
       this->voff[q] = row < valid ? static_cast<uint32_t>(token[row]) * row_bytes + ch * 16 : OOB_OFF;
     }
-  }
-};
-
-// The reduction-strided operand whose k are the rows of a token list.  A wave's
-// loads of a slice are consecutive k.  The list lies in vector registers, 64
-// tokens each, 64 CHUNKS tokens at a time; a load reads its rows' tokens from the
-// lanes that hold them, between the MFMAs.  (Tokens loaded by the scalar unit a
-// slice ahead cost 6 to 13 % of the product: a wait for the LDS fragments is
-// then a wait for them too.)
-template <int EXT, int SL>
-struct GatherStrided {
-  typedef Operand<true, false, EXT, lin::W, SL> Base;
-  static constexpr int BYTES = Base::BYTES, Q = Base::Q, CPR = EXT / 8, PER = 64 / CPR;
-  static constexpr int CHUNKS = 16;
-  static_assert(64 % CPR == 0 && PER * Q * lin::W == SL, "whole rows of every load");
-  i32x4 rsrc;
-  uint32_t step, first;  // bytes of a row of x, of the tile's first column
-  uint32_t voff[4];      // the lane's chunk in loads q, q + 4, ..: the swizzle repeats every 4 rows
-  const int32_t* token;
-  int last, lane;        // last entry of the list
-  typedef uint32_t u32x16 __attribute__((ext_vector_type(CHUNKS)));
-  u32x16 list;
-  uint32_t now;          // the slice's
-  int run;               // which 64 CHUNKS tokens the list is of
-
-  __device__ __forceinline__ void init(const uint16_t* x, int n0, size_t ld, size_t x_rows,
-                                       const int32_t* tok, int tokens, int valid, int lane_) {
-    lane = lane_;
-    step = static_cast<uint32_t>(ld) * 2;
-    first = static_cast<uint32_t>(n0) * 2;
-    rsrc = buffer_rsrc(x, static_cast<uint32_t>(x_rows * step));
-    token = tok;
-    last = tokens - 1;
-    run = -1;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int ch = lane % CPR ^ Base::swizzle(q * PER + lane / CPR);
-      voff[q] = ch * 8 < valid ? first + ch * 16 : OOB_OFF;
-    }
-  }
-  __device__ __forceinline__ void fetch(int k0) {
-    const int at = k0 / 64;
-    if (at / CHUNKS != run) {
-      run = at / CHUNKS;
-#pragma unroll
-      for (int i = 0; i < CHUNKS; ++i)
-        list[i] = static_cast<uint32_t>(token[min((run * CHUNKS + i) * 64 + lane, last)]);
-    }
-    now = list[at % CHUNKS];
-  }
-  __device__ __forceinline__ void load(int q, int k0, int kend, uint32_t lds, int wave) const {
-    uint32_t row = OOB_OFF;
-#pragma unroll
-    for (int s = 0; s < PER; ++s) {
-      const int k = wave * (PER * Q) + q * PER + s;
-      const uint32_t t =
-          static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(now), k0 % 64 + k));
-      const uint32_t off = k0 + k < kend ? t * step : OOB_OFF;
-      row = s == 0 || lane / CPR == s ? off : row;
-    }
-    const uint32_t v = voff[q % 4];
-    // either may be OOB_OFF; both would add up to a valid offset
-    lds_dma16(rsrc, row == OOB_OFF ? OOB_OFF : row + v, 0, lds + (wave * Q + q) * 1024);
   }
 };
 
@@ -155,47 +92,33 @@ __device__ __forceinline__ void data_product(const Prod& p, int block, unsigned 
   else run(std::integral_constant<int, 4>());
 }
 
-// DW: the tiles of this workgroup, every (workgroups of the XCD)-th of its range.
-template <int BM, int BN, int SL, int RA, bool GATHER>
-__device__ __forceinline__ void weight_product(const Prod& p, unsigned char* smem) {
+template <int BM, int BN, int SL, int RA>
+__device__ __forceinline__ void weight_product(const Prod& p, int block, unsigned char* smem) {
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
-  const int tm = (p.W + BM - 1) / BM, tn = (p.K + BN - 1) / BN;
-  const Range range = weight_tiles(p.g, tm * tn, blockIdx.x % 8);
-  for (int at = range.first + blockIdx.x / 8; at < range.end; at += gridDim.x / 8) {
-    const int e = at / (tm * tn);
-    int mt, nt;
-    banded(at - e * tm * tn, tm, tn, mt, nt);
-    const Span s = span_of(p.g, e);
-    const int n0 = nt * BN, m0 = mt * BM, lo = s.lo, count = s.hi - s.lo;
-    const int rows = min(BM, p.W - m0), width = min(BN, p.K - n0);
-    uint16_t* out = static_cast<uint16_t*>(p.e.y) + static_cast<size_t>(e) * p.W * p.K;
-    if (count == 0) {  // no rows: zeros
-      for (int i = threadIdx.x; i < rows * (BN / 8); i += lin::W * MOE_WAVE) {
-        const int r = i / (BN / 8), c = i % (BN / 8) * 8;
-        if (c < width)
-          *reinterpret_cast<u32x4*>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c) = u32x4{0, 0, 0, 0};
-      }
-      continue;
+  int e, mt, nt;
+  if (!weight_tile(p.g.N, (p.W + BM - 1) / BM, (p.K + BN - 1) / BN, block, e, mt, nt)) return;
+  const Span s = span_of(p.g, e);
+  const int n0 = nt * BN, m0 = mt * BM, lo = s.lo, count = s.hi - s.lo;
+  const int rows = min(BM, p.W - m0), width = min(BN, p.K - n0);
+  uint16_t* out = static_cast<uint16_t*>(p.e.y) + static_cast<size_t>(e) * p.W * p.K;
+  if (count == 0) {  // no rows: zeros
+    for (int i = threadIdx.x; i < rows * (BN / 8); i += lin::W * MOE_WAVE) {
+      const int r = i / (BN / 8), c = i % (BN / 8) * 8;
+      if (c < width)
+        *reinterpret_cast<u32x4*>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c) = u32x4{0, 0, 0, 0};
     }
-    Operand<true, false, BM, lin::W, SL> row;
-    row.init(static_cast<const uint16_t*>(p.r) + static_cast<size_t>(lo) * p.W + m0, p.W, rows, wave,
-             lane);
-    auto chunk = [&](int r, int c, float* g, float*) {
-      if (r < rows && c < width) store_v<8>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c, g);
-    };
-    const uint16_t* x = static_cast<const uint16_t*>(p.c);
-    if constexpr (GATHER) {
-      GatherStrided<BN, SL> col;
-      col.init(x, n0, p.K, p.x_rows, p.token + lo, p.g.R - lo, width, lane);
-      mma_core<true, true, BM, BN, false, 8, SL, RA>(row, col, 0, count, smem, chunk);
-    } else {
-      Operand<true, false, BN, lin::W, SL> col;
-      col.init(x + static_cast<size_t>(lo) * p.K + n0, p.K, width, wave, lane);
-      mma_core<true, true, BM, BN, false, 8, SL, RA>(row, col, 0, count, smem, chunk);
-    }
-    __syncthreads();  // the next tile's ring takes the place of this one's output
+    return;
   }
+  Operand<true, false, BM, lin::W, SL> row;
+  row.init(static_cast<const uint16_t*>(p.r) + static_cast<size_t>(lo) * p.W + m0, p.W, rows, wave,
+           lane);
+  Operand<true, false, BN, lin::W, SL> col;
+  col.init(static_cast<const uint16_t*>(p.c) + static_cast<size_t>(lo) * p.K + n0, p.K, width, wave,
+           lane);
+  mma_core<true, true, BM, BN, false, 8, SL, RA>(row, col, 0, count, smem, [&](int r, int c, float* g, float*) {
+    if (r < rows && c < width) store_v<8>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c, g);
+  });
 }
 
 // RA: ring stages of the row operand.
@@ -203,7 +126,7 @@ template <int MODE, int BM, int BN, int SL, int RA, int WGS, bool GLU, bool GATH
 __global__ __launch_bounds__(lin::W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(WGS, WGS)))
 void grouped_mma_kernel(Prod p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  if constexpr (MODE == DW) weight_product<BM, BN, SL, RA, GATHER>(p, smem);
+  if constexpr (MODE == DW) weight_product<BM, BN, SL, RA>(p, blockIdx.x, smem);
   else data_product<MODE, BM, BN, SL, RA, GLU, GATHER>(p, blockIdx.x, smem);
 }
 

@@ -13,33 +13,39 @@ namespace grp {
 enum { FWD, DX, DW };
 
 // Tiles of the bf16 products
-enum { TILE_256, TILE_128, TILE_128x256 };
+enum { TILE_256, TILE_128, TILE_128x256, STREAM };
+
+constexpr int STREAM_EXPERTS = 512;  // most that the streaming kernel's plan holds
 
 inline double rounds(double tiles, int cus) { return std::ceil(tiles / cus); }
 
-// rows, W, K: of a product as in Prod; cols: output columns (FWD with a gated
-// activation: of W).  Times in us, from sweeps of 64 .. 1024 rows per expert, 128
-// experts, weights of 512^2 .. 4096^2: a slice of 64 k takes a 256 x 256 tile 1.55
-// (the matrix pipe at its power limit), a 128 x 128 tile 0.43, on top of 14 (8 for
-// a weight gradient, whose workgroups stay) and 4.
-//   64 rows, 1536 x 2048:  dw 257 with 256 x 256 tiles, 274 with 128 x 128;
-//     dx 165, 170, and 150 with 128 x 256 tiles and slices of 32: it is the weights
-//     that are read, 5.4 TB/s, by two workgroups a CU
-//   512 rows:  dw 518 and 642, dx 432 and 523 (481), forward 374 and 429
+// rows, W, K: of a product as in Prod (FWD with a gated activation: gate and up).
+// Times in us, from sweeps of 64 .. 1024 rows per expert, 128 experts, weights of
+// 512^2 .. 4096^2: a slice of 64 k takes a 256 x 256 tile 1.55 (the matrix pipe at
+// its power limit) on top of 14 (10 for a weight gradient), a 128 x 128 tile, two to
+// a CU, 0.57 on top of 2.  128 experts of 1536 x 2048:
+//   64 rows   dx 165 with 256 x 256 tiles, 170 with 128 x 128, and 150 with 128 x
+//             256 and slices of 32: it is the weights that are read, 5.4 TB/s, by
+//             two workgroups a CU
+//             dw 200 streaming, 250 with 256 x 256 tiles, 274 with 128 x 128
+//   512 rows  dx 432, 523 and 481; dw 470, 530, 642; forward 374 and 429
+// The streaming weight gradient deals whole experts to the XCDs, which takes several
+// for each: with 8 experts it took 1.7 times as long as the tiles.
 inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
   const int used = std::min(N, R);  // experts that can have rows
   const double rows = static_cast<double>(R) / used;
   auto tiles = [&](int m, int n) {
-    const double a = mode == DW ? std::ceil(static_cast<double>(W) / m) : std::ceil(rows / m);
+    const double a = std::ceil((mode == DW ? W : rows) / m);
     const double b = std::ceil(static_cast<double>(mode == FWD ? W : K) / n);
     return (mode == DW ? N : used) * a * b;
   };
+  if (mode == DW && N >= 64 && N <= STREAM_EXPERTS && W > 128 && K > 128) return STREAM;
+  if (mode == DX && rows <= 128 && tiles(128, 256) >= cus) return TILE_128x256;
   const double slices = (mode == DW ? rows : mode == FWD ? K : W) / 64.0;
   const double height = mode == DW ? 1.0 : std::min(1.0, std::ceil(rows / 64) / 4);
   const double large = rounds(tiles(256, 256), cus) *
-                       (slices * std::max(0.4, 1.55 * height) + (mode == DW ? 8 : 14));
-  const double small = rounds(tiles(128, 128), cus) * (slices * 0.43 + 2) + 4;
-  if (mode == DX && rows <= 128 && tiles(128, 256) >= cus) return TILE_128x256;
+                       (slices * std::max(0.4, 1.55 * height) + (mode == DW ? 10 : 14));
+  const double small = rounds(tiles(128, 128), cus) * (slices * 0.57 + 2) + 4;
   return large <= small ? TILE_256 : TILE_128;
 }
 

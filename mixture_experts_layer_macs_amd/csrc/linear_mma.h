@@ -35,6 +35,22 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// A value that every lane has, in a scalar register from here on.  The vector
+// unit computes some of them (a division by a run-time number), and the compiler
+// then moves them where they are used; a load that reads a scalar register less
+// than five wait states behind the vector instruction that wrote it may see the
+// old value, and the compiler keeps that distance only for loads that it knows.
+// What an inline load's resource and offset are made of passes through here where
+// a kernel starts; the build looks for loads that come too close all the same.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  const uint64_t b = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(b));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(b >> 32));
+  return reinterpret_cast<T*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 constexpr int SLICE = 64;        // k per ring stage
 constexpr int SA = 2, SB = 3;    // stages of the row and the column operand
 constexpr int WM = 2, WN = 2, W = WM * WN;  // waves of a workgroup along M and N
@@ -64,9 +80,9 @@ struct Operand {
   static_assert(!(STRIDED && MIX), "gated weights are reduction-contiguous");
   uint32_t voff[Q];
   int first[2];  // contiguous: k of the lane's chunk in the slice, by load parity
-  i32x4 rsrc, rsrc_up;  // contiguous: the tile's rows (MIX: gate, up)
+  i32x4 rsrc, rsrc_up;  // contiguous: the tile's rows (MIX: gate, up); strided: the slice
   const char* base;
-  size_t step;   // strided: bytes of a k row
+  uint32_t step; // strided: bytes of a k row
   uint32_t tail; // strided: bytes from base to the end of a k row's used part
 
   // valid: rows from p (contiguous), or elements of a k row from p (strided);
@@ -88,14 +104,14 @@ struct Operand {
         voff[q] = at < valid ? static_cast<uint32_t>(at) * row_bytes + ch * 16 : OOB_OFF;
       }
     } else {
-      base = reinterpret_cast<const char*>(p);
-      step = ld * 2;
-      tail = static_cast<uint32_t>(valid) * 2;
+      base = uniform(reinterpret_cast<const char*>(p));
+      step = uniform(static_cast<int>(ld * 2));
+      tail = uniform(valid * 2);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         const int at = (wave * Q + q) * 64 + lane, row = at / CPR;
         const int ch = at % CPR ^ swizzle(row);
-        voff[q] = ch * 8 < valid ? static_cast<uint32_t>(row) * static_cast<uint32_t>(step) + ch * 16
+        voff[q] = ch * 8 < valid ? static_cast<uint32_t>(row) * step + ch * 16
                                  : OOB_OFF;
       }
     }
@@ -111,19 +127,21 @@ struct Operand {
   static __device__ __forceinline__ int swizzle(int k) {
     return EXT % 128 == 0 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
   }
-  // what the loads of the slice from k0 need to know beforehand: nothing here
-  __device__ __forceinline__ void fetch(int) {}
-  // load q of the slice from k0 (k up to kend) into the stage at lds
+  // before the loads of the slice from k0 (k up to kend)
+  __device__ __forceinline__ void fetch(int k0, int kend) {
+    if constexpr (STRIDED) {
+      const uint32_t rows = static_cast<uint32_t>(min(SL, kend - k0));
+      rsrc = buffer_rsrc(base + static_cast<size_t>(k0) * step, (rows - 1) * step + tail);
+    }
+  }
+  // load q of that slice into the stage at lds
   __device__ __forceinline__ void load(int q, int k0, int kend, uint32_t lds, int wave) const {
     if constexpr (!STRIDED) {
       lds_dma16(MIX && ((wave * Q + q) / (16 / RPL) & 1) ? rsrc_up : rsrc,
                 first[q & 1] < kend - k0 ? voff[q] : OOB_OFF, static_cast<uint32_t>(k0) * 2,
                 lds + (wave * Q + q) * 1024);
     } else {
-      const uint32_t rows = static_cast<uint32_t>(min(SL, kend - k0));
-      const i32x4 rs = buffer_rsrc(base + static_cast<size_t>(k0) * step,
-                                   (rows - 1) * static_cast<uint32_t>(step) + tail);
-      lds_dma16(rs, voff[q], 0, lds + (wave * Q + q) * 1024);
+      lds_dma16(rsrc, voff[q], 0, lds + (wave * Q + q) * 1024);
     }
   }
 };
@@ -228,8 +246,10 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
     col.load(q, k_lo + min(t, nk - 1) * SL, k_hi, lds_base + B_BASE + (t % SB) * Col::BYTES,
              wave);
   };
-  auto fetch_col = [&](int t) { col.fetch(k_lo + min(t, nk - 1) * SL); };
+  auto fetch_row = [&](int t) { row.fetch(k_lo + min(t, nk - 1) * SL, k_hi); };
+  auto fetch_col = [&](int t) { col.fetch(k_lo + min(t, nk - 1) * SL, k_hi); };
   auto load_rows = [&](int t) {
+    fetch_row(t);
 #pragma unroll
     for (int q = 0; q < Row::Q; ++q) load_row(t, q);
   };
@@ -308,6 +328,7 @@ __device__ __forceinline__ void mma_core(Row& row, Col& col, int k_lo, int k_hi,
     wait_vmcnt<(SA - 2) * Row::Q + (SB - 2) * Col::Q>();
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     fetch_col(t + SB);
+    fetch_row(t + SA);
     step(KK - 1, t + 1, Row::Q, [&](int q) { load_row(t + SA, q); });
   }
   wait_vmcnt<0>();  // no load may land after the workgroup ends

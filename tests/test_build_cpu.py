@@ -24,3 +24,26 @@ def test_scratch_check():
 def test_scratch_check_needs_a_kernel_to_look_at(remarks):
     with pytest.raises(RuntimeError, match="name no kernel"):
         build._check_scratch("linear.hip", remarks)
+
+
+ASM = """_ZN3moe3lin10mma_kernelEv:
+{write}
+{between}	buffer_load_dwordx4 v8, s[0:3], s22 offen lds
+"""
+
+
+@pytest.mark.parametrize("write", ["\tv_readfirstlane_b32 s2, v35", "\tv_readlane_b32 s22, v1, s5",
+                                   "\tv_cmp_lt_i32_e64 s[2:3], v1, v2", "\tv_mad_u64_u32 v[2:3], s[0:1], v1, v2, v[4:5]"])
+def test_hazard_check(write):
+    near = "".join(f"\tv_mov_b32 v{i}, 0\n.Lx:\n\t; a comment\n" for i in range(4))
+    with pytest.raises(RuntimeError, match="4 wait states"):
+        build._check_hazards("linear.hip", ASM.format(write=write, between=near))
+    build._check_hazards("linear.hip", ASM.format(write=write, between=near + "\ts_mov_b32 s40, 1\n"))
+    build._check_hazards("linear.hip", ASM.format(write=write, between="\ts_nop 4\n"))
+    build._check_hazards("linear.hip", ASM.format(write=write.replace("s2", "s42").replace("s[2:3]", "s[8:9]").replace(
+        "s[0:1]", "s[8:9]"), between=""))
+
+
+def test_hazard_check_needs_a_load_to_look_at():
+    with pytest.raises(RuntimeError, match="no direct-to-LDS load"):
+        build._check_hazards("linear.hip", "_Zx:\n\ts_endpgm\n")

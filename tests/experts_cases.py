@@ -1,0 +1,25 @@
+"""Sizes of the grouped products' tests: rows of each expert, rows behind the last
+expert's, K, O."""
+
+# no rows, one row, one expert with everything, empty experts at both ends, groups
+# around every tile edge, reductions that end inside a slice, more columns than a
+# tile; from 64 experts on the streaming weight gradient: reductions of one to many
+# slices in a row, several tiles to a workgroup, experts without rows, widths that
+# end inside a tile
+GROUPS = [
+    ([0, 0, 0], 5, 64, 32), ([1], 0, 8, 8), ([0, 1, 0], 3, 72, 24), ([1, 1, 1, 1, 1, 1, 1, 1], 0, 2048, 768),
+    ([3, 0, 7, 1], 2, 136, 264), ([15, 16, 17], 1, 520, 40), ([0, 0, 64, 0], 0, 64, 128), ([63, 65], 9, 200, 136),
+    ([127, 0, 129, 1], 4, 264, 72), ([300], 20, 328, 520), ([255, 257], 0, 72, 264), ([2] * 70, 3, 128, 64),
+    ([513, 3], 5, 136, 776), ([40, 0, 500, 260, 31], 100, 1032, 200), ([33] * 5 + [0] * 130 + [50], 7, 40, 72),
+    ([700, 20], 0, 64, 1544), ([900], 1, 264, 264),
+    ([1] * 64, 0, 136, 136), ([0] * 63 + [5], 2, 264, 136), ([0, 1, 64, 65, 129, 3, 200, 7] * 10, 11, 264, 136),
+    ([70, 2, 0, 128, 1, 63, 0, 300] * 9, 0, 520, 520), ([1300] + [1, 0] * 40, 5, 264, 264),
+    ([20] * 40, 0, 520, 1032),
+]
+
+# many full tiles, compared in some rows: experts below and above the tiles' heights
+LARGE = [
+    ([400 + 37 * i % 220 for i in range(33)], 50, 2056, 4104),
+    ([60 + 5 * i % 40 for i in range(64)], 0, 1032, 2056),
+    ([260 + 3 * i % 50 for i in range(16)], 9, 712, 1032),
+]

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import experts_ref as E
+from experts_cases import GROUPS, LARGE
 import training_ref as R
 from gpu_util import load_binding, needs_gpu
 
@@ -48,20 +49,8 @@ def _outside(buf, n, pad=64):
 
 
 # -------------------------------------------------------------------- grouped
-# rows of each expert, rows behind the last expert's, K, O: no rows, one row, one
-# expert with everything, empty experts at both ends, groups around every tile
-# edge, reductions that end inside a slice, more columns than a tile
-GROUPS = [
-    ([0, 0, 0], 5, 64, 32), ([1], 0, 8, 8), ([0, 1, 0], 3, 72, 24), ([1, 1, 1, 1, 1, 1, 1, 1], 0, 2048, 768),
-    ([3, 0, 7, 1], 2, 136, 264), ([15, 16, 17], 1, 520, 40), ([0, 0, 64, 0], 0, 64, 128), ([63, 65], 9, 200, 136),
-    ([127, 0, 129, 1], 4, 264, 72), ([300], 20, 328, 520), ([255, 257], 0, 72, 264), ([2] * 70, 3, 128, 64),
-    ([513, 3], 5, 136, 776), ([40, 0, 500, 260, 31], 100, 1032, 200), ([33] * 5 + [0] * 130 + [50], 7, 40, 72),
-    ([700, 20], 0, 64, 1544), ([900], 1, 264, 264),
-]
-
-
-def _grouped_inputs(i, act, dtype, gather, seed):
-    counts, behind, K, O = GROUPS[i]
+def _grouped_inputs(case, act, dtype, gather, seed):
+    counts, behind, K, O = case
     g = np.random.default_rng(seed)
     M = sum(counts)
     rows = M + behind
@@ -84,7 +73,7 @@ def test_grouped(B, i, dtype):
     for j in range(2):  # two of the activations with each size, all of them over the sizes
         act, gather, keep = ACTS[(i + 3 * j) % 5], (i + j) % 2 == 0, (i + j) % 3 != 0
         print(f"[gpu-test] grouped {GROUPS[i]} {act} {gather} {dtype}", flush=True)
-        g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(i, act, dtype, gather, 10 * i + j)
+        g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(GROUPS[i], act, dtype, gather, 10 * i + j)
         ws = B.new_workspace(B.moe_grouped_linear_workspace_size(rows, len(w), x.shape[1], O, act, dtype), "cuda")
         ybuf, y = _guard((rows, O), dtype)
         zbuf, z = _guard((rows, W), dtype)
@@ -106,7 +95,7 @@ def test_grouped_backward(B, i, dtype):
     for j in range(2):
         act, gather = ACTS[(i + 2 + 3 * j) % 5], (i + j) % 2 == 1
         print(f"[gpu-test] grouped backward {GROUPS[i]} {act} {gather} {dtype}", flush=True)
-        g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(i, act, dtype, gather, 10 * i + j)
+        g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(GROUPS[i], act, dtype, gather, 10 * i + j)
         K = x.shape[1]
         dy, z = _rand(g, (rows, O), 0.5, dtype), _rand(g, (rows, W), 1.0, dtype)
         dy[M:], z[M:] = float("nan"), float("nan")
@@ -125,6 +114,41 @@ def test_grouped_backward(B, i, dtype):
         B.moe_grouped_linear_backward(dy, None, w, off, ws, z=zz, act=act, dx=dx)
         # rows behind the experts' stay, so the whole buffers are equal
         assert torch.equal(first[0], dx) and torch.equal(first[1], dw)
+
+
+@pytest.mark.parametrize("i", range(len(LARGE)))
+@pytest.mark.parametrize("act,gather", [("none", False), ("swiglu", True)])
+@DTYPES
+def test_grouped_large_tiles(B, i, act, gather, dtype):
+    """Every row is computed; compared are the first, the last and some rows of each
+    expert (dw: rows of the weights of some experts)."""
+    counts, _, K, O = LARGE[i]
+    print(f"[gpu-test] grouped large {len(counts)} {K} {O} {act} {dtype}", flush=True)
+    g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(LARGE[i], act, dtype, gather, 100 + i)
+    N = len(counts)
+    at = sorted({int(r) for e in range(N) for r in (offsets[e], offsets[e + 1] - 1, *g.integers(offsets[e], offsets[e + 1], 2))})
+    few = np.searchsorted(at, offsets)  # offsets among the compared rows
+    dy, z = _rand(g, (rows, O), 0.5, dtype), torch.empty(rows, W, dtype=dtype, device="cuda")
+    dy[M:] = float("nan")
+    ws = B.new_workspace(max(B.moe_grouped_linear_workspace_size(rows, N, K, O, act, dtype),
+                             B.moe_grouped_linear_backward_workspace_size(rows, N, K, O, act, dtype)), "cuda")
+    y = B.moe_grouped_linear(x, w, off, ws, row_token=token, act=act, z=z)
+    xs, W64 = R.f64(x[at] if tok is None else x[tok[at]]), R.f64(w)
+    yr, zr, ey, ez = E.grouped(xs, None, few, W64, act, dtype)
+    _near(y[at], yr, ey, "y")
+    _near(z[at], zr, ez, "z")
+    dx, dw = torch.empty(rows, K, dtype=dtype, device="cuda"), torch.full_like(w, 7.0)
+    ws.fill_(0xFF)
+    B.moe_grouped_linear_backward(dy, x, w, off, ws, row_token=token, z=z, act=act, dx=dx, dw=dw)
+    r = E.grouped_backward(R.f64(dy[at]), xs, None, few, W64, R.f64(z[at]), act, dtype)
+    _near(dx[at], *r["dx"], "dx")
+    for e in (0, N // 2, N - 1):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        some = sorted({0, O - 1, *g.integers(0, O, 6)})  # columns of dy; gate and up rows of dw
+        pick = some + [O + c for c in some] if act == "swiglu" else some
+        xe = R.f64(x[lo:hi] if tok is None else x[tok[lo:hi]])
+        v = R.linear_backward(R.f64(dy[lo:hi][:, some]), xe, np.zeros((len(pick), K)), R.f64(z[lo:hi][:, pick]), act, dtype)
+        _near(dw[e][pick], *v["dw"], f"dw of expert {e}")
 
 
 @DTYPES

@@ -729,7 +729,7 @@ int moe_grouped_linear_backward(const void* dy, const void* x,
  * eps          finite, >= 0.  A row of variance 0 with eps == 0 gives NaN.
  * sum          [T,H] out: s; required with residual, unused and may be NULL
  *              without; may equal x or residual (in place).
- * y            [T,H] out; may equal x (in place) when nothing else reads it.
+ * y            [T,H] out; may equal x or residual (in place), not sum.
  * mean, rstd   f32[T] out, for moe_norm_backward; each may be NULL.
  * Statistics are fp32, the variance from the centred values.
  * Limits: 1 <= H <= MOE_LINEAR_MAX_DIM, a multiple of 8 (MOE_BF16) or 4
@@ -794,7 +794,8 @@ int moe_norm_backward(const void* dy, const void* s, const void* weight,
  *           no gradient of the type's range overflows.
  * Where the norm is at most max_norm, and where it is not finite (an
  * infinite or NaN gradient, for the caller to see in norm), the factor is 1: in
- * place nothing changes.  Workspace of moe_grad_clip_workspace_size() bytes, at
+ * place nothing changes.  (A finite norm beyond fp32's range shows as +inf in norm
+ * and scales all the same.)  Workspace of moe_grad_clip_workspace_size() bytes, at
  * a multiple of 16 bytes (scratch only).  n == 0 gives norm 0.
  */
 #define MOE_GRAD_TABLE_WORDS 4

@@ -126,11 +126,23 @@ inline bool streams(const Prod& p) {
   return tile_choice(DW, p.g.R, p.g.N, p.W, p.K, cu_count()) == STREAM;
 }
 
+template <bool GLU, bool GATHER>
+int launch_skinny(const Prod& p, hipStream_t s) {
+  constexpr int NC = GLU ? 8 : 16;
+  const int O = GLU ? p.W / 2 : p.W;
+  const long tiles = max_row_tiles(p.g.R, p.g.N, 16) * ((O + NC - 1) / NC);
+  hipLaunchKernelGGL((grouped_skinny_kernel<GLU, GATHER>), dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)),
+                     dim3(SK_WAVES * MOE_WAVE), 0, s, p);
+  return MOE_OK;
+}
+
 // plan: of the streaming product
 template <int MODE, bool GLU, bool GATHER>
 int launch_tile(const Prod& p, Plan* plan, hipStream_t s) {
   switch (tile_choice(MODE, p.g.R, p.g.N, p.W, p.K, cu_count())) {
     case STREAM: return launch_stream(p, plan, s);
+    case SKINNY:
+      if constexpr (MODE == FWD) return launch_skinny<GLU, GATHER>(p, s);
     case TILE_256: return launch_mma<MODE, 256, 256, 64, 2, 1, GLU, GATHER>(p, s);
     case TILE_128x256:
       if constexpr (MODE == DX) return launch_mma<MODE, 128, 256, 32, 3, 2, GLU, GATHER>(p, s);

@@ -13,6 +13,7 @@
 #include "grouped_common.h"
 #include "grouped_plan.h"
 #include "linear_mma.h"
+#include "linear_skinny.h"
 
 namespace moe {
 namespace grp {
@@ -128,6 +129,29 @@ void grouped_mma_kernel(Prod p) {
   extern __shared__ __align__(16) unsigned char smem[];
   if constexpr (MODE == DW) weight_product<BM, BN, SL, RA>(p, blockIdx.x, smem);
   else data_product<MODE, BM, BN, SL, RA, GLU, GATHER>(p, blockIdx.x, smem);
+}
+
+// FWD, a few rows to an expert: the dense layer's product for few tokens, 16 rows
+// and 16 weight rows (8 gate and 8 up) to a workgroup, whose weights go straight
+// to the MFMA registers.  Bound by HBM: one token, 8 experts of 1536 x 2048 (50 MB)
+// 11.8 us, 4.3 TB/s.
+template <bool GLU, bool GATHER>
+__global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void grouped_skinny_kernel(Prod p) {
+  constexpr int NC = GLU ? 8 : 16;
+  __shared__ float red[SK_WAVES][16][17];
+  const int O = GLU ? p.W / 2 : p.W;
+  int e, lo, hi, mt, nt;
+  if (!data_tile(p.g, 16, (O + NC - 1) / NC, blockIdx.x, e, lo, hi, mt, nt)) return;
+  Skinny q{};
+  q.x = static_cast<const uint16_t*>(p.r) + (GATHER ? 0 : static_cast<size_t>(lo) * p.K);
+  q.w = static_cast<const uint16_t*>(p.c) + static_cast<size_t>(e) * p.W * p.K;
+  q.T = hi - lo;
+  q.K = p.K;
+  q.O = O;
+  q.e = p.e;
+  q.e.y = static_cast<uint16_t*>(p.e.y) + static_cast<size_t>(lo) * O;
+  if (p.e.z) q.e.z = static_cast<uint16_t*>(p.e.z) + static_cast<size_t>(lo) * p.W;
+  skinny_tile<1, GLU, GATHER>(q, nt * NC, mt * 16, GATHER ? p.token + lo : nullptr, red);
 }
 
 }  // namespace grp

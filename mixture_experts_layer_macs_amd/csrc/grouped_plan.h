@@ -13,7 +13,7 @@ namespace grp {
 enum { FWD, DX, DW };
 
 // Tiles of the bf16 products
-enum { TILE_256, TILE_128, TILE_128x256, STREAM };
+enum { TILE_256, TILE_128, TILE_128x256, STREAM, SKINNY };
 
 constexpr int STREAM_EXPERTS = 512;  // most that the streaming kernel's plan holds
 
@@ -29,6 +29,9 @@ inline double rounds(double tiles, int cus) { return std::ceil(tiles / cus); }
 //             two workgroups a CU
 //             dw 200 streaming, 250 with 256 x 256 tiles, 274 with 128 x 128
 //   512 rows  dx 432, 523 and 481; dw 470, 530, 642; forward 374 and 429
+// Few rows: where the 128 x 128 tiles leave half the compute units without one, 16
+// weight rows to a workgroup: 8 experts with a row each 11.8 us, 16.1 with tiles
+// (768 x 2048 swiglu); 16 such experts 20.3 and 18.8, 2048 x 768 10.0 and 8.9.
 // The streaming weight gradient deals whole experts to the XCDs, which takes several
 // for each: with 8 experts it took 1.7 times as long as the tiles.
 inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
@@ -40,6 +43,7 @@ inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
     return (mode == DW ? N : used) * a * b;
   };
   if (mode == DW && N >= 64 && N <= STREAM_EXPERTS && W > 128 && K > 128) return STREAM;
+  if (mode == FWD && rows <= 16 && K >= 1024 && tiles(128, 128) * 2 < cus) return SKINNY;
   if (mode == DX && rows <= 128 && tiles(128, 256) >= cus) return TILE_128x256;
   const double slices = (mode == DW ? rows : mode == FWD ? K : W) / 64.0;
   const double height = mode == DW ? 1.0 : std::min(1.0, std::ceil(rows / 64) / 4);

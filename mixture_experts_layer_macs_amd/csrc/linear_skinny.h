@@ -30,17 +30,15 @@ struct Skinny {
 
 constexpr int SK_WAVES = 8, SK_BLOCK = 64;
 
-template <int RF, bool GLU>
-__global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
+// Rows t0 .. of x (LISTED: of the stored rows in `token`) and columns n0 .. of y;
+// red: the waves' sums.
+template <int RF, bool GLU, bool LISTED>
+__device__ __forceinline__ void skinny_tile(const Skinny& p, int n0, int t0, const int32_t* token,
+                                            float (*red)[RF * 16][17]) {
   constexpr int NC = GLU ? 8 : 16;              // columns of y per workgroup
   constexpr int AHEAD = RF >= 4 ? 1 : 4 / RF;   // blocks in flight per wave
-  __shared__ float red[SK_WAVES][RF * 16][17];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
-  const int total = p.panels * p.parts, per = (total + 7) / 8;
-  const int id = blockIdx.x % 8 * per + blockIdx.x / 8;
-  if (id >= total) return;
-  const int n0 = id / p.parts * NC, t0 = id % p.parts * RF * 16;
   const int r = lane & 15, k_lane = (lane >> 4) * 8;
   // rows past the end repeat the last one; their results are not stored
   const int wr = GLU ? (r < 8 ? min(n0 + r, p.O - 1) : p.O + min(n0 + r - 8, p.O - 1))
@@ -48,8 +46,10 @@ __global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
   const uint16_t* w = p.w + static_cast<size_t>(wr) * p.K + k_lane;
   const uint16_t* x[RF];
 #pragma unroll
-  for (int f = 0; f < RF; ++f)
-    x[f] = p.x + static_cast<size_t>(min(t0 + f * 16 + r, p.T - 1)) * p.K + k_lane;
+  for (int f = 0; f < RF; ++f) {
+    const int t = min(t0 + f * 16 + r, p.T - 1);
+    x[f] = p.x + static_cast<size_t>(LISTED ? token[t] : t) * p.K + k_lane;
+  }
   f32x4 acc[RF];
 #pragma unroll
   for (int f = 0; f < RF; ++f) acc[f] = f32x4{0, 0, 0, 0};
@@ -111,6 +111,15 @@ __global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
     }
     finish<uint16_t, GLU, 4>(p.e, t0 + t, n0 + c, p.O, g, u);
   }
+}
+
+template <int RF, bool GLU>
+__global__ __launch_bounds__(SK_WAVES* MOE_WAVE) void skinny_kernel(Skinny p) {
+  __shared__ float red[SK_WAVES][RF * 16][17];
+  const int total = p.panels * p.parts, per = (total + 7) / 8;
+  const int id = blockIdx.x % 8 * per + blockIdx.x / 8;
+  if (id >= total) return;
+  skinny_tile<RF, GLU, false>(p, id / p.parts * (GLU ? 8 : 16), id % p.parts * RF * 16, nullptr, red);
 }
 
 }  // namespace lin

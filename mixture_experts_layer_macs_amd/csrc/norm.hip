@@ -540,7 +540,7 @@ extern "C" int moe_norm(const void* x, const void* residual, const void* weight,
   if (rc != MOE_OK) return rc;
   if (!(eps >= 0.0 && eps <= 3.4e38)) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
-  if (!x || !weight || !y || (residual && !sum)) return MOE_EINVAL;
+  if (!x || !weight || !y || (residual && (!sum || sum == y))) return MOE_EINVAL;
   for (const void* q : {x, residual, weight, bias, static_cast<const void*>(sum),
                         static_cast<const void*>(y)})
     if (!aligned16(q)) return MOE_EINVAL;

@@ -82,10 +82,10 @@ def test_grouped_workspaces(lib):
     (dict(kind=2), EINVAL), (dict(kind=-1), EINVAL), (dict(dtype=2), EUNSUP), (dict(H=60), EUNSUP),
     (dict(H=62, dtype=F32), EUNSUP), (dict(eps=-1e-9), EINVAL), (dict(eps=float("nan")), EINVAL),
     (dict(eps=float("inf")), EINVAL), (dict(x=None), EINVAL), (dict(w=None), EINVAL), (dict(y=None), EINVAL),
-    (dict(sum=None), EINVAL), (dict(x=ODD), EINVAL), (dict(res=ODD), EINVAL), (dict(w=ODD), EINVAL),
+    (dict(sum=None), EINVAL), (dict(sum=A), EINVAL), (dict(x=ODD), EINVAL), (dict(res=ODD), EINVAL), (dict(w=ODD), EINVAL),
     (dict(b=ODD), EINVAL), (dict(sum=ODD), EINVAL), (dict(y=ODD), EINVAL), (dict(T=0, x=None, y=None), OK)])
 def test_norm_refusals(lib, kw, rc):
-    a = dict(x=A, res=A, w=A, b=A, T=4, H=64, kind=0, eps=1e-5, dtype=BF16, sum=A, y=A, mean=None, rstd=None)
+    a = dict(x=A, res=A, w=A, b=A, T=4, H=64, kind=0, eps=1e-5, dtype=BF16, sum=P(0x20000), y=A, mean=None, rstd=None)
     a.update(kw)
     assert lib.moe_norm(*a.values(), None) == rc
 

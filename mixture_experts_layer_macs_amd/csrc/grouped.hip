@@ -114,16 +114,18 @@ int launch_mma(const Prod& p, hipStream_t s) {
   return MOE_OK;
 }
 
-inline int launch_stream(const Prod& p, Plan* plan, hipStream_t s) {
+template <int MODE>
+int launch_stream(const Prod& p, Plan* plan, hipStream_t s) {
+  const auto fn = grouped_stream_mma_kernel<MODE>;
   static std::atomic<bool> done[64];
-  if (!allow_lds(reinterpret_cast<const void*>(grouped_stream_mma_kernel), ST_LDS, done)) return MOE_EHIP;
-  hipLaunchKernelGGL(grouped_stream_mma_kernel, dim3((cu_count() + 7) / 8 * 8), dim3(lin::W * MOE_WAVE),
+  if (!allow_lds(reinterpret_cast<const void*>(fn), ST_LDS, done)) return MOE_EHIP;
+  hipLaunchKernelGGL(fn, dim3((cu_count() + 7) / 8 * 8), dim3(lin::W * MOE_WAVE),
                      ST_LDS, s, p, plan);
   return MOE_OK;
 }
 
-inline bool streams(const Prod& p) {
-  return tile_choice(DW, p.g.R, p.g.N, p.W, p.K, cu_count()) == STREAM;
+inline bool streams(int mode, const Prod& p) {
+  return tile_choice(mode, p.g.R, p.g.N, p.W, p.K, cu_count()) == STREAM;
 }
 
 template <bool GLU, bool GATHER>
@@ -136,11 +138,12 @@ int launch_skinny(const Prod& p, hipStream_t s) {
   return MOE_OK;
 }
 
-// plan: of the streaming product
+// plan: of the streaming products
 template <int MODE, bool GLU, bool GATHER>
 int launch_tile(const Prod& p, Plan* plan, hipStream_t s) {
   switch (tile_choice(MODE, p.g.R, p.g.N, p.W, p.K, cu_count())) {
-    case STREAM: return launch_stream(p, plan, s);
+    case STREAM:
+      if constexpr (MODE != FWD) return launch_stream<MODE>(p, plan, s);
     case SKINNY:
       if constexpr (MODE == FWD) return launch_skinny<GLU, GATHER>(p, s);
     case TILE_256: return launch_mma<MODE, 256, 256, 64, 2, 1, GLU, GATHER>(p, s);
@@ -255,7 +258,7 @@ int backward(const void* dy, const void* x, const int32_t* row_token, const Grou
   px.e.y = dx;
   pw.e.y = dw;
   Plan* plan = nullptr;
-  if (sizeof(E) == 2 && dw && streams(pw))
+  if (sizeof(E) == 2 && ((dx && streams(DX, px)) || (dw && streams(DW, pw))))
     plan = reinterpret_cast<Plan*>(space + b.plan);
   const unsigned own = act == MOE_ACT_NONE ? 0 : grid_of(static_cast<size_t>(g.R) * (O / D::V)).x;
   const unsigned copy = a.rows ? grid_of(static_cast<size_t>(g.R) * (K / 8)).x : 0;

@@ -28,11 +28,11 @@ inline double rounds(double tiles, int cus) { return std::ceil(tiles / cus); }
 //             256 and slices of 32: it is the weights that are read, 5.4 TB/s, by
 //             two workgroups a CU
 //             dw 200 streaming, 250 with 256 x 256 tiles, 274 with 128 x 128
-//   512 rows  dx 432, 523 and 481; dw 470, 530, 642; forward 374 and 429
+//   512 rows  dx 395 streaming, 432, 523 and 481; dw 470, 530, 642; forward 374 and 429
 // Few rows: where the 128 x 128 tiles leave half the compute units without one, 16
 // weight rows to a workgroup: 8 experts with a row each 11.8 us, 16.1 with tiles
 // (768 x 2048 swiglu); 16 such experts 20.3 and 18.8, 2048 x 768 10.0 and 8.9.
-// The streaming weight gradient deals whole experts to the XCDs, which takes several
+// The streaming kernel deals whole experts to the XCDs, which takes several
 // for each: with 8 experts it took 1.7 times as long as the tiles.
 inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
   const int used = std::min(N, R);  // experts that can have rows
@@ -50,6 +50,7 @@ inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
   const double large = rounds(tiles(256, 256), cus) *
                        (slices * std::max(0.4, 1.55 * height) + (mode == DW ? 10 : 14));
   const double small = rounds(tiles(128, 128), cus) * (slices * 0.57 + 2) + 4;
+  if (mode == DX && large <= small && N >= 64 && N <= STREAM_EXPERTS) return STREAM;
   return large <= small ? TILE_256 : TILE_128;
 }
 

@@ -1,9 +1,11 @@
-// bf16 weight gradients of many experts: dW_e = sum over e's rows of dz_r x_r^T, one
-// workgroup per CU that stays and walks its tiles of 256 x 256, the ring of
-// linear_mma.h running on across their borders.
+// bf16 gradients of many experts, one workgroup per CU that stays and walks its
+// tiles of 256 x 256, the ring of linear_mma.h running on across their borders:
 //
-// An expert's reduction is short (8 slices of 64 rows at 512 rows), so a tile is
-// half start and output.  Here a tile's first two slices are requested under the
+//   DW  dW_e = sum over e's rows of dz_r x_r^T
+//   DX  dx_r = dz_r W_e
+//
+// An expert's reductions are short (DW: 8 slices of 64 rows at 512 rows), so a tile
+// is half start and output.  Here a tile's first two slices are requested under the
 // last two of the tile before it, and the output leaves through the one ring stage
 // that is free then (32 KB, 64 rows at a time, already bf16); its stores go out
 // behind those requests, and the wait of the next tile's first slice lets them be
@@ -11,11 +13,18 @@
 // the same number of stores, those outside the matrix at an offset that the
 // buffer's bounds drop.
 //
-// Measured, 128 experts of 1536 x 2048: 512 rows each 470 us (0.88 PFLOP/s; a
-// workgroup per tile 530, the library's batched product 610), 64 rows each 200 (250;
+// DX: an expert's rows are cut into units of 64 and these shared out evenly over its
+// tiles; the waves hold them in fragments of 32 in turn, so that a tile of fewer
+// than four units leaves out the MFMAs of whole fragments in every wave alike.
+//
+// Measured, DX of the spread tokens below: 511 us, a workgroup per tile 583.
+// DW, 128 experts of 1536 x 2048: 512 rows each 470 us (0.88 PFLOP/s; a
+// workgroup per tile 530, the library's batched product 600), 64 rows each 200 (250;
 // 805 MB written, 118 at the rate of a fill); 8192 tokens as a router spreads them
-// (up to 3700 rows) 567 (656).
+// (up to 3700 rows) 541 to 567 (656).
 #pragma once
+
+#include <type_traits>
 
 #include "grouped_common.h"
 #include "grouped_mma.h"
@@ -39,7 +48,7 @@ struct alignas(16) PlanEntry {
 };
 struct Plan {
   PlanEntry entry[8][MOE_WAVE];  // e < 0: none
-  int32_t ticket[8];             // tiles drawn
+  int32_t ticket[2][8];          // tiles drawn, of DX and of DW
 };
 static_assert(STREAM_EXPERTS == 8 * MOE_WAVE, "an entry for each lane");
 
@@ -53,7 +62,7 @@ __device__ __forceinline__ void make_plan(const Groups& g, Plan* plan) {
       rows[i] = s.hi - s.lo;
     }
   }
-  if (threadIdx.x < 8) plan->ticket[threadIdx.x] = 0;
+  if (threadIdx.x < 16) (&plan->ticket[0][0])[threadIdx.x] = 0;
   __syncthreads();  // also between the two writers of an entry
   for (int i = threadIdx.x; i < g.N; i += 256) {
     const int mine = rows[i];
@@ -66,36 +75,59 @@ __device__ __forceinline__ void make_plan(const Groups& g, Plan* plan) {
 }
 
 struct StreamTile {
-  int e, lo, len;  // expert, its first row, its rows
-  int m0, rows;    // first row of the weights, rows
+  int e, lo, len;  // expert, first row of its reduction (DX: of the tile), reduction
+  int m0, rows;    // first output row, rows
   int n0, width;   // first column, columns
+  int live;        // units of 64 rows
 };
 
+// The row tiles of an expert: `first` of height + 1 units, then the others of height.
+struct Cut {
+  int tiles, height, first;
+};
+__device__ __forceinline__ Cut cut_of(int rows) {
+  const int units = (rows + UNIT - 1) / UNIT, tiles = (units + 3) / 4;
+  const int height = tiles ? units / tiles : 0;
+  return {tiles, height, units - height * tiles};
+}
+
 // The tiles of the workgroup's XCD, an entry of the plan in each lane.
+template <int MODE>
 struct StreamTiles {
   const Prod& p;
   int tm, tn, e, lo, hi, incl, end;
 
   __device__ __forceinline__ StreamTiles(const Prod& q, const Plan* plan) : p(q) {
-    tm = (p.W + ST - 1) / ST;
+    tm = (p.W + ST - 1) / ST;  // DW
     tn = (p.K + ST - 1) / ST;
     const PlanEntry own = plan->entry[blockIdx.x % 8][lane_id()];
     e = own.e;
     lo = own.lo;
     hi = own.hi;
-    incl = wave_incl_scan(e < 0 ? 0 : tm * tn);
+    incl = wave_incl_scan(e < 0 ? 0 : (MODE == DW ? tm : cut_of(hi - lo).tiles) * tn);
     end = read_lane(incl, MOE_WAVE - 1);
   }
   __device__ __forceinline__ StreamTile tile(int i) const {  // i < end
     const int l = __builtin_ctzll(__ballot(incl > i));
+    const int first = read_lane(lo, l), count = read_lane(hi, l) - first;
+    const Cut c = cut_of(count);
+    const int height = MODE == DW ? tm : c.tiles;
     int mt, nt;
-    banded(i - (read_lane(incl, l) - tm * tn), tm, tn, mt, nt);
+    banded(i - (read_lane(incl, l) - height * tn), height, tn, mt, nt);
     StreamTile t;
     t.e = read_lane(e, l);
-    t.lo = read_lane(lo, l);
-    t.len = read_lane(hi, l) - t.lo;
-    t.m0 = uniform(mt * ST);
-    t.rows = uniform(min(ST, p.W - t.m0));
+    if (MODE == DW) {
+      t.lo = first;
+      t.len = count;
+      t.m0 = uniform(mt * ST);
+      t.rows = uniform(min(ST, p.W - t.m0));
+      t.live = 4;
+    } else {
+      t.live = uniform(c.height + (mt < c.first));
+      t.m0 = t.lo = uniform(first + (mt * c.height + min(mt, c.first)) * UNIT);
+      t.rows = uniform(min(t.live * UNIT, first + count - t.m0));
+      t.len = p.W;
+    }
     t.n0 = uniform(nt * ST);
     t.width = uniform(min(ST, p.K - t.n0));
     return t;
@@ -107,12 +139,16 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-__device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsigned char* smem) {
-  typedef Operand<true, false, ST, lin::W> Op;
-  typedef Reader<true, ST> Frag;
+template <int MODE>
+__device__ __forceinline__ void stream_product(const Prod& p, Plan* plan, unsigned char* smem) {
+  constexpr bool RS = MODE == DW;
+  typedef Operand<RS, false, ST, lin::W> Row;
+  typedef Operand<true, false, ST, lin::W> Col;
+  typedef Reader<RS, ST> RowR;
+  typedef Reader<true, ST> ColR;
   constexpr int FM = 4, FN = 4, KK = SLICE / 16, Q = 8, BASE = SA * ST_STAGE;
-  constexpr int STORES = 32;  // of a tile, per wave
-  static_assert(Op::Q == Q && WM == 2 && WN == 2 && SA == 2 && SB == 3, "the waits' counts");
+  constexpr int STORES = 32;  // of a whole tile, per wave
+  static_assert(Row::Q == Q && Col::Q == Q && WM == 2 && WN == 2 && SA == 2 && SB == 3, "the waits' counts");
   typedef __attribute__((address_space(3))) unsigned char lds_byte;
   typedef __attribute__((address_space(3))) int32_t lds_int;
   typedef __attribute__((address_space(3))) u32x2 lds_u2;
@@ -121,12 +157,12 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
   const int wm = wave / WN, wn = wave % WN;
-  const StreamTiles tiles(p, plan);
+  const StreamTiles<MODE> tiles(p, plan);
   // The first tile goes by the workgroup's number, the others by ticket: drawn by
   // one thread, handed round through LDS that is free at the time.
   auto draw = [&]() __attribute__((always_inline)) {
     return threadIdx.x == 0
-               ? static_cast<int32_t>(gridDim.x / 8) + atomicAdd(&plan->ticket[blockIdx.x % 8], 1)
+               ? static_cast<int32_t>(gridDim.x / 8) + atomicAdd(&plan->ticket[MODE == DW][blockIdx.x % 8], 1)
                : 0;
   };
   auto hand_round = [&](lds_byte* s, int32_t drawn) __attribute__((always_inline)) {
@@ -145,7 +181,8 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
   int queue[2] = {-1, -1};  // tiles requested behind `here`, in order
   bool more = false;
   if (here >= tiles.end) return;
-  Op row, col;
+  Row row;
+  Col col;
   auto aim = [&]() __attribute__((always_inline)) {
     slice = 0;
     StreamTile t;
@@ -156,9 +193,9 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
     kend = more ? t.len : 1;
     if (!more) return;
     slices = (t.len + SLICE - 1) / SLICE;
-    row.init(static_cast<const uint16_t*>(p.r) + static_cast<size_t>(t.lo) * p.W + t.m0, p.W, t.rows,
-             wave, lane);
-    col.init(static_cast<const uint16_t*>(p.c) + static_cast<size_t>(t.lo) * p.K + t.n0, p.K, t.width,
+    const uint16_t *r = static_cast<const uint16_t*>(p.r), *c = static_cast<const uint16_t*>(p.c);
+    row.init(r + static_cast<size_t>(t.lo) * p.W + (RS ? t.m0 : 0), p.W, t.rows, wave, lane);
+    col.init(c + (RS ? static_cast<size_t>(t.lo) : static_cast<size_t>(t.e) * p.W) * p.K + t.n0, p.K, t.width,
              wave, lane);
   };
   // free: the stage that this slice's columns are about to take
@@ -188,9 +225,9 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
   bool stored = false;  // the output's stores lie between the last requests
   uint32_t ro[FM], co[FN];
 #pragma unroll
-  for (int x = 0; x < FM; ++x) ro[x] = Frag::lane_off(wm * (ST / 2) + x * 32, lane);
+  for (int x = 0; x < FM; ++x) ro[x] = RowR::lane_off(x * UNIT + wm * 32, lane);
 #pragma unroll
-  for (int y = 0; y < FN; ++y) co[y] = Frag::lane_off(wn * (ST / 2) + y * 32, lane);
+  for (int y = 0; y < FN; ++y) co[y] = ColR::lane_off(wn * (ST / 2) + y * 32, lane);
   f32x16 acc[FM][FN];
   bf16x8 fr[2][FM], fc[2][FN];
   auto clear = [&](int x) {
@@ -201,18 +238,21 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
   };
   auto read = [&](int r, int c, int kk, int f) {
     if (f >= 1 && f <= FN)
-      fc[kk & 1][f - 1] = Frag::read(lds0 + BASE + c * ST_STAGE, co[f - 1], kk, lane);
+      fc[kk & 1][f - 1] = ColR::read(lds0 + BASE + c * ST_STAGE, co[f - 1], kk, lane);
     else
-      fr[kk & 1][f ? f - FN : 0] = Frag::read(lds0 + r * ST_STAGE, ro[f ? f - FN : 0], kk, lane);
+      fr[kk & 1][f ? f - FN : 0] = RowR::read(lds0 + r * ST_STAGE, ro[f ? f - FN : 0], kk, lane);
   };
   // As in mma_core: the MFMAs of 16 k, the reads of the next 16 k from stages r and
-  // c behind the first, the requests between them.
-  auto step = [&](int kk, int r, int c, int requests, auto request) __attribute__((always_inline)) {
+  // c behind the first, the requests between them; live: row fragments of a wave.
+  auto step = [&](auto live, int kk, int r, int c, int requests, auto request)
+      __attribute__((always_inline)) {
+    constexpr int LIVE = decltype(live)::value;
 #pragma unroll
     for (int i = 0; i < FM * FN; ++i) {
       const int x = i / FN, y = i % FN;
-      acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[kk & 1][y], fr[kk & 1][x], acc[x][y],
-                                                         0, 0, 0);
+      if (x < LIVE)
+        acc[x][y] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fc[kk & 1][y], fr[kk & 1][x],
+                                                             acc[x][y], 0, 0, 0);
       if (i < FM + FN) read(r, c, (kk + 1) % KK, i);
 #pragma unroll
       for (int q = 0; q < requests; ++q)
@@ -223,17 +263,17 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
   // Slice g, while column slice g + 2 and, behind the barrier, row slice g + 2 are
   // requested.  The wait is for row and column slice g + 1; behind those come, in
   // this order, the stores of an output in between and column slice g + 2.
-  auto one_slice = [&]() __attribute__((always_inline)) {
+  auto one_slice = [&](auto live) __attribute__((always_inline)) {
     const int rn = rs ^ 1, cn = cs == 2 ? 0 : cs + 1, cr = cs == 0 ? 2 : cs - 1;
     begin(cr);
-    step(0, rs, cs, 3, [&](int q) { load_col(q, cr); });
-    step(1, rs, cs, 3, [&](int q) { load_col(3 + q, cr); });
-    step(2, rs, cs, 2, [&](int q) { load_col(6 + q, cr); });
+    step(live, 0, rs, cs, 3, [&](int q) { load_col(q, cr); });
+    step(live, 1, rs, cs, 3, [&](int q) { load_col(3 + q, cr); });
+    step(live, 2, rs, cs, 2, [&](int q) { load_col(6 + q, cr); });
     if (stored) wait_vmcnt<STORES + Q>();
     else wait_vmcnt<Q>();
     stored = false;
     lds_barrier();
-    step(3, rn, cn, Q, [&](int q) { load_row(q, rs); });
+    step(live, 3, rn, cn, Q, [&](int q) { load_row(q, rs); });
     slice += more;
     rs = rn;
     cs = cn;
@@ -249,7 +289,8 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
     if (drawing) drawn = draw();
     const uint32_t bytes = static_cast<uint32_t>(p.K) * 2;
     const auto rsrc = store_rsrc(
-        static_cast<uint16_t*>(p.e.y) + (static_cast<size_t>(t.e) * p.W + t.m0) * p.K + t.n0,
+        static_cast<uint16_t*>(p.e.y) +
+            ((RS ? static_cast<size_t>(t.e) * p.W : 0) + t.m0) * p.K + t.n0,
         (t.rows - 1) * bytes + t.width * 2);
     // The lane's places are worked out anew for each output: held over the product
     // they would take the registers of a third of the fragments.
@@ -257,7 +298,11 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
     asm volatile("" : "+v"(tid));
     const int half = tid / 32 % 2, wr = tid % 32, ch = tid % CH, r0 = tid / CH;
 #pragma unroll
-    for (int x = 0; x < FM; ++x) {  // rows 32 x .. of both wave rows
+    for (int x = 0; x < FM; ++x) {
+      if (x >= t.live) {
+        clear(x);
+        continue;
+      }
 #pragma unroll
       for (int y = 0; y < FN; ++y)
 #pragma unroll
@@ -277,12 +322,12 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int r = r0 + 8 * j, m = r / 32 * (ST / 2) + x * 32 + r % 32;
+        const int m = x * UNIT + r0 + 8 * j;
         buf_store16(rsrc, ch * 8 < t.width ? m * bytes + ch * 16 : OOB_OFF, v[j]);
       }
       lds_barrier();
     }
-    stored = true;
+    stored = t.live == 4;
     if (drawing) next = hand_round(s, drawn);
   };
 
@@ -306,7 +351,13 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
     while (here < tiles.end) {
       const StreamTile t = tiles.tile(here);
       if (t.len == 0) break;
-      for (int k = 0; k < t.len; k += SLICE) one_slice();
+      auto multiply = [&](auto live) __attribute__((always_inline)) {
+        for (int k = 0; k < t.len; k += SLICE) one_slice(live);
+      };
+      if (MODE == DW || t.live == 4) multiply(std::integral_constant<int, 4>());
+      else if (t.live == 3) multiply(std::integral_constant<int, 3>());
+      else if (t.live == 2) multiply(std::integral_constant<int, 2>());
+      else multiply(std::integral_constant<int, 1>());
       output(t);
       here = queue[0];
       queue[0] = queue[1];
@@ -314,8 +365,8 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
     }
   }
   wait_vmcnt<0>();  // no load may land after the workgroup ends
-  // What is left are weights of experts without rows: zeros.
-  while (here < tiles.end) {
+  // DW: what is left are weights of experts without rows: zeros.
+  while (MODE == DW && here < tiles.end) {
     const StreamTile t = tiles.tile(here);
     uint16_t* out =
         static_cast<uint16_t*>(p.e.y) + (static_cast<size_t>(t.e) * p.W + t.m0) * p.K + t.n0;
@@ -329,10 +380,11 @@ __device__ __forceinline__ void stream_weights(const Prod& p, Plan* plan, unsign
   }
 }
 
+template <int MODE>
 __global__ __launch_bounds__(lin::W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void grouped_stream_mma_kernel(Prod p, Plan* plan) {
   extern __shared__ __align__(16) unsigned char smem[];
-  stream_weights(p, plan, smem);
+  stream_product<MODE>(p, plan, smem);
 }
 
 }  // namespace grp

@@ -21,5 +21,6 @@ GROUPS = [
 LARGE = [
     ([400 + 37 * i % 220 for i in range(33)], 50, 2056, 4104),
     ([60 + 5 * i % 40 for i in range(64)], 0, 1032, 2056),
+    ([3500, 0, 1] + [30 + 97 * i % 350 for i in range(61)], 7, 1544, 1032),
     ([260 + 3 * i % 50 for i in range(16)], 9, 712, 1032),
 ]

@@ -126,7 +126,8 @@ def test_grouped_large_tiles(B, i, act, gather, dtype):
     print(f"[gpu-test] grouped large {len(counts)} {K} {O} {act} {dtype}", flush=True)
     g, M, rows, O, W, x, w, token, tok, off, offsets = _grouped_inputs(LARGE[i], act, dtype, gather, 100 + i)
     N = len(counts)
-    at = sorted({int(r) for e in range(N) for r in (offsets[e], offsets[e + 1] - 1, *g.integers(offsets[e], offsets[e + 1], 2))})
+    at = sorted({int(r) for e in range(N) if counts[e]
+                 for r in (offsets[e], offsets[e + 1] - 1, *g.integers(offsets[e], offsets[e + 1], 2))})
     few = np.searchsorted(at, offsets)  # offsets among the compared rows
     dy, z = _rand(g, (rows, O), 0.5, dtype), torch.empty(rows, W, dtype=dtype, device="cuda")
     dy[M:] = float("nan")

@@ -37,7 +37,7 @@ def _sizes():
 
 def test_every_bf16_tile_is_tested(plan):
     seen = {(m, plan.bf16(m, *s)) for s in _sizes() if s[0] for m in (FWD, DX, DW)}
-    assert seen == {(FWD, TILE_256), (FWD, TILE_128), (FWD, SKINNY), (DX, TILE_256), (DX, TILE_128), (DX, TILE_128x256),
+    assert seen == {(FWD, TILE_256), (FWD, TILE_128), (FWD, SKINNY), (DX, TILE_256), (DX, TILE_128), (DX, TILE_128x256), (DX, STREAM),
                     (DW, TILE_256), (DW, TILE_128), (DW, STREAM)}
 
 
@@ -52,6 +52,7 @@ def test_no_size_reaches_another_tile(plan):
             for W in (8, 128, 136, 1536, 65536, 131072):
                 for K in (8, 128, 136, 2048, 65536):
                     assert plan.bf16(FWD, R, N, W, K) in (TILE_256, TILE_128, SKINNY)
-                    assert plan.bf16(DX, R, N, W, K) in (TILE_256, TILE_128, TILE_128x256)
+                    assert plan.bf16(DX, R, N, W, K) in (TILE_256, TILE_128, TILE_128x256, STREAM)
                     assert plan.bf16(DW, R, N, W, K) in (TILE_256, TILE_128, STREAM)
-                    assert (plan.bf16(DW, R, N, W, K) == STREAM) <= (64 <= N <= 512)
+                    for mode in (DX, DW):
+                        assert (plan.bf16(mode, R, N, W, K) == STREAM) <= (64 <= N <= 512)

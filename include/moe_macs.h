@@ -27,9 +27,14 @@
  *   moe_combine_dropout -> (loss) -> moe_combine_backward
  *   moe_balance_loss -> moe_router_backward (with the gates' gradient)
  *   -> moe_linear_backward (the router's product, the shared expert)
+ * and what training the routed experts takes around that:
+ *   moe_norm -> (router, moe_dispatch) -> moe_grouped_linear (gate-up, z kept)
+ *   -> moe_grouped_linear (down) -> (combine, loss, combine backward)
+ *   -> moe_grouped_linear_backward (down, then gate-up) -> moe_combine with
+ *   gates of one (the tokens' gradient) -> moe_norm_backward -> moe_grad_clip
  *
  * Conventions shared by every entry point
- *   - Every array argument is a DEVICE pointer owned by the caller; the
+ *   - Every array argument (moe_grad_table's apart) is a DEVICE pointer owned by the caller; the
  *     library never allocates, frees or keeps pointers after returning.
  *     The only state it keeps is per device and set on first use: the
  *     compute-unit count, whether a GEMM kernel's LDS limit has been set,
@@ -46,8 +51,9 @@
  *        MOE_EHIP    the HIP runtime reported a launch error,
  *        MOE_ESCRATCH  the no-allocation variant's fixed buffer is too
  *                    small for the call.
- *   - T == 0 is valid and enqueues nothing (moe_linear_backward and
- *     moe_balance_loss write zeros to the sums over tokens).
+ *   - T == 0 is valid and enqueues nothing (moe_linear_backward,
+ *     moe_grouped_linear_backward, moe_norm_backward and moe_balance_loss write
+ *     zeros to the sums over tokens).
  *   - Limits: 1 <= N <= 1024 experts, 1 <= k <= N, 0 <= R <= N - k,
  *     T <= 2^20 tokens.
  *   - Device data are not validated: router logits must be finite, expert
@@ -59,7 +65,9 @@
  *   moe_router_topk, moe_capacity_assign, moe_dispatch, moe_routing_fused,
  *   moe_expert_ffn and moe_expert_ffn_combine take a workspace of at least
  *   the size their *_workspace_size() query returns, and so do moe_linear,
- *   moe_linear_backward and moe_balance_loss (scratch only).  The router, capacity,
+ *   moe_linear_backward, moe_balance_loss, moe_grouped_linear,
+ *   moe_grouped_linear_backward, moe_norm_backward and moe_grad_clip (scratch
+ *   only).  The router, capacity,
  *   dispatch, fused-routing and FFN-combine workspaces hold a few control
  *   words: they must be filled with zero bytes once, before their first use
  *   (e.g. allocated zeroed); every call leaves those words zero again.  A workspace must not be

@@ -711,8 +711,8 @@ int moe_grouped_linear(const void* x, const int32_t* row_token,
  *           with gates of one.
  * dw        as w, out (dtype), overwritten; zeros for an expert without rows.
  * dx or dw may be NULL to skip it, not both (R == 0: any).
- * dz is rounded to dtype for the two products, as in moe_linear_backward.
- * R == 0 writes zeros to dw.  Workspace of
+ * dz is rounded to dtype for the two products, as in moe_linear_backward.  The
+ * outputs must not overlap the inputs.  R == 0 writes zeros to dw.  Workspace of
  * moe_grouped_linear_backward_workspace_size() bytes (scratch only), limits
  * and errors as moe_grouped_linear.
  */

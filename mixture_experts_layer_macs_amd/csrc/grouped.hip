@@ -39,7 +39,7 @@ __device__ __forceinline__ void act_grad_rows(const typename D::elem* dy, const 
 
 // The rows of x in the experts' order, for the reduction over them: a gather
 // inside the product, along the axis that it reduces, cost it 20 to 37 % (8192
-// tokens, 128 experts, 1536 x 2048: 743 us for 543), this copy 50 us beside the
+// tokens, 128 experts, 1536 x 2048: 743 us for 543), this copy 75 us beside the
 // activation gradient.
 struct Gathered {
   const uint16_t* x;

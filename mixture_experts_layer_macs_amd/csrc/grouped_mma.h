@@ -6,6 +6,12 @@
 //   DX   dx_r = dz_r W_e         rows of dz by W_e's columns
 //   DW   dW_e = sum dz_r x_t^T   reduction over the expert's rows, both operands
 //                                reduction-strided, x laid out by rows beforehand
+//
+// Bound by the matrix pipe, by the partial tiles of ragged groups and by a tile's
+// start and output (14 us beside 50 for 32 slices), which one workgroup a CU cannot
+// hide.  Measured: 8192 tokens spread over 128 experts of 1536 x 2048, swiglu with z
+// kept, 413 to 445 us (0.89 to 0.95 PFLOP/s); even groups of 512 rows 374; 8192 rows in
+// 8 experts of 28672 x 4096 1675 (1.15 PFLOP/s).
 #pragma once
 
 #include <type_traits>

@@ -76,6 +76,22 @@ __global__ __launch_bounds__(256) void prepare_kernel(const typename D::elem* dy
   }
 }
 
+// The parts' sums, in their order, to dw.
+__global__ __launch_bounds__(256) void join_weights_kernel(Prod p, size_t quads) {
+  const size_t step = gridDim.x * static_cast<size_t>(256);
+  for (size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; i < quads; i += step) {
+    float v[4] = {};
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+      float f[4];
+      load4(p.part + (s * quads + i) * 4, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += f[j];
+    }
+    store4(static_cast<uint16_t*>(p.e.y) + i * 4, v);
+  }
+}
+
 // --------------------------------------------------------------------- host
 inline size_t elem_size(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 inline int width(int O, int act) { return act == MOE_ACT_SWIGLU ? 2 * O : O; }
@@ -107,7 +123,7 @@ int launch_mma(const Prod& p, hipStream_t s) {
   const int N = MODE == FWD ? (GLU ? p.W / 2 : p.W) : p.K;
   const long rows = MODE == DW ? static_cast<long>(p.g.N) * ((p.W + BM - 1) / BM)
                                : max_row_tiles(p.g.R, p.g.N, BM);
-  const long tiles = rows * ((N + NC - 1) / NC);
+  const long tiles = rows * ((N + NC - 1) / NC) * (MODE == DW && GLU ? p.splits : 1);
   if (tiles > (1 << 23)) return MOE_EUNSUP;  // the outputs alone would not fit the card
   hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(lin::W * MOE_WAVE), lds,
                      s, p);
@@ -149,7 +165,16 @@ int launch_tile(const Prod& p, Plan* plan, hipStream_t s) {
     case TILE_256: return launch_mma<MODE, 256, 256, 64, 2, 1, GLU, GATHER>(p, s);
     case TILE_128x256:
       if constexpr (MODE == DX) return launch_mma<MODE, 128, 256, 32, 3, 2, GLU, GATHER>(p, s);
-    default: return launch_mma<MODE, 128, 128, 64, 2, 2, GLU, GATHER>(p, s);
+    default:
+      if constexpr (MODE == DW)
+        if (p.splits > 1) {
+          const int rc = launch_mma<DW, 128, 128, 64, 2, 2, true, false>(p, s);
+          const size_t quads = static_cast<size_t>(p.g.N) * p.W * p.K / 4;
+          if (rc == MOE_OK)
+            hipLaunchKernelGGL(join_weights_kernel, grid_of(quads), dim3(256), 0, s, p, quads);
+          return rc;
+        }
+      return launch_mma<MODE, 128, 128, 64, 2, 2, GLU, GATHER>(p, s);
   }
 }
 
@@ -221,15 +246,27 @@ int products(const Prod& x, const Prod& w, Plan* plan, hipStream_t s) {
   return rc;
 }
 
-// The backward pass's workspace: dz, then (bf16) the rows of x, then the plan.
+// Parts of the weight gradient's reduction.
+inline int splits_of(int R, int N, int W, int K, int dtype) {
+  const int cus = cu_count();
+  return dtype == MOE_BF16 && R > 0 && tile_choice(DW, R, N, W, K, cus) == TILE_128
+             ? split_choice(R, N, W, K, cus) : 1;
+}
+
+// The backward pass's workspace: dz, then (bf16) the rows of x, the plan and the
+// parts of dw.
 struct BackSpace {
-  size_t rows, plan, bytes;
+  size_t rows, plan, part, bytes;
+  int splits;
 };
-inline BackSpace back_space(int R, int K, int O, int act, int dtype) {
+inline BackSpace back_space(int R, int N, int K, int O, int act, int dtype) {
   const size_t el = elem_size(dtype);
   const size_t dz = act == MOE_ACT_NONE ? 0 : (R * (width(O, act) * el) + 255) / 256 * 256;
   const size_t rows = dtype == MOE_BF16 ? (static_cast<size_t>(R) * K * el + 255) / 256 * 256 : 0;
-  return {dz, dz + rows, dz + rows + sizeof(Plan)};
+  const size_t part = dz + rows + (sizeof(Plan) + 255) / 256 * 256;
+  const int splits = splits_of(R, N, width(O, act), K, dtype);
+  return {dz, dz + rows, part,
+          part + (splits > 1 ? static_cast<size_t>(splits) * N * width(O, act) * K * 4 : 0), splits};
 }
 
 template <typename D>
@@ -246,7 +283,7 @@ int backward(const void* dy, const void* x, const int32_t* row_token, const Grou
   }
   char* space = static_cast<char*>(ws);
   const void* dz = act == MOE_ACT_NONE ? dy : ws;
-  const BackSpace b = back_space(g.R, K, O, act, sizeof(E) == 2 ? MOE_BF16 : MOE_F32);
+  const BackSpace b = back_space(g.R, g.N, K, O, act, sizeof(E) == 2 ? MOE_BF16 : MOE_F32);
   Gathered a{};
   if (sizeof(E) == 2 && row_token && dw) {
     a = Gathered{static_cast<const uint16_t*>(x), row_token, reinterpret_cast<uint16_t*>(space + b.rows), K};
@@ -257,6 +294,8 @@ int backward(const void* dy, const void* x, const int32_t* row_token, const Grou
   Prod pw{dz, x, row_token, static_cast<size_t>(T), g, W, K, Epilogue{}};
   px.e.y = dx;
   pw.e.y = dw;
+  pw.splits = b.splits;
+  pw.part = reinterpret_cast<float*>(space + b.part);
   Plan* plan = nullptr;
   if (sizeof(E) == 2 && ((dx && streams(DX, px)) || (dw && streams(DW, pw))))
     plan = reinterpret_cast<Plan*>(space + b.plan);
@@ -306,7 +345,7 @@ extern "C" int moe_grouped_linear(const void* x, const int32_t* row_token,
 extern "C" size_t moe_grouped_linear_backward_workspace_size(int R, int N, int K, int O, int act,
                                                              int dtype) {
   if (check(R, N, K, O, act, dtype) != MOE_OK) return 0;
-  return back_space(R, K, O, act, dtype).bytes;
+  return back_space(R, N, K, O, act, dtype).bytes;
 }
 
 extern "C" int moe_grouped_linear_backward(const void* dy, const void* x, const int32_t* row_token,

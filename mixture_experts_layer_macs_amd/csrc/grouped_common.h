@@ -91,13 +91,15 @@ __device__ __forceinline__ bool data_tile(const Groups& g, int height, int cols,
   return true;
 }
 
-// Tile of a weight gradient.
-__device__ __forceinline__ bool weight_tile(int N, int rows, int cols, int block, int& e, int& mt,
-                                            int& nt) {
-  const int at = place_of(block, N * rows * cols);
+// Tile of a weight gradient, and part of its reduction.
+__device__ __forceinline__ bool weight_tile(int N, int rows, int cols, int splits, int block, int& e,
+                                            int& mt, int& nt, int& split) {
+  const int at = place_of(block, N * rows * cols * splits);
   if (at < 0) return false;
-  e = at / (rows * cols);
-  banded(at - e * rows * cols, rows, cols, mt, nt);
+  split = at % splits;
+  const int tile = at / splits;
+  e = tile / (rows * cols);
+  banded(tile - e * rows * cols, rows, cols, mt, nt);
   return true;
 }
 

@@ -35,6 +35,8 @@ struct Prod {
   Groups g;
   int W, K;              // rows (GLU: gate and up) and columns of an expert's weights
   Epilogue e;            // y: dx, dw
+  int splits;            // DW in parts: their number and [splits][N][W][K] sums
+  float* part;
 };
 
 // The dense layer's row operand with the rows of a token list: the tile's rows
@@ -99,19 +101,31 @@ __device__ __forceinline__ void data_product(const Prod& p, int block, unsigned 
   else run(std::integral_constant<int, 4>());
 }
 
-template <int BM, int BN, int SL, int RA>
+// DW: one tile, or (PART) one of `splits` parts of its reduction.
+template <int BM, int BN, int SL, int RA, bool PART>
 __device__ __forceinline__ void weight_product(const Prod& p, int block, unsigned char* smem) {
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / MOE_WAVE);
-  int e, mt, nt;
-  if (!weight_tile(p.g.N, (p.W + BM - 1) / BM, (p.K + BN - 1) / BN, block, e, mt, nt)) return;
+  int e, mt, nt, split;
+  if (!weight_tile(p.g.N, (p.W + BM - 1) / BM, (p.K + BN - 1) / BN, PART ? p.splits : 1, block, e, mt, nt,
+                   split))
+    return;
   const Span s = span_of(p.g, e);
   const int n0 = nt * BN, m0 = mt * BM, lo = s.lo, count = s.hi - s.lo;
   const int rows = min(BM, p.W - m0), width = min(BN, p.K - n0);
-  uint16_t* out = static_cast<uint16_t*>(p.e.y) + static_cast<size_t>(e) * p.W * p.K;
-  if (count == 0) {  // no rows: zeros
-    for (int i = threadIdx.x; i < rows * (BN / 8); i += lin::W * MOE_WAVE) {
-      const int r = i / (BN / 8), c = i % (BN / 8) * 8;
+  int k_lo = 0, k_hi = count;
+  if constexpr (PART) {
+    const int per = ((count + p.splits - 1) / p.splits + SLICE - 1) / SLICE * SLICE;
+    k_lo = uniform(split * per);
+    k_hi = uniform(min(count, k_lo + per));
+  }
+  typedef std::conditional_t<PART, float, uint16_t> E;
+  constexpr int V = PART ? 4 : 8;
+  E* out = (PART ? reinterpret_cast<E*>(p.part) : static_cast<E*>(p.e.y)) +
+           (PART ? static_cast<size_t>(split) * p.g.N + e : static_cast<size_t>(e)) * p.W * p.K;
+  if (k_lo >= k_hi) {  // no rows: zeros
+    for (int i = threadIdx.x; i < rows * (BN / V); i += lin::W * MOE_WAVE) {
+      const int r = i / (BN / V), c = i % (BN / V) * V;
       if (c < width)
         *reinterpret_cast<u32x4*>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c) = u32x4{0, 0, 0, 0};
     }
@@ -123,17 +137,19 @@ __device__ __forceinline__ void weight_product(const Prod& p, int block, unsigne
   Operand<true, false, BN, lin::W, SL> col;
   col.init(static_cast<const uint16_t*>(p.c) + static_cast<size_t>(lo) * p.K + n0, p.K, width, wave,
            lane);
-  mma_core<true, true, BM, BN, false, 8, SL, RA>(row, col, 0, count, smem, [&](int r, int c, float* g, float*) {
-    if (r < rows && c < width) store_v<8>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c, g);
-  });
+  mma_core<true, true, BM, BN, false, V, SL, RA>(
+      row, col, k_lo, k_hi, smem, [&](int r, int c, float* g, float*) {
+        if (r < rows && c < width) store_v<V>(out + static_cast<size_t>(m0 + r) * p.K + n0 + c, g);
+      });
 }
 
 // RA: ring stages of the row operand.
+// DW: GLU says that the reduction is in parts.
 template <int MODE, int BM, int BN, int SL, int RA, int WGS, bool GLU, bool GATHER>
 __global__ __launch_bounds__(lin::W* MOE_WAVE) __attribute__((amdgpu_waves_per_eu(WGS, WGS)))
 void grouped_mma_kernel(Prod p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  if constexpr (MODE == DW) weight_product<BM, BN, SL, RA>(p, blockIdx.x, smem);
+  if constexpr (MODE == DW) weight_product<BM, BN, SL, RA, GLU>(p, blockIdx.x, smem);
   else data_product<MODE, BM, BN, SL, RA, GLU, GATHER>(p, blockIdx.x, smem);
 }
 

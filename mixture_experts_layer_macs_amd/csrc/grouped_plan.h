@@ -19,6 +19,23 @@ constexpr int STREAM_EXPERTS = 512;  // most that the streaming kernel's plan ho
 
 inline double rounds(double tiles, int cus) { return std::ceil(tiles / cus); }
 
+// A weight gradient of few tiles over many rows: its reduction in `splits` parts,
+// whose fp32 sums a second launch adds; the time with 128 x 128 tiles. In parts and
+// whole, us: one expert of 512^2 with 8192 rows 17.5 and 61.8, two of 1024^2 with 8192
+// each 48 and 67, four of 768^2 with 8192 each 54 and 67.
+inline double split_us(int R, int N, int W, int K, int splits, int cus) {
+  const double tiles = N * std::ceil(W / 128.0) * std::ceil(K / 128.0);
+  const double slices = static_cast<double>(R) / std::min(N, R) / 64 / splits;
+  const double join = splits > 1 ? 4 + splits * (static_cast<double>(N) * W * K * (8 / 4.0e6)) : 0;
+  return rounds(tiles * splits, cus) * (slices * 0.57 + 2) + 4 + join;
+}
+inline int split_choice(int R, int N, int W, int K, int cus) {
+  int best = 1;
+  for (int s = 2; s <= 8; ++s)
+    if (split_us(R, N, W, K, s, cus) < split_us(R, N, W, K, best, cus)) best = s;
+  return best;
+}
+
 // rows, W, K: of a product as in Prod (FWD with a gated activation: gate and up).
 // Times in us, from sweeps of 64 .. 1024 rows per expert, 128 experts, weights of
 // 512^2 .. 4096^2: a slice of 64 k takes a 256 x 256 tile 1.55 (the matrix pipe at
@@ -49,7 +66,8 @@ inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
   const double height = mode == DW ? 1.0 : std::min(1.0, std::ceil(rows / 64) / 4);
   const double large = rounds(tiles(256, 256), cus) *
                        (slices * std::max(0.4, 1.55 * height) + (mode == DW ? 10 : 14));
-  const double small = rounds(tiles(128, 128), cus) * (slices * 0.57 + 2) + 4;
+  double small = rounds(tiles(128, 128), cus) * (slices * 0.57 + 2) + 4;
+  if (mode == DW) small = std::min(small, split_us(R, N, W, K, split_choice(R, N, W, K, cus), cus));
   if (mode == DX && large <= small && N >= 64 && N <= STREAM_EXPERTS) return STREAM;
   return large <= small ? TILE_256 : TILE_128;
 }

@@ -15,6 +15,8 @@ GROUPS = [
     ([1] * 64, 0, 136, 136), ([0] * 63 + [5], 2, 264, 136), ([0, 1, 64, 65, 129, 3, 200, 7] * 10, 11, 264, 136),
     ([70, 2, 0, 128, 1, 63, 0, 300] * 9, 0, 520, 520), ([1300] + [1, 0] * 40, 5, 264, 264),
     ([20] * 40, 0, 520, 1032),
+    # few experts with many rows: the weight gradient's reduction in parts, some of them empty
+    ([1600, 0, 3, 1900], 9, 264, 392), ([2500, 70], 5, 136, 264), ([4000], 30, 72, 128),
 ]
 
 # many full tiles, compared in some rows: experts below and above the tiles' heights

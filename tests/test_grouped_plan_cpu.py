@@ -13,6 +13,7 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 CODE = """
 #include "grouped_plan.h"
 extern "C" int bf16(int mode, int R, int N, int W, int K) { return moe::grp::tile_choice(mode, R, N, W, K, 256); }
+extern "C" int splits(int R, int N, int W, int K) { return moe::grp::split_choice(R, N, W, K, 256); }
 extern "C" int f32(int mode, int R, int N, int W, int K) { return moe::grp::tile_choice_f32(mode, R, N, W, K, 256); }
 """
 FWD, DX, DW = 0, 1, 2
@@ -39,6 +40,13 @@ def test_every_bf16_tile_is_tested(plan):
     seen = {(m, plan.bf16(m, *s)) for s in _sizes() if s[0] for m in (FWD, DX, DW)}
     assert seen == {(FWD, TILE_256), (FWD, TILE_128), (FWD, SKINNY), (DX, TILE_256), (DX, TILE_128), (DX, TILE_128x256), (DX, STREAM),
                     (DW, TILE_256), (DW, TILE_128), (DW, STREAM)}
+
+
+def test_weight_gradients_in_parts_are_tested(plan):
+    some = [s for s in _sizes() if s[0] and plan.bf16(DW, *s) == TILE_128 and plan.splits(*s) > 1]
+    assert len(some) >= 4 and any(s[1] > 1 for s in some)
+    for R, N, W, K in ((64, 1, 128, 128), (8192, 8, 28672, 4096), (300, 8, 64, 64)):
+        assert plan.splits(R, N, W, K) == 1
 
 
 def test_every_fp32_tile_is_tested(plan):

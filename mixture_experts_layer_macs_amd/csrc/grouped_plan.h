@@ -26,7 +26,7 @@ inline double rounds(double tiles, int cus) { return std::ceil(tiles / cus); }
 inline double split_us(int R, int N, int W, int K, int splits, int cus) {
   const double tiles = N * std::ceil(W / 128.0) * std::ceil(K / 128.0);
   const double slices = static_cast<double>(R) / std::min(N, R) / 64 / splits;
-  const double join = splits > 1 ? 4 + splits * (static_cast<double>(N) * W * K * (8 / 4.0e6)) : 0;
+  const double join = splits > 1 ? 4 + splits * (static_cast<double>(N) * W * K / 1.0e6) : 0;
   return rounds(tiles * splits, cus) * (slices * 0.57 + 2) + 4 + join;
 }
 inline int split_choice(int R, int N, int W, int K, int cus) {

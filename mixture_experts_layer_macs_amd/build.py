@@ -62,6 +62,8 @@ def _check_scratch(src: str, remarks: str) -> None:
 
 
 def _scalars(operand: str) -> set:
+    if operand == "m0":
+        return {"m0"}
     m = re.fullmatch(r"s(?:(\d+)|\[(\d+):(\d+)\])", operand)
     if not m:
         return set()
@@ -70,9 +72,10 @@ def _scalars(operand: str) -> set:
 
 def _check_hazards(src: str, assembly: str) -> None:
     """The direct-to-LDS loads are inline assembly, for which the compiler does
-    not keep the five wait states between a vector instruction that writes a
-    scalar register and a load that reads it: a load closer than that may use a
-    stale address."""
+    not keep the wait states that it keeps before its own: five between a vector
+    instruction that writes a scalar register and a load that reads it, one
+    between a scalar instruction that writes M0 and the load, which takes its LDS
+    address from there.  A load closer than that may use a stale address."""
     kernel, loads, recent = "", 0, []
     for line in assembly.splitlines():
         if re.match(r"_Z\w+:", line):
@@ -84,19 +87,21 @@ def _check_hazards(src: str, assembly: str) -> None:
         args = [a.strip() for a in rest.split(",")]
         if op.startswith("buffer_load") and text.endswith(" lds"):
             loads += 1
-            used = set().union(*(_scalars(w) for a in args for w in a.split()))
+            used = set().union(*(_scalars(w) for a in args for w in a.split())) | {"m0"}
             away = 0
-            for wrote, states, what in reversed(recent):
-                if away < 5 and wrote & used:
+            for wrote, needs, states, what in reversed(recent):
+                if away < needs and wrote & used:
                     raise RuntimeError(f"{src}: {kernel}: {text!r} reads what {what!r} writes {away} wait "
                                        "states before it")
                 away += states
-        wrote = set()
+        wrote, needs = set(), 5
         if op.startswith(("v_readfirstlane", "v_readlane")):
             wrote = _scalars(args[0])
         elif op.startswith(("v_cmp", "v_div_scale", "v_mad_u64", "v_mad_i64")) or "_co_" in op:
             wrote = set().union(*(_scalars(a) for a in args[:2]))
-        recent = recent[-5:] + [(wrote, int(args[0], 0) + 1 if op == "s_nop" else 1, text)]
+        elif op.startswith("s_") and args[0] == "m0" and not op.startswith(("s_cmp", "s_bitcmp")):
+            wrote, needs = {"m0"}, 1
+        recent = recent[-5:] + [(wrote, needs, int(args[0], 0) + 1 if op == "s_nop" else 1, text)]
     if not loads:
         raise RuntimeError(f"{src}: no direct-to-LDS load in its assembly, so their hazards are not known")
 

@@ -5,10 +5,13 @@
 // in scalar registers, a per-lane 32-bit byte offset, and a scalar offset
 // (typically the K position), so one request costs a scalar add for M0 (the
 // LDS destination of the wave's 1 KB: 64 lanes x 16 bytes at consecutive
-// addresses) and the load itself.  Issued as inline assembly so the
-// compiler's automatic wait insertion does not treat later LDS reads as
+// addresses), one wait state and the load itself.  Issued as inline assembly so
+// the compiler's automatic wait insertion does not treat later LDS reads as
 // dependent on it: completion is tracked explicitly by the caller
-// (wait_vmcnt + barrier).
+// (wait_vmcnt + barrier).  The wait state, which a load needs behind a scalar
+// write of M0, is part of the assembly for the same reason: the compiler keeps it
+// only before loads that it knows, and without it the load may take the LDS
+// address of the one before.
 #pragma once
 
 #include "common.h"
@@ -37,7 +40,7 @@ __device__ __forceinline__ i32x4 buffer_rsrc(const void* base, uint32_t bytes) {
 
 __device__ __forceinline__ void lds_dma16(i32x4 rsrc, uint32_t voff, uint32_t soff,
                                           uint32_t m0) {
-  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc),
                "s"(soff), "{m0}"(m0)
                : "memory");
 }

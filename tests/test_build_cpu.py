@@ -47,3 +47,15 @@ def test_hazard_check(write):
 def test_hazard_check_needs_a_load_to_look_at():
     with pytest.raises(RuntimeError, match="no direct-to-LDS load"):
         build._check_hazards("linear.hip", "_Zx:\n\ts_endpgm\n")
+
+
+@pytest.mark.parametrize("write,states", [("\ts_add_i32 m0, s2, 0x400", 1), ("\ts_mov_b32 m0, s2", 1),
+                                          ("\tv_readfirstlane_b32 m0, v35", 5)])
+def test_hazard_check_of_the_lds_address(write, states):
+    """A load takes its LDS address from M0: one wait state behind a scalar
+    instruction that writes it, five behind a vector instruction."""
+    near = "".join(f"\ts_add_i32 s{40 + i}, m0, 1\n" for i in range(states - 1))
+    with pytest.raises(RuntimeError, match=f" {states - 1} wait states"):
+        build._check_hazards("linear.hip", ASM.format(write=write, between=near))
+    build._check_hazards("linear.hip", ASM.format(write=write, between=near + "\ts_nop 0\n"))
+    build._check_hazards("linear.hip", ASM.format(write=write, between=near + "\ts_cmp_eq_u32 m0, 0\n"))

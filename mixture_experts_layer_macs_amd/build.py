@@ -47,6 +47,9 @@ def _flags(src: str) -> list:
 # spilled to scratch memory would add instructions to the count.
 COUNTED = {"linear.hip": "mma_", "grouped.hip": "mma_"}
 
+# Sources whose kernels load straight to LDS through inline assembly (dma.h).
+DIRECT = ("ffn.hip", "router.hip", "similarity.hip", "linear.hip", "grouped.hip")
+
 
 def _check_scratch(src: str, remarks: str) -> None:
     found = [(name, size) for name, size in re.findall(
@@ -70,38 +73,66 @@ def _scalars(operand: str) -> set:
     return {int(m[1])} if m[1] else set(range(int(m[2]), int(m[3]) + 1))
 
 
+def _writes(op: str, args: list) -> tuple:
+    """The scalar registers whose writing by this instruction a load has to keep
+    a distance from, and that distance in wait states."""
+    if op.startswith(("v_readfirstlane", "v_readlane")):
+        return _scalars(args[0]), 5
+    if op.startswith(("v_cmp", "v_div_scale", "v_mad_u64", "v_mad_i64")) or "_co_" in op:
+        return set().union(*(_scalars(a) for a in args[:2])), 5
+    if op.startswith("s_") and args[0] == "m0" and not op.startswith(("s_cmp", "s_bitcmp")):
+        return {"m0"}, 1
+    return set(), 0
+
+
 def _check_hazards(src: str, assembly: str) -> None:
     """The direct-to-LDS loads are inline assembly, for which the compiler does
     not keep the wait states that it keeps before its own: five between a vector
     instruction that writes a scalar register and a load that reads it, one
     between a scalar instruction that writes M0 and the load, which takes its LDS
-    address from there.  A load closer than that may use a stale address."""
-    kernel, loads, recent = "", 0, []
+    address from there.  A load closer than that, on any way that leads to it, may
+    use a stale address."""
+    kernel, code, labels, jumps = "", [], {}, []  # code: kernel, operation, arguments, text
     for line in assembly.splitlines():
-        if re.match(r"_Z\w+:", line):
-            kernel, recent = line.split(":")[0], []
+        name = re.match(r"([\w.$]+):", line)
+        if name and name[1].startswith("_Z"):
+            kernel = name[1]
         text = line.split(";")[0].strip()
-        if not text or text.startswith(".") or text.endswith(":"):
+        if name:
+            labels.setdefault(name[1], []).append(len(code))
+        elif text and not text.startswith("."):
+            op, _, rest = text.partition(" ")
+            args = [a.strip() for a in rest.split(",")]
+            if op == "s_branch" or op.startswith("s_cbranch"):
+                jumps.append((len(code), args[0]))
+            code.append((kernel, op, args, text))
+    sources = {}  # jumps that lead to an instruction
+    for at, label in jumps:
+        for to in labels.get(label, []):
+            sources.setdefault(to, []).append(at)
+    ends = ("s_branch", "s_endpgm", "s_setpc", "s_trap")
+    loads = 0
+    for i, (kernel, op, args, text) in enumerate(code):
+        if not (op.startswith("buffer_load") and text.endswith(" lds")):
             continue
-        op, _, rest = text.partition(" ")
-        args = [a.strip() for a in rest.split(",")]
-        if op.startswith("buffer_load") and text.endswith(" lds"):
-            loads += 1
-            used = set().union(*(_scalars(w) for a in args for w in a.split())) | {"m0"}
-            away = 0
-            for wrote, needs, states, what in reversed(recent):
+        loads += 1
+        used = set().union(*(_scalars(w) for a in args for w in a.split())) | {"m0"}
+        ways, seen = [(i, 0)], set()  # an instruction, wait states between it and the load
+        while ways:
+            at, away = ways.pop()
+            before = list(sources.get(at, []))
+            if at > 0 and code[at - 1][0] == kernel and not code[at - 1][1].startswith(ends):
+                before.append(at - 1)
+            for j in before:
+                _, o, a, what = code[j]
+                wrote, needs = _writes(o, a)
                 if away < needs and wrote & used:
                     raise RuntimeError(f"{src}: {kernel}: {text!r} reads what {what!r} writes {away} wait "
                                        "states before it")
-                away += states
-        wrote, needs = set(), 5
-        if op.startswith(("v_readfirstlane", "v_readlane")):
-            wrote = _scalars(args[0])
-        elif op.startswith(("v_cmp", "v_div_scale", "v_mad_u64", "v_mad_i64")) or "_co_" in op:
-            wrote = set().union(*(_scalars(a) for a in args[:2]))
-        elif op.startswith("s_") and args[0] == "m0" and not op.startswith(("s_cmp", "s_bitcmp")):
-            wrote, needs = {"m0"}, 1
-        recent = recent[-5:] + [(wrote, needs, int(args[0], 0) + 1 if op == "s_nop" else 1, text)]
+                to = (j, away + (int(a[0], 0) + 1 if o == "s_nop" else 1))
+                if to[1] < 5 and to not in seen:
+                    seen.add(to)
+                    ways.append(to)
     if not loads:
         raise RuntimeError(f"{src}: no direct-to-LDS load in its assembly, so their hazards are not known")
 
@@ -112,19 +143,22 @@ def build(verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
-        report = ["-Rpass-analysis=kernel-resource-usage", "-save-temps=obj"] if src in COUNTED else []
+        report = ["-Rpass-analysis=kernel-resource-usage"] if src in COUNTED else []
+        if src in DIRECT:
+            report.append("-save-temps=obj")
         cmd = [cc, *_flags(src), *report, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")
-        if report:
+        if src in COUNTED:
+            _check_scratch(src, r.stderr)
+        if src in DIRECT:
             stem = src.replace(".hip", "-hip-")
             with open(os.path.join(BUILD, f"{stem}amdgcn-amd-amdhsa-{ARCH}.s")) as f:
                 assembly = f.read()
             for name in os.listdir(BUILD):  # the other intermediate files with it
                 if name.startswith((stem, src.replace(".hip", "-host-"), src + "-")):
                     os.remove(os.path.join(BUILD, name))
-            _check_scratch(src, r.stderr)
             _check_hazards(src, assembly)
         if verbose and r.stderr.strip():
             print(r.stderr, file=sys.stderr)

@@ -1,4 +1,7 @@
 """The build's check of kernels that count vector-memory instructions."""
+import os
+import re
+
 import pytest
 
 from mixture_experts_layer_macs_amd import build
@@ -59,3 +62,53 @@ def test_hazard_check_of_the_lds_address(write, states):
         build._check_hazards("linear.hip", ASM.format(write=write, between=near))
     build._check_hazards("linear.hip", ASM.format(write=write, between=near + "\ts_nop 0\n"))
     build._check_hazards("linear.hip", ASM.format(write=write, between=near + "\ts_cmp_eq_u32 m0, 0\n"))
+
+
+LOOP = """_ZN3moe3lin10mma_kernelEv:
+	s_mov_b32 m0, 0
+	s_branch .LBB0_2
+.LBB0_1:
+{first}	s_cbranch_scc1 .LBB0_3
+	s_nop 4
+.LBB0_2:
+	s_nop 4
+	{back}
+	s_nop 4
+{last}.LBB0_3:
+	buffer_load_dwordx4 v8, s[0:3], s22 offen lds
+	s_endpgm
+"""
+
+
+def test_hazard_check_follows_branches():
+    """What a jump leads past the instructions in between, and what stands before
+    a jump that is always taken."""
+    check = lambda **k: build._check_hazards("linear.hip", LOOP.format(**{  # noqa: E731
+        "first": "", "back": "s_cbranch_scc0 .LBB0_1", "last": "", **k}))
+    check()
+    near = "\tv_readfirstlane_b32 s22, v1\n"
+    with pytest.raises(RuntimeError, match="s22, v1' writes 1 wait states"):
+        check(first=near)                                          # behind a jump
+    with pytest.raises(RuntimeError, match="s22, v1' writes 0 wait states"):
+        check(last=near)                                           # in the text's order
+    check(first=near + "\ts_nop 3\n")
+    check(last=near + "\ts_branch .LBB0_2\n")                      # not on the way to the load
+    check(first="\ts_mov_b32 m0, s1\n")                            # the jump itself is the wait state
+
+
+def test_hazard_check_of_two_kernels():
+    """What ends a kernel is not on the way into the next one."""
+    end = "_Za:\n\tv_readfirstlane_b32 s22, v1\n"
+    load = "_Zb:\n\tbuffer_load_dwordx4 v8, s[0:3], s22 offen lds\n"
+    build._check_hazards("linear.hip", end + "\ts_endpgm\n" + load)
+    build._check_hazards("linear.hip", end + load)
+
+
+def test_every_source_with_inline_loads_is_checked():
+    """A source that includes dma.h, itself or through its headers, issues them."""
+    def includes(name):
+        with open(os.path.join(build.CSRC, name)) as f:
+            own = re.findall(r'#include "([^"/]+)"', f.read())
+        return set(own).union(*(includes(n) for n in own))
+    assert {s for s in build.SOURCES if "dma.h" in includes(s)} == set(build.DIRECT)
+    assert set(build.COUNTED) <= set(build.DIRECT)

@@ -26,3 +26,19 @@ LARGE = [
     ([3500, 0, 1] + [30 + 97 * i % 350 for i in range(61)], 7, 1544, 1032),
     ([260 + 3 * i % 50 for i in range(16)], 9, 712, 1032),
 ]
+
+# Every form of the kernels: each size with silu and swiglu, gathered and not.  A few
+# rows to an expert (the panels of 16 weight rows): one to three row tiles of 16, an
+# expert without rows, reductions that 64 does not divide, columns that end inside a
+# panel; experts of one to four units of 64 rows to a tile and of several tiles, also
+# where the streaming kernels hold many experts; one expert of 64 or 128 with
+# rows, and four.
+FORMS = [
+    ([1, 0, 5, 17, 3], 2, 1096, 72), ([2, 0, 17], 3, 1032, 264), ([40, 0, 1], 4, 1160, 40), ([1], 0, 1024, 8),
+    ([8] * 64, 0, 1032, 72), ([0, 1, 64, 65, 9, 3, 127, 130] * 7 + [513, 260, 0, 1, 5, 20, 40, 33], 7, 520, 264),
+    ([0, 1, 64, 65, 9, 3, 127, 130] * 7 + [513, 260, 0, 1, 5, 20, 40, 33], 7, 520, 520),
+    ([0, 1, 64, 65, 129, 3, 200, 257] * 9, 11, 72, 776), ([0] * 70 + [1500] + [0] * 57, 9, 520, 264), ([0] * 20 + [3300] + [0] * 43, 7, 520, 520),
+    ([0] * 30 + [300, 1, 0, 129, 600] + [0] * 93, 0, 264, 520), ([0, 1, 64, 65, 129, 200, 257, 300], 5, 520, 1032),
+    ([200, 0, 300, 257, 129, 333, 191, 190], 4, 1544, 200), ([90, 0, 31], 4, 72, 4112), ([2500, 0, 70], 3, 136, 264),
+]
+FORM_ACTS = ("silu", "swiglu")

@@ -687,9 +687,12 @@ int moe_combine_backward(const void* dy, const void* out_rows,
  * (MOE_BF16) or 4 (MOE_F32) and, with row_token, x of at most 2 GiB, else
  * MOE_EUNSUP (MOE_EINVAL for sizes out of range); every array but the two index
  * arrays starts at a multiple of 16 bytes, else MOE_EINVAL.  The outputs must not
- * overlap the inputs.  R == 0 enqueues nothing.
+ * overlap the inputs.  R == 0 enqueues nothing.  A bf16 product of more than
+ * MOE_GROUPED_MAX_TILES tiles of 128 rows and 128 columns (MOE_ACT_SWIGLU: 64) is
+ * MOE_EUNSUP too: y of 120 GB or more with MOE_ACT_SWIGLU, else y, dx or dw of 240.
  */
 #define MOE_GROUPED_MAX_ROWS (1 << 23)
+#define MOE_GROUPED_MAX_TILES (1 << 23)
 size_t moe_grouped_linear_workspace_size(int R, int N, int K, int O, int act,
                                          int dtype);
 int moe_grouped_linear(const void* x, const int32_t* row_token,

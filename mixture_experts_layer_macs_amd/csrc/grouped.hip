@@ -118,13 +118,13 @@ template <int MODE, int BM, int BN, int SL, int RA, int WGS, bool GLU, bool GATH
 int launch_mma(const Prod& p, hipStream_t s) {
   constexpr int lds = (RA * BM + SB * BN) * SL * 2, NC = GLU ? BN / 2 : BN;
   const auto fn = grouped_mma_kernel<MODE, BM, BN, SL, RA, WGS, GLU, GATHER>;
-  static std::atomic<bool> done[64];
-  if (!allow_lds(reinterpret_cast<const void*>(fn), lds, done)) return MOE_EHIP;
   const int N = MODE == FWD ? (GLU ? p.W / 2 : p.W) : p.K;
   const long rows = MODE == DW ? static_cast<long>(p.g.N) * ((p.W + BM - 1) / BM)
                                : max_row_tiles(p.g.R, p.g.N, BM);
   const long tiles = rows * ((N + NC - 1) / NC) * (MODE == DW && GLU ? p.splits : 1);
-  if (tiles > (1 << 23)) return MOE_EUNSUP;  // the outputs alone would not fit the card
+  if (tiles > MOE_GROUPED_MAX_TILES) return MOE_EUNSUP;  // a grid holds fewer than 2^32 threads
+  static std::atomic<bool> done[64];
+  if (!allow_lds(reinterpret_cast<const void*>(fn), lds, done)) return MOE_EHIP;
   hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>((tiles + 7) / 8 * 8)), dim3(lin::W * MOE_WAVE), lds,
                      s, p);
   return MOE_OK;

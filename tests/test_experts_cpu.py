@@ -68,6 +68,16 @@ def test_grouped_backward_refusals(lib, kw, rc):
     assert lib.moe_grouped_linear_backward(*a.values(), None) == rc
 
 
+@pytest.mark.parametrize("kw,rc", [
+    (dict(R=ROWS, O=8192), EUNSUP), (dict(R=1 << 20, N=1024, O=65536), EUNSUP),
+    (dict(R=ROWS, O=16384, act=2), EUNSUP), (dict(R=ROWS, O=8192, ws=None), EINVAL)])
+def test_grouped_refuses_more_tiles_than_a_grid_holds(lib, kw, rc):
+    """Outputs of 137 GB and more, of sizes that are each within their limits."""
+    a = dict(x=A, token=A, offsets=A, w=A, T=4, R=8, N=1, K=8, O=32, act=4, dtype=BF16, z=None, y=A, ws=A, size=1 << 40)
+    a.update(kw)
+    assert lib.moe_grouped_linear(*a.values(), None) == rc
+
+
 def test_grouped_workspaces(lib):
     f, b = lib.moe_grouped_linear_workspace_size, lib.moe_grouped_linear_backward_workspace_size
     assert f(64, 8, 64, 64, 0, BF16) > 0 and f(0, 8, 64, 64, 0, BF16) > 0

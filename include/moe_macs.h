@@ -742,7 +742,8 @@ int moe_grouped_linear_backward(const void* dy, const void* x,
  *              without; may equal x or residual (in place).
  * y            [T,H] out; may equal x or residual (in place), not sum.
  * mean, rstd   f32[T] out, for moe_norm_backward; each may be NULL.
- * Statistics are fp32, the variance from the centred values.
+ * Statistics are fp32, the variance from the centred values: a row whose sum of
+ * squares is beyond fp32's range gets rstd 0, and eps counts as rounded to fp32.
  * Limits: 1 <= H <= MOE_LINEAR_MAX_DIM, a multiple of 8 (MOE_BF16) or 4
  * (MOE_F32), else MOE_EUNSUP; arrays of H columns start at a multiple of 16
  * bytes, else MOE_EINVAL.  T == 0 enqueues nothing.  One launch.

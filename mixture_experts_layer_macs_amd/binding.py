@@ -819,8 +819,8 @@ def _kind(kind: str) -> int:
 def moe_norm(x, weight, bias=None, residual=None, kind="layer", eps=1e-5, total=None, y=None,
              mean=None, rstd=None):
     """(s - mean) rstd weight + bias of the sum s = x + residual (x without
-    residual); kind "rms" takes mean = 0.  total, needed with residual,
-    receives s; mean and rstd [T], if given, the statistics for
+    residual); kind "rms" takes mean = 0.  total, needed with residual and left as
+    it was without, receives s; mean and rstd [T], if given, the statistics for
     moe_norm_backward."""
     code, dt, d = _kind(kind), _elem(x.dtype), x.dtype
     T, H = x.shape

@@ -11,7 +11,7 @@
 // start and output (14 us beside 50 for 32 slices), which one workgroup a CU cannot
 // hide.  Measured: 8192 tokens spread over 128 experts of 1536 x 2048, swiglu with z
 // kept, 413 to 445 us (0.89 to 0.95 PFLOP/s); even groups of 512 rows 374; 8192 rows in
-// 8 experts of 28672 x 4096 1675 (1.15 PFLOP/s).
+// 8 experts of 28672 x 4096 1675 to 1740 (1.11 to 1.15 PFLOP/s).
 #pragma once
 
 #include <type_traits>

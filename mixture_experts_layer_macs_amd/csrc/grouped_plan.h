@@ -50,7 +50,9 @@ inline int split_choice(int R, int N, int W, int K, int cus) {
 // weight rows to a workgroup: 8 experts with a row each 11.8 us, 16.1 with tiles
 // (768 x 2048 swiglu); 16 such experts 20.3 and 18.8, 2048 x 768 10.0 and 8.9.
 // The streaming kernel deals whole experts to the XCDs, which takes several
-// for each: with 8 experts it took 1.7 times as long as the tiles.
+// for each: with 8 experts it took 1.7 times as long as the tiles, with 128 less than
+// they did (above).  Between those the border at 64 is not measured.  That a few of
+// many experts hold the rows does not show in the mean, and costs (grouped_stream.h).
 inline int tile_choice(int mode, int R, int N, int W, int K, int cus) {
   const int used = std::min(N, R);  // experts that can have rows
   const double rows = static_cast<double>(R) / used;

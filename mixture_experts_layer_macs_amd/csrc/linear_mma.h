@@ -41,7 +41,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // than five wait states behind the vector instruction that wrote it may see the
 // old value, and the compiler keeps that distance only for loads that it knows.
 // What an inline load's resource and offset are made of passes through here where
-// a kernel starts; the build looks for loads that come too close all the same.
+// a kernel starts; the build fails on loads that come too close all the same.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 template <typename T>
 __device__ __forceinline__ T* uniform(T* p) {
